@@ -535,6 +535,13 @@ __device__ __forceinline__ void gemm_f16_body(const uint16_t *__restrict__ X,
     for (int gi = 0; gi < kGPB; ++gi) szv[gi] = read_sz(sSZ0, gi);
 #pragma unroll
     for (int gi = 0; gi < kGPB; ++gi) szc[0][gi] = szv[gi];
+    if constexpr (NW == 8) {
+      // waves 0-3 hand over every wave's scales: the first step writes block
+      // kb0+2's where kb0's are, so every wave must have read those first
+      // (with four waves each writes only its own)
+      wait_lds_all();
+      __builtin_amdgcn_s_barrier();
+    }
 #pragma unroll
     for (int q = 0; q < kWords; ++q) {
       const int j = q / kSteps, st = q % kSteps, gi = st / kWpl, w = st % kWpl;
