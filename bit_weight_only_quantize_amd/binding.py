@@ -28,9 +28,13 @@ AWQ_ERR_NONFINITE = 5
 AWQ_F16, AWQ_BF16, AWQ_F32 = 0, 1, 2
 AWQ_KERNEL_AUTO, AWQ_KERNEL_GEMV, AWQ_KERNEL_GEMM, AWQ_KERNEL_BATCHED = 0, 1, 2, 3
 AWQ_EPILOGUE_NONE, AWQ_EPILOGUE_SILU_MUL = 0, 1
+AWQ_ACT_NONE, AWQ_ACT_RELU, AWQ_ACT_SILU, AWQ_ACT_GELU, AWQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": AWQ_ACT_NONE, "relu": AWQ_ACT_RELU, "silu": AWQ_ACT_SILU,
+               "gelu": AWQ_ACT_GELU, "gelu_tanh": AWQ_ACT_GELU_TANH}
 AWQ_MAX_PARTS = 4
 AWQ_GEMV_MAX_M = 16
 AWQ_BATCHED_MAX_M = 64
+AWQ_KV_MIN_PAGE, AWQ_KV_MAX_PAGE, AWQ_KV_MAX_HEADS = 16, 1024, 1024
 
 #: Every symbol include/awq355.h declares.
 EXPORTS = (
@@ -38,6 +42,7 @@ EXPORTS = (
     "awq_dequantize",
     "awq_linear",
     "awq_linear_ex",
+    "awq_linear_epilogue",
     "awq_linear_workspace_size",
     "awq_linear_ws",
     "awq_linear_noalloc",
@@ -47,6 +52,11 @@ EXPORTS = (
     "awq_scale_search",
     "awq_scale_search_workspace_size_ex",
     "awq_scale_search_ex",
+    "awq_kv_assign",
+    "awq_kv_append",
+    "awq_kv_gather",
+    "awq_kv_attention",
+    "awq_kv_attention_workspace_size",
     "awq_status_string",
     "awq_last_error",
     "awq_version",
@@ -65,6 +75,18 @@ class awq_linear_part(ctypes.Structure):
 
 class awq_search_options(ctypes.Structure):
     _fields_ = [("duo_scaling", ctypes.c_int32), ("apply_clip", ctypes.c_int32)]
+
+
+class awq_epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("activation", ctypes.c_int32)]
+
+
+class awq_kv_cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 class AwqError(RuntimeError):
@@ -124,6 +146,23 @@ def _load():
                                         ctypes.c_size_t, ctypes.POINTER(ctypes.c_int32),
                                         ctypes.POINTER(ctypes.c_double), vp, vp, vp, vp, vp, vp]
     lib.awq_scale_search_ex.restype = ctypes.c_int
+    lib.awq_linear_epilogue.argtypes = [vp, i32, vp, vp, vp, i64, i64, i64, awq_config,
+                                        ctypes.POINTER(awq_epilogue), vp, i32, i32, vp,
+                                        ctypes.c_size_t, vp]
+    lib.awq_linear_epilogue.restype = ctypes.c_int
+    pc = ctypes.POINTER(awq_kv_cache)
+    lib.awq_kv_assign.argtypes = [vp, vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, i64, vp, vp]
+    lib.awq_kv_assign.restype = ctypes.c_int
+    lib.awq_kv_append.argtypes = [vp, vp, i32, i64, i64, i64, pc, awq_config, vp, vp, vp]
+    lib.awq_kv_append.restype = ctypes.c_int
+    lib.awq_kv_gather.argtypes = [pc, awq_config, vp, i64, vp, vp, i32, vp]
+    lib.awq_kv_gather.restype = ctypes.c_int
+    lib.awq_kv_attention.argtypes = [vp, i32, i64, i64, i32, pc, awq_config, vp, i32, vp, vp, i32,
+                                     i32, i64, ctypes.c_float, i32, i32, vp, vp, vp,
+                                     ctypes.c_size_t, vp]
+    lib.awq_kv_attention.restype = ctypes.c_int
+    lib.awq_kv_attention_workspace_size.argtypes = [i64, i32, i32, pc, awq_config, i32, i64, i32]
+    lib.awq_kv_attention_workspace_size.restype = ctypes.c_size_t
     lib.awq_status_string.argtypes = [ctypes.c_int]
     lib.awq_status_string.restype = ctypes.c_char_p
     lib.awq_last_error.argtypes = []
@@ -195,6 +234,19 @@ def _ptr(t):
 def _stream(device):
     torch = _torch()
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _device(device):
+    """The C calls launch on the current device: make it the tensors'."""
+    return _torch().cuda.device(device)
+
+
+def _apart(a, a_name, b, b_name):
+    """Contiguous tensors a and b share no memory."""
+    a0, b0 = a.data_ptr(), b.data_ptr()
+    a1, b1 = a0 + a.numel() * a.element_size(), b0 + b.numel() * b.element_size()
+    if a0 < b1 and b0 < a1:
+        raise ValueError(f"{b_name} overlaps {a_name}")
 
 
 def _dtype_code(dt):
@@ -372,6 +424,50 @@ def awq_linear_ex(X, qweight, scales, zeros, kernel: int = AWQ_KERNEL_AUTO,
                            ctypes.c_void_p(0) if ws is None else _ptr(ws),
                            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev))
     check(st, "awq_linear_ex")
+    return out
+
+
+def awq_linear_epilogue(X, qweight, scales, zeros, bias=None, residual=None,
+                        activation: str = "none", kernel: int = AWQ_KERNEL_AUTO,
+                        group_size: int = 128, out_dtype=None, out=None, workspace="auto"):
+    """activation(X * deq(W)^T + bias) + residual in one call; activation one of
+    ACTIVATIONS.  bias [N] and residual [M][N] have the output's dtype (that of
+    X unless out or out_dtype says otherwise); residual may be `out` itself.
+    Kernel and workspace as in awq_linear_ex."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
+    if isinstance(workspace, str) and workspace != "auto":
+        raise ValueError("workspace must be a tensor, None or 'auto'")
+    if workspace is not None and not isinstance(workspace, str):
+        _tensor(workspace, "workspace")
+    _tensor(X, "X", (_torch().float16, _torch().bfloat16))
+    odt = out.dtype if out is not None else X.dtype if out_dtype is None else out_dtype
+    for t, name, dims in ((bias, "bias", 1), (residual, "residual", 2)):
+        if t is not None:
+            _tensor(t, name, odt)
+            if t.dim() != dims:
+                raise ValueError(f"{name} must be {dims}-D")
+    if bias is not None:
+        _tensor(bias, "bias", shape=(qweight.shape[0],))
+    if residual is not None:
+        _tensor(residual, "residual", shape=(X.shape[0], qweight.shape[0]))
+    M, N, K, out, dev = _linear_args(X, qweight, scales, zeros, group_size, out_dtype, out)
+    _placed((X, "X"), *[(t, name) for t, name in ((bias, "bias"), (residual, "residual"))
+                        if t is not None])
+    if residual is not None and residual.data_ptr() != out.data_ptr():
+        _apart(residual, "residual", out, "out")
+    need = awq_linear_workspace_size(M, N, K, group_size, X.dtype, kernel)
+    epi = awq_epilogue(None if bias is None else bias.data_ptr() or None,
+                       None if residual is None else residual.data_ptr() or None,
+                       ACTIVATIONS[activation])
+    with _device(dev):
+        ws = _workspace_arg(workspace, need, dev)
+        st = lib.awq_linear_epilogue(
+            _ptr(X), _dtype_code(X.dtype), _ptr(qweight), _ptr(scales), _zp_ptr(zeros), M, N, K,
+            config(group_size, zero_point=zeros is not None), ctypes.byref(epi), _ptr(out),
+            _dtype_code(out.dtype), int(kernel), ctypes.c_void_p(0) if ws is None else _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev))
+    check(st, "awq_linear_epilogue")
     return out
 
 
@@ -559,3 +655,267 @@ def awq_scale_search(X, W, group_size: int = 128, alphas=None, workspace=None, o
     if clip is not None:
         res["clip_index"] = clip
     return res
+
+
+# ---- the 4-bit paged key/value cache --------------------------------------------
+
+def empty_kv_cache(num_pages: int, num_kv_heads: int, head_dim: int, page_size: int = 64,
+                   device="cuda", zero_point: bool = True):
+    """Allocate a cache: (codes int32 [pages][2][heads][page_size * head_dim / 8],
+    scales fp16 and zeros uint8 [pages][heads][page_size][2]); zeros is None for
+    the symmetric grid (zero_point=False).  The contents are arbitrary."""
+    torch = _torch()
+    _check_cache_sizes(num_pages, num_kv_heads, head_dim, page_size)
+    meta = (num_pages, num_kv_heads, page_size, 2)
+    return (torch.empty((num_pages, 2, num_kv_heads, page_size * head_dim // 8), dtype=torch.int32,
+                        device=device),
+            torch.empty(meta, dtype=torch.float16, device=device),
+            torch.empty(meta, dtype=torch.uint8, device=device) if zero_point else None)
+
+
+def _check_cache_sizes(num_pages, num_kv_heads, head_dim, page_size):
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim={head_dim}: supported values are 64 and 128")
+    if page_size & (page_size - 1) or not AWQ_KV_MIN_PAGE <= page_size <= AWQ_KV_MAX_PAGE:
+        raise ValueError(f"page_size={page_size} is not a power of two in "
+                         f"[{AWQ_KV_MIN_PAGE}, {AWQ_KV_MAX_PAGE}]")
+    if num_pages < 1 or not 1 <= num_kv_heads <= AWQ_KV_MAX_HEADS:
+        raise ValueError(f"num_pages={num_pages} and num_kv_heads={num_kv_heads} must be positive "
+                         f"(at most {AWQ_KV_MAX_HEADS} heads)")
+
+
+def _cache_arg(cache):
+    """(awq_kv_cache, awq_config, named tensors) of a (codes, scales, zeros) cache."""
+    torch = _torch()
+    if not isinstance(cache, (tuple, list)) or len(cache) != 3:
+        raise TypeError("cache must be (codes, scales, zeros)")
+    codes, scales, zeros = cache
+    _tensor(codes, "codes", torch.int32)
+    _tensor(scales, "scales", torch.float16)
+    if codes.dim() != 4 or codes.shape[1] != 2:
+        raise ValueError("codes must be [pages][2][heads][page_size * head_dim / 8]")
+    if scales.dim() != 4:
+        raise ValueError("scales must be [pages][heads][page_size][2]")
+    pages, _, heads, words = codes.shape
+    page = scales.shape[2]
+    _tensor(scales, "scales", shape=(pages, heads, page, 2))
+    if page < 1 or words * 8 % page:
+        raise ValueError(f"codes hold {words} words per head and page, not a multiple of "
+                         f"page_size={page} / 8")
+    D = words * 8 // page
+    _check_cache_sizes(pages, heads, D, page)
+    named = [(codes, "codes"), (scales, "scales")]
+    if zeros is not None:
+        _tensor(zeros, "zeros", torch.uint8, (pages, heads, page, 2))
+        named.append((zeros, "zeros"))
+    c = awq_kv_cache(codes.data_ptr() or None, scales.data_ptr() or None,
+                     None if zeros is None else zeros.data_ptr() or None, pages, page, heads, D)
+    return c, config(D, zero_point=zeros is not None), named
+
+
+def _token_rows(t, name, heads, D, dtypes):
+    """[tokens][heads][D] with dense heads; returns the token stride."""
+    _tensor(t, name, dtypes)
+    if t.dim() != 3 or t.shape[1:] != (heads, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens][{heads}][{D}]")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
+    if t.shape[0] == 0:
+        return heads * D
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else heads * D
+    if stride < heads * D or stride % 8:
+        raise ValueError(f"{name}: token stride {stride} must be a multiple of 8 of at least "
+                         f"{heads * D}")
+    return stride
+
+
+def _same_device(dev, *named):
+    for t, name in named:
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev} like the other tensors")
+
+
+def awq_kv_assign(old_lens, new_lens, block_table, free_pages, page_size: int, num_slots: int,
+                  out=None):
+    """Pages and slots for the new_lens tokens that each request gets on top of
+    its old_lens (int32 [B]).  block_table (int32 [B][max_blocks]) is updated in
+    place with pages from the front of free_pages (int32).  Returns (seq_lens
+    int32 [B], query_start int32 [B + 1], slots int32 [num_slots], pages_used
+    int32 [1]), or fills `out`, a tuple of those."""
+    torch = _torch()
+    for t, name, dims in ((old_lens, "old_lens", 1), (new_lens, "new_lens", 1),
+                          (block_table, "block_table", 2), (free_pages, "free_pages", 1)):
+        _tensor(t, name, torch.int32)
+        if t.dim() != dims:
+            raise ValueError(f"{name} must be {dims}-D")
+    B = old_lens.shape[0]
+    _tensor(new_lens, "new_lens", shape=(B,))
+    _tensor(block_table, "block_table", shape=(B, block_table.shape[1]))
+    if num_slots < 0:
+        raise ValueError(f"num_slots={num_slots} is negative")
+    shapes = ((B,), (B + 1,), (num_slots,), (1,))
+    names = ("seq_lens", "query_start", "slots", "pages_used")
+    if out is not None:
+        if len(out) != 4:
+            raise ValueError("out must be (seq_lens, query_start, slots, pages_used)")
+        for t, name, shape in zip(out, names, shapes):
+            _tensor(t, name, torch.int32, shape)
+    dev = _placed((old_lens, "old_lens"), (new_lens, "new_lens"), (block_table, "block_table"),
+                  (free_pages, "free_pages"))
+    if out is None:
+        out = tuple(torch.empty(s, dtype=torch.int32, device=dev) for s in shapes)
+    _placed((old_lens, "old_lens"), *zip(out, names))
+    seq_lens, query_start, slots, used = out
+    with _device(dev):
+        st = lib.awq_kv_assign(_ptr(old_lens), _ptr(new_lens), B, page_size, _ptr(block_table),
+                               block_table.shape[1], _ptr(free_pages), free_pages.shape[0],
+                               _ptr(seq_lens), _ptr(query_start), _ptr(slots), num_slots,
+                               _ptr(used), _stream(dev))
+    check(st, "awq_kv_assign")
+    return tuple(out)
+
+
+def awq_kv_append(K, V, cache, slots, nonfinite_count=None):
+    """Quantize K and V (fp16 or bf16 [tokens][heads][D]; tokens may be strided,
+    as slices of a fused projection's output are) into the cache's slots (int32
+    [tokens]; tokens with a negative slot are skipped).  Returns the cache."""
+    torch = _torch()
+    c, cfg, named = _cache_arg(cache)
+    H, D = c.num_kv_heads, c.head_dim
+    dts = (torch.float16, torch.bfloat16)
+    ks, vs = _token_rows(K, "K", H, D, dts), _token_rows(V, "V", H, D, dts)
+    if V.dtype != K.dtype or V.shape[0] != K.shape[0]:
+        raise ValueError("K and V must have the same dtype and number of tokens")
+    T = K.shape[0]
+    _tensor(slots, "slots", torch.int32, (T,))
+    named.append((slots, "slots"))
+    cp = ctypes.c_void_p(0)
+    if nonfinite_count is not None:
+        _tensor(nonfinite_count, "nonfinite_count", torch.int32)
+        if nonfinite_count.numel() < 1:
+            raise ValueError("nonfinite_count must hold one element")
+        named.append((nonfinite_count, "nonfinite_count"))
+        cp = _ptr(nonfinite_count)
+    dev = _placed(*named)
+    _same_device(dev, (K, "K"), (V, "V"))
+    with _device(dev):
+        st = lib.awq_kv_append(_ptr(K), _ptr(V), _dtype_code(K.dtype), T, ks, vs, ctypes.byref(c),
+                               cfg, _ptr(slots), cp, _stream(dev))
+    check(st, "awq_kv_append")
+    return cache
+
+
+def awq_kv_gather(cache, slots, out_dtype=None, out=None):
+    """The values that slots (int32 [tokens]) of the cache stand for: (K, V), each
+    [tokens][heads][D] of out_dtype (float16 by default, bfloat16 or float32);
+    zeros for negative slots."""
+    torch = _torch()
+    c, cfg, named = _cache_arg(cache)
+    _tensor(slots, "slots", torch.int32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be 1-D")
+    named.append((slots, "slots"))
+    shape = (slots.shape[0], c.num_kv_heads, c.head_dim)
+    dts = (torch.float16, torch.bfloat16, torch.float32)
+    odt = torch.float16 if out_dtype is None else out_dtype
+    if out is not None:
+        if len(out) != 2:
+            raise ValueError("out must be (K, V)")
+        for t, name in zip(out, ("K", "V")):
+            _tensor(t, name, dts, shape)
+        odt = out[0].dtype
+        _tensor(out[1], "V", odt)
+    elif odt not in dts:
+        raise TypeError(f"out_dtype {odt} is not float16, bfloat16 or float32")
+    dev = _placed(*named)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=odt, device=dev) for _ in range(2))
+    _placed((slots, "slots"), (out[0], "K"), (out[1], "V"))
+    with _device(dev):
+        st = lib.awq_kv_gather(ctypes.byref(c), cfg, _ptr(slots), slots.shape[0], _ptr(out[0]),
+                               _ptr(out[1]), _dtype_code(odt), _stream(dev))
+    check(st, "awq_kv_gather")
+    return tuple(out)
+
+
+def awq_kv_attention_workspace_size(num_tokens: int, num_seqs: int, num_heads: int, cache,
+                                    max_query_len: int, max_seq_len: int, window: int = 0) -> int:
+    """Workspace bytes of awq_kv_attention for these sizes; cache as passed to it."""
+    c, cfg, _ = _cache_arg(cache)
+    return int(lib.awq_kv_attention_workspace_size(num_tokens, num_seqs, num_heads, ctypes.byref(c),
+                                                   cfg, max_query_len, max_seq_len, window))
+
+
+def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_query_len=None,
+                     max_seq_len=None, scale=None, causal: bool = True, window: int = 0, out=None,
+                     return_lse: bool = False, workspace="auto"):
+    """Attention of Q (fp16 or bf16 [tokens][num_heads][D], tokens may be strided)
+    over the cached keys and values of each request: block_table int32
+    [B][max_blocks] and seq_lens int32 [B] as awq_kv_assign gives them.
+
+    ``query_start`` (int32 [B + 1]) says which tokens are whose, the last ones of
+    each request; without it every request has one.  ``max_query_len`` is the
+    most tokens of a request (all tokens, if not given), ``max_seq_len`` the
+    expected longest request (the table's width; it decides only how the work is
+    split).  ``scale`` defaults to D ** -0.5.  ``window`` > 0 keeps the last
+    `window` keys.  Returns O [tokens][num_heads][D], and with return_lse also
+    the natural log of the softmax denominators, fp32 [tokens][num_heads]; rows
+    of tokens of no request are not written (pass `out` to say what they hold).
+    ``workspace``: as in awq_linear_ex."""
+    torch = _torch()
+    c, cfg, named = _cache_arg(cache)
+    D = c.head_dim
+    _tensor(Q, "Q", (torch.float16, torch.bfloat16))
+    if Q.dim() != 3 or Q.shape[2] != D:
+        raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [tokens][num_heads][{D}]")
+    T, heads = Q.shape[:2]
+    if heads < 1 or heads % c.num_kv_heads:
+        raise ValueError(f"{heads} query heads are not a multiple of {c.num_kv_heads} key/value heads")
+    _tensor(block_table, "block_table", torch.int32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [B][max_blocks]")
+    B, blocks = block_table.shape
+    _tensor(seq_lens, "seq_lens", torch.int32, (B,))
+    named += [(block_table, "block_table"), (seq_lens, "seq_lens")]
+    if query_start is not None:
+        _tensor(query_start, "query_start", torch.int32, (B + 1,))
+        named.append((query_start, "query_start"))
+    elif T != B:
+        raise ValueError(f"{T} query tokens for {B} requests need query_start")
+    if max_query_len is None:
+        max_query_len = T if query_start is not None else 1
+    if query_start is None and max_query_len != 1:
+        raise ValueError("without query_start, max_query_len is 1")
+    if max_seq_len is None:
+        max_seq_len = blocks * c.page_size
+    if out is not None:
+        _tensor(out, "out", Q.dtype, (T, heads, D))
+    if isinstance(workspace, str) and workspace != "auto":
+        raise ValueError("workspace must be a tensor, None or 'auto'")
+    if workspace is not None and not isinstance(workspace, str):
+        _tensor(workspace, "workspace")
+    stride = _token_rows(Q, "Q", heads, D, Q.dtype)
+    dev = _placed(*named)
+    _same_device(dev, (Q, "Q"))
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=Q.dtype, device=dev)
+    _placed((seq_lens, "seq_lens"), (out, "out"))
+    lse = None
+    if return_lse:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+    need = int(lib.awq_kv_attention_workspace_size(T, B, heads, ctypes.byref(c), cfg,
+                                                   max_query_len, max_seq_len, window))
+    with _device(dev):
+        ws = _workspace_arg(workspace, need, dev)
+        st = lib.awq_kv_attention(
+            _ptr(Q), _dtype_code(Q.dtype), T, stride, heads, ctypes.byref(c), cfg,
+            _ptr(block_table), blocks, _ptr(seq_lens),
+            ctypes.c_void_p(0) if query_start is None else _ptr(query_start), B, max_query_len,
+            max_seq_len, D ** -0.5 if scale is None else float(scale), int(bool(causal)), window,
+            _ptr(out), ctypes.c_void_p(0) if lse is None else _ptr(lse),
+            ctypes.c_void_p(0) if ws is None else _ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev))
+    check(st, "awq_kv_attention")
+    return (out, lse) if return_lse else out

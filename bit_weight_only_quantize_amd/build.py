@@ -30,8 +30,12 @@ SOURCES = [
     "linear_batched.hip",
     "linear_gemm.hip",
     "gemm_f16.hip",
+    "gemm_f16_epilogue.hip",
     "search.hip",
+    "kv_cache.hip",
+    "kv_attention.hip",
     "api.cpp",
+    "api_kv.cpp",
 ]
 
 ARCH = "gfx950"

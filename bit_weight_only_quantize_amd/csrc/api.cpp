@@ -11,12 +11,16 @@
 
 #include <mutex>
 
-#include "../../include/awq355.h"
+#include "api_common.h"
 #include "awq_internal.h"
 
-namespace {
+using namespace awq;
 
+namespace {
 thread_local char g_last_error[512] = "";
+}
+
+namespace awq {
 
 awq_status fail(awq_status st, const char *fmt, ...) {
   va_list ap;
@@ -36,7 +40,9 @@ awq_status hip_status(hipError_t e, const char *where) {
   return fail(AWQ_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace awq
+
+namespace {
 
 // Automatic kernel choice, from measured times (fp16, graph replays) on 7B-
 // and 13B-class layers: the GEMV wins wherever it stages the activation rows
@@ -90,8 +96,6 @@ awq_status check_config(awq_config cfg, int64_t K) {
   return AWQ_OK;
 }
 
-hipStream_t as_stream(awq_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
-
 awq_status check_linear(const void *X, int32_t x_dtype, const uint32_t *qweight,
                         const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
                         int64_t K, awq_config cfg, const void *Y, int32_t y_dtype,
@@ -128,10 +132,6 @@ awq_status check_linear(const void *X, int32_t x_dtype, const uint32_t *qweight,
   if (!aligned(scales, 2)) return fail(AWQ_ERR_INVALID_ARG, "scales must be 2-byte aligned");
   return AWQ_OK;
 }
-
-constexpr size_t kAlign = 256;
-
-size_t round_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 // Workspace layout of the scale search (each region 256-byte aligned; the
 // duo-scaling and clipping regions only when those options are on).
@@ -285,7 +285,8 @@ bool runs_gemv(int64_t M, int64_t N, int64_t K, int gs, int32_t kernel, bool has
 awq_status linear_impl(const char *who, const void *X, int32_t x_dtype, const uint32_t *qweight,
                        const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
                        int64_t K, awq_config cfg, void *Y, int32_t y_dtype, int32_t kernel,
-                       void *workspace, size_t workspace_bytes, awq_stream_t stream) {
+                       void *workspace, size_t workspace_bytes, awq_stream_t stream,
+                       const awq::Epilogue &epi = awq::Epilogue{}) {
   awq_status st =
       check_linear(X, x_dtype, qweight, scales, zeros, M, N, K, cfg, Y, y_dtype, kernel);
   if (st != AWQ_OK) return st;
@@ -302,7 +303,7 @@ awq_status linear_impl(const char *who, const void *X, int32_t x_dtype, const ui
   const hipStream_t hs = as_stream(stream);
   if (runs_gemv(M, N, K, cfg.group_size, kernel, workspace != nullptr))
     return hip_status(awq::launch_gemv(X, xt, qweight, scales, cfg.zero_point ? zeros : nullptr, M, N, K, cfg.group_size, Y,
-                                       yt, hs),
+                                       yt, hs, epi),
                       who);
   if (runs_batched(M, N, K, cfg.group_size, kernel, workspace != nullptr)) {
     const awq::BatchedPlan bp = awq::batched_gemv_plan(
@@ -317,7 +318,7 @@ awq_status linear_impl(const char *who, const void *X, int32_t x_dtype, const ui
                   workspace_bytes, bp.partial_bytes);
     return hip_status(awq::launch_batched_gemv(X, xt, qweight, scales,
                                                cfg.zero_point ? zeros : nullptr, M, N, K,
-                                               cfg.group_size, Y, yt, bp, workspace, hs),
+                                               cfg.group_size, Y, yt, bp, workspace, hs, epi),
                       who);
   }
   const awq::GemmPlan plan =
@@ -333,7 +334,7 @@ awq_status linear_impl(const char *who, const void *X, int32_t x_dtype, const ui
                   workspace_bytes, plan.workspace_bytes);
   }
   return hip_status(awq::launch_gemm(X, xt, qweight, scales, cfg.zero_point ? zeros : nullptr, M, N, K, cfg.group_size, Y,
-                                     yt, plan, workspace, hs),
+                                     yt, plan, workspace, hs, epi),
                     who);
 }
 
@@ -345,6 +346,23 @@ awq_status awq_linear_ex(const void *X, int32_t x_dtype, const uint32_t *qweight
                          void *workspace, size_t workspace_bytes, awq_stream_t stream) {
   return linear_impl("awq_linear_ex", X, x_dtype, qweight, scales, zeros, M, N, K, cfg, Y,
                      y_dtype, kernel, workspace, workspace_bytes, stream);
+}
+
+awq_status awq_linear_epilogue(const void *X, int32_t x_dtype, const uint32_t *qweight,
+                               const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
+                               int64_t K, awq_config cfg, const awq_epilogue *epilogue, void *Y,
+                               int32_t y_dtype, int32_t kernel, void *workspace,
+                               size_t workspace_bytes, awq_stream_t stream) {
+  const char *who = "awq_linear_epilogue";
+  if (!epilogue) return fail(AWQ_ERR_INVALID_ARG, "%s: epilogue is NULL", who);
+  if (epilogue->activation < AWQ_ACT_NONE || epilogue->activation > AWQ_ACT_GELU_TANH)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: activation=%d: unknown", who, epilogue->activation);
+  const size_t a = y_dtype == AWQ_F32 ? 4 : 2;
+  if (!aligned(epilogue->bias, a) || !aligned(epilogue->residual, a))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: bias and residual must be aligned to y_dtype's size", who);
+  const awq::Epilogue epi{epilogue->bias, epilogue->residual, (awq::Act)epilogue->activation};
+  return linear_impl(who, X, x_dtype, qweight, scales, zeros, M, N, K, cfg, Y, y_dtype, kernel,
+                     workspace, workspace_bytes, stream, epi);
 }
 
 size_t awq_linear_workspace_size(int64_t M, int64_t N, int64_t K, awq_config cfg,

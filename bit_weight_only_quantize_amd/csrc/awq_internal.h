@@ -13,6 +13,16 @@ namespace awq {
 enum class XType : int { F16 = 0, BF16 = 1 };
 enum class YType : int { F16 = 0, BF16 = 1, F32 = 2 };
 
+// What follows a linear layer's sum: act(sum + bias[n]) + residual[m][n].  Bias
+// and residual have the output's type; null where absent.  (Epilogue{}: none.)
+enum class Act : int { None = 0, Relu = 1, Silu = 2, Gelu = 3, GeluTanh = 4 };
+struct Epilogue {
+  const void *bias = nullptr;
+  const void *residual = nullptr;
+  Act act = Act::None;
+  bool any() const { return bias || residual || act != Act::None; }
+};
+
 // ---- quantize_pack.hip -----------------------------------------------------
 hipError_t launch_quantize_pack(const uint16_t *W, int64_t N, int64_t K, int gs,
                                 const float *s, uint32_t *qweight,
@@ -43,7 +53,7 @@ int64_t gemv_groups_per_wave(int64_t N, int64_t K, int gs);
 hipError_t launch_gemv(const void *X, XType xt, const uint32_t *qweight,
                        const uint16_t *scales, const uint8_t *zeros, int64_t M,
                        int64_t N, int64_t K, int gs, void *Y, YType yt,
-                       hipStream_t st);
+                       hipStream_t st, const Epilogue &epi = Epilogue{});
 // Up to 4 weight sets sharing X in one launch (each writes its own Y); with
 // silu_mul, exactly 2 of equal N and Y of part 0 receives silu(X W0^T) *
 // (X W1^T).  The zero-point mode of part 0 holds for all parts.
@@ -89,7 +99,8 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, XType xt, Scratch sc);
 hipError_t launch_gemm(const void *X, XType xt, const uint32_t *qweight,
                        const uint16_t *scales, const uint8_t *zeros, int64_t M,
                        int64_t N, int64_t K, int gs, void *Y, YType yt,
-                       const GemmPlan &plan, void *workspace, hipStream_t st);
+                       const GemmPlan &plan, void *workspace, hipStream_t st,
+                       const Epilogue &epi = Epilogue{});
 
 // ---- gemm_f16.hip (the quantized GEMM: fp16, or bf16 converted to fp16) ---------------
 // Row tile (16 * mt rows), K split and workspace of the GEMM.
@@ -97,7 +108,13 @@ GemmPlan gemm_f16_plan(int64_t M, int64_t N, int64_t K, bool bf16, Scratch sc);
 hipError_t launch_gemm_f16(const uint16_t *X, bool bf16, const uint32_t *qweight,
                            const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
                            int64_t K, int gs, void *Y, YType yt, const GemmPlan &plan,
-                           void *workspace, hipStream_t st);
+                           void *workspace, hipStream_t st, const Epilogue &epi = Epilogue{});
+// gemm_f16_epilogue.hip: launch_gemm_f16's GEMM (row tile mt, factors rowf) with epi.any().
+hipError_t launch_gemm_f16_epilogue(const uint16_t *X, const uint32_t *qweight,
+                                    const uint16_t *scales, const uint8_t *zeros, int64_t M,
+                                    int64_t N, int64_t K, int gs, void *Y, YType yt, int mt,
+                                    SplitK sk, const float *rowf, const Epilogue &epi,
+                                    hipStream_t st);
 
 // ---- linear_batched.hip (batched decode, M <= 64) ---------------------------------
 // Workgroups of 256 columns over a range of gps groups of K (a split); with
@@ -112,7 +129,7 @@ BatchedPlan batched_gemv_plan(int64_t M, int64_t N, int64_t K, int gs, Scratch s
 hipError_t launch_batched_gemv(const void *X, XType xt, const uint32_t *qweight,
                                const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
                                int64_t K, int gs, void *Y, YType yt, const BatchedPlan &plan,
-                               void *workspace, hipStream_t st);
+                               void *workspace, hipStream_t st, const Epilogue &epi = Epilogue{});
 
 // linear_gemm.hip: H = silu(A) * B elementwise over n fp32 values, rounded to yt.
 hipError_t launch_silu_mul(const float *A, const float *B, int64_t n, void *H, YType yt,
@@ -163,5 +180,54 @@ hipError_t launch_scale_activation(const uint16_t *X, const float *s, int64_t M,
 hipError_t launch_reduce_losses(const double *partials, int64_t n_per_alpha,
                                 int n_alpha, double *losses, int32_t *best,
                                 hipStream_t st);
+
+// ---- kv_cache.hip: the 4-bit paged key/value cache ------------------------------
+struct KvCache {
+  uint32_t *codes;     // [pages][2][heads][page_size * head_dim / 8]
+  uint16_t *scales;    // fp16 bits [pages][heads][page_size][2]
+  uint8_t *zeros;      // [pages][heads][page_size][2]; null: the symmetric grid
+  int64_t pages;
+  int page_size, heads, head_dim;
+};
+hipError_t launch_kv_assign(const int32_t *old_lens, const int32_t *new_lens, int B, int page_size,
+                            int32_t *table, int max_blocks, const int32_t *free_pages, int num_free,
+                            int32_t *seq_lens, int32_t *query_start, int32_t *slots,
+                            int64_t num_slots, int32_t *pages_used, hipStream_t st);
+hipError_t launch_kv_append(const uint16_t *K, const uint16_t *V, XType xt, int64_t T,
+                            int64_t k_stride, int64_t v_stride, const int32_t *slots,
+                            const KvCache &c, int32_t *nonfinite, hipStream_t st);
+hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int64_t T, void *K, void *V,
+                            YType ot, hipStream_t st);
+
+// ---- kv_attention.hip -------------------------------------------------------------
+// Arguments of one attention call (the last three are the launcher's).
+struct KvAttn {
+  const uint16_t *Q;
+  int64_t q_stride;           // elements between query tokens
+  void *O;                    // [T][heads * group][D], the type of Q
+  float *lse;                 // [T][heads * group] or null
+  const uint32_t *codes;
+  const uint16_t *scales;
+  const uint8_t *zeros;
+  int64_t pages, T;
+  int pshift, heads, group;   // log2 of the page size; key/value heads; query heads per each
+  const int32_t *table;
+  int max_blocks;
+  const int32_t *seq_lens, *query_start;
+  int max_q, causal, window;
+  float scale_log2;           // softmax scale * log2(e)
+  int splits;
+  float *part_o, *part_lse;   // [splits][T * heads * group][D] and [splits][T * heads * group]
+};
+// Kernel, number of parts of the keys, and workspace of a call.
+struct KvAttnPlan {
+  bool prompt;
+  int splits;
+  size_t lse_offset, workspace_bytes;   // 0 when splits == 1
+};
+KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
+                             int window);
+hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPlan &plan,
+                               void *workspace, hipStream_t st);
 
 }  // namespace awq

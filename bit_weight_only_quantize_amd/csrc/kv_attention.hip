@@ -1,0 +1,906 @@
+// Attention over the 4-bit paged key/value cache on gfx950.
+//
+// For a query row q (one head of one token) over the keys t that it sees:
+//   S_t = sum_d q_d (kc_td - kz_t)          exact integers kc - kz, fp32 sums
+//   u_t = S_t * ks_t * scale * log2(e)
+//   O   = sum_t 2^(u_t) vs_t (vc_t - vz_t) / sum_t 2^(u_t)
+// with codes c, zero points z and steps s of the key and value of token t.
+// Codes reach the matrix cores as exact small integers in fp16 and queries as
+// fp16 (bfloat16 ones after an exact power-of-two scaling), so the only
+// operand that is rounded is the weight P'_t = 2^(u_t - M) vs_t, once, to fp16
+// (2^-11 relative, a quarter of what the fp16 output's own rounding adds in
+// quadrature with it); sums, the running maximum and the normalizer are fp32.
+// M is the running maximum of u plus the exponent of the largest value step
+// seen, so that P' <= 2^kSlack whatever the steps: it neither overflows nor
+// sinks into fp16's subnormals because a layer's values are small.  M moves
+// only when a logit exceeds it by kSlack, which makes the rescaling of O (and
+// the exchange between lanes that it needs) rare: a wave tests one ballot.
+//
+// Rows of one key/value head are packed: row r of a request is query token
+// r / group, head r % group of the `group` query heads that share the
+// key/value head, so that shared heads cost one pass over the cache.
+//
+// Products are taken transposed, S^T = K Q^T and O^T = V^T P^T: the result of
+// the first then holds, in each lane, several keys of one query row, which is
+// the operand layout of the second, with no exchange between lanes.  The
+// contraction over keys may run in any order, so the key order inside an MFMA
+// is the one that falls out of the first product; the cache interleaves four
+// tokens of a value word to match.
+
+#include <type_traits>
+
+#include "awq_internal.h"
+#include "device_common.h"
+
+namespace awq {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kSlack = 8.0f;         // log2 of the largest P' between rescalings
+constexpr float kNone = -1e30f;        // "no key yet": finite, so kNone - kNone is 0
+
+__device__ __forceinline__ f32x16 mfma32x16(u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float lo_half(uint32_t w) { return half_bits_to_float((uint16_t)(w & 0xFFFFu)); }
+__device__ __forceinline__ float hi_half(uint32_t w) { return half_bits_to_float((uint16_t)(w >> 16)); }
+
+__device__ __forceinline__ uint32_t pack_half2(float a, float b) {
+  const f16x2 h = {(_Float16)a, (_Float16)b};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// Bytes b of x and y as the low bytes of the two halves of a word.
+template <int B>
+__device__ __forceinline__ uint32_t byte_pair(uint32_t x, uint32_t y) {
+  return __builtin_amdgcn_perm(y, x, 0x0C000C00u | ((4u + B) << 16) | (uint32_t)B);
+}
+// byte_pair with the byte pair's selector in a register.
+__device__ __forceinline__ uint32_t byte_pair(uint32_t x, uint32_t y, uint32_t sel) {
+  return __builtin_amdgcn_perm(y, x, sel);
+}
+
+__device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) + __builtin_bit_cast(f16x2, b));
+}
+
+// Power of two that brings a tile's largest finite magnitude (fp32 bits of a
+// non-negative value) into [2^14, 2^15): bfloat16 queries times it are fp16
+// numbers, exactly, unless they are below 2^-31 of the largest.  Kept within
+// 2^+-100 so that its inverse is normal.
+__device__ __forceinline__ float half_range_factor(uint32_t max_bits) {
+  const int e = (int)(max_bits >> 23);
+  if (e == 0) return 1.0f;
+  int k = 268 - e;                                   // biased exponent of 2^(14 - (e - 127))
+  k = k > 227 ? 227 : k < 27 ? 27 : k;
+  return __builtin_bit_cast(float, (uint32_t)k << 23);
+}
+__device__ __forceinline__ uint32_t finite_magnitude(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
+  return b < 0x7F800000u ? b : 0u;
+}
+
+// Eight bfloat16 values as fp16 after multiplication by f.
+__device__ __forceinline__ u32x4 bf16_to_half8(u32x4 raw, float f) {
+  u32x4 out;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = raw[i];
+    out[i] = pack_half2(__builtin_bit_cast(float, r << 16) * f,
+                        __builtin_bit_cast(float, r & 0xFFFF0000u) * f);
+  }
+  return out;
+}
+__device__ __forceinline__ uint32_t bf16_magnitude8(u32x4 raw) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = raw[i];
+    const uint32_t a = finite_magnitude(__builtin_bit_cast(float, r << 16));
+    const uint32_t b = finite_magnitude(__builtin_bit_cast(float, r & 0xFFFF0000u));
+    m = m > a ? m : a;
+    m = m > b ? m : b;
+  }
+  return m;
+}
+
+// What a workgroup knows about its request.
+struct Request {
+  int64_t token0;        // first query token
+  int qn, ql;            // query tokens in all, and those served (at most max_q)
+  int kv;                // tokens in the cache
+};
+__device__ __forceinline__ Request request_of(const KvAttn &p, int b) {
+  Request r;
+  if (p.query_start) {
+    int64_t a = p.query_start[b], z = p.query_start[b + 1];
+    a = a < 0 ? 0 : a > p.T ? p.T : a;
+    z = z < a ? a : z > p.T ? p.T : z;
+    r.token0 = a;
+    r.qn = (int)(z - a);
+  } else {
+    r.token0 = b;
+    r.qn = 1;
+  }
+  r.ql = r.qn < p.max_q ? r.qn : p.max_q;
+  const int64_t cap = (int64_t)p.max_blocks << p.pshift;
+  const int64_t n = p.seq_lens[b];
+  r.kv = (int)(n < 0 ? 0 : n > cap ? cap : n);
+  return r;
+}
+// Last key that query token qi sees, and the first (the window's start).
+__device__ __forceinline__ int last_key(const KvAttn &p, const Request &r, int qi) {
+  return p.causal ? r.kv - r.qn + qi : r.kv - 1;
+}
+__device__ __forceinline__ int first_key(const KvAttn &p, int last) {
+  if (!p.window) return 0;
+  const int f = last - p.window + 1;
+  return f > 0 ? f : 0;
+}
+
+// ---- few query rows: the decode kernel ------------------------------------------------------
+// Bound by reading the cache: D/2 bytes of key and of value codes and 4 to 6
+// bytes of steps and zero points per token and key/value head.  A workgroup
+// serves 16 query rows of one key/value head; each of its waves streams its
+// own run of tokens, 32 at a time, straight from memory into MFMA operands
+// (no LDS, no barrier until the end), the next 32 in flight meanwhile.  The
+// waves' results meet in LDS; with few requests the tokens are split over
+// several workgroups as well, whose results a second kernel joins.
+//
+// Lane (c = l & 15, kq = l >> 4).  Per 16 tokens: one 16-byte load of key
+// codes (D = 128: words 4kq.. of token c; 1 KiB per wave, one run), one of
+// value codes (word c of tokens 4kq..4kq+3), one of their steps, and 8 bytes
+// of zero points.  S^T comes out as keys 4kq + e of row c.
+template <int D>
+struct DecodeBuf {
+  static constexpr int kWords = D / 32;              // key words per lane and token
+  uint32_t k[2][kWords];
+  u32x4 v[2];
+  u32x4 sc[2];
+  u32x2 z[2];
+  uint32_t bad;                                      // bit i: tokens of half i have no page
+};
+
+template <int D, bool SYM, bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
+  constexpr int kWords = D / 32, kTiles = D / 16;
+  constexpr int kRow = D + 4;                        // floats per row in LDS
+  __shared__ __attribute__((aligned(16))) float red[NW][16][kRow];
+  __shared__ float red_m[NW][16], red_l[NW][16];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, kq = lane >> 4;
+  const int h = blockIdx.x % p.heads, row0 = (int)(blockIdx.x / p.heads) * 16;
+  const int split = blockIdx.y, b = blockIdx.z;
+  const Request rq = request_of(p, b);
+  const int rows = rq.ql * p.group;
+  if (row0 >= rows) return;
+  const int row_last = row0 + 15 < rows ? row0 + 15 : rows - 1;
+  const int row = row0 + c < rows ? row0 + c : rows - 1;
+  const int qi = row / p.group;
+  const int my_last = last_key(p, rq, qi), my_first = first_key(p, my_last);
+  // keys that any row sees, and keys that all rows see
+  const int any_last = last_key(p, rq, row_last / p.group);
+  const int all_last = last_key(p, rq, row0 / p.group);
+  const int any_first = first_key(p, all_last), all_first = first_key(p, any_last);
+  const int t_lo = any_first & ~31;
+  const int nt = any_last >= t_lo ? (any_last - t_lo) / 32 + 1 : 0;
+  const int64_t parts = (int64_t)p.splits * NW, part = (int64_t)split * NW + wave;
+  const int i0 = (int)((int64_t)nt * part / parts), i1 = (int)((int64_t)nt * (part + 1) / parts);
+
+  // queries: lane (c, kq) holds channels 32kq.. (D = 128) or 16kq.. (D = 64)
+  // of row c, the channels of the key words that it will load
+  const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
+                       (int64_t)(h * p.group + row % p.group) * D + kq * (8 * kWords);
+  u32x4 q[kWords];
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
+  float cs = p.scale_log2;
+  if constexpr (BF16) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const uint32_t a = bf16_magnitude8(q[j]);
+      m = m > a ? m : a;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
+      m = m > o ? m : o;
+    }
+    const float f = half_range_factor(m);
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) q[j] = bf16_to_half8(q[j], f);
+    cs *= 1.0f / f;
+  }
+  // sum of the row's queries, for the zero points: S = s (codes - 8) . q + (8 - z) sum q
+  float qsum = 0.0f;
+  if constexpr (!SYM) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = q[j][i];
+        qsum += lo_half(w) + hi_half(w);
+      }
+    qsum += __shfl_xor(qsum, 16, 64);
+    qsum += __shfl_xor(qsum, 32, 64);
+  }
+
+  const int pmask = (1 << p.pshift) - 1;
+  const int32_t *table = p.table + (int64_t)b * p.max_blocks;
+  int page_base = 0;
+  int32_t page_ids = -1;                             // lane i: page page_base + i of the request
+  auto load_pages = [&](int first) {
+    page_base = first;
+    const int at = first + lane;
+    page_ids = at < p.max_blocks ? table[at] : -1;
+  };
+  // lane offsets within a page's key words, value words, steps, zero points
+  const uint32_t k_lane = D == 128 ? c * 16 + kq * 4 : c * 8 + kq * 2;       // words
+  const uint32_t v_lane = kq * (D / 2) + (c & (D / 8 - 1)) * 4;              // words
+  auto load = [&](int t, DecodeBuf<D> &buf) {
+    buf.bad = 0;
+    // the pages of both halves lie within 64 of page_base, or are fetched
+    const int last = (t + 31) >> p.pshift;
+    if (last - page_base > 63) load_pages(t >> p.pshift);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int tt = t + 16 * i;
+      const int id = __builtin_amdgcn_readlane(page_ids, (tt >> p.pshift) - page_base);
+      const bool ok = id >= 0 && id < p.pages;
+      if (!ok) buf.bad |= 1u << i;
+      const int64_t page = ok ? id : 0;
+      const int64_t off = tt & pmask;
+      const int64_t P = (int64_t)pmask + 1;
+      const uint32_t *kb = p.codes + ((page * 2 * p.heads + h) * P + off) * (D / 8);
+      const uint32_t *vb = kb + (int64_t)p.heads * P * (D / 8);
+      const int64_t meta = ((page * p.heads + h) * P + off) * 2;
+      if constexpr (D == 128) {
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(kb + k_lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) buf.k[i][j] = w[j];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(kb + k_lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) buf.k[i][j] = w[j];
+      }
+      buf.v[i] = *reinterpret_cast<const u32x4 *>(vb + v_lane);
+      buf.sc[i] = *reinterpret_cast<const u32x4 *>(p.scales + meta + kq * 8);
+      if constexpr (!SYM) buf.z[i] = *reinterpret_cast<const u32x2 *>(p.zeros + meta + kq * 8);
+    }
+  };
+
+  f32x4 o[kTiles];
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float M = kNone, top = kNone, vlim = 0.0f, l = 0.0f, pz = 0.0f;
+  float vexp = 0.0f;                                 // M = top + vexp, 2^vexp = vlim
+  const DeqRegs dq;
+  const DeqF16 deq8(8u);
+  // D = 64 has 8 words per token but an MFMA operand 16 rows: lanes c and
+  // c + 8 take the same word, the first its even channels (bytes 0, 1), the
+  // second its odd ones (bytes 2, 3)
+  const uint32_t sel0 = D == 128 ? 0u : (c < 8 ? 0x0C040C00u : 0x0C060C02u);
+  const uint32_t sel1 = D == 128 ? 0u : (c < 8 ? 0x0C050C01u : 0x0C070C03u);
+
+  auto compute = [&](const DecodeBuf<D> &buf, int t) {
+    float u[8], vs[8], kz[8], vz[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) s = mfma32<TagF16>(deq8(buf.k[i][j], dq), q[j], s);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t w = buf.sc[i][e];
+        float x = s[e];
+        if constexpr (!SYM) {
+          const uint32_t zz = buf.z[i][e >> 1] >> (16 * (e & 1));
+          kz[4 * i + e] = 8.0f - (float)(zz & 0xFFu);
+          vz[4 * i + e] = (float)((zz >> 8) & 0xFFu) - 8.0f;
+          x = __builtin_fmaf(kz[4 * i + e], qsum, x);
+        }
+        vs[4 * i + e] = hi_half(w);
+        u[4 * i + e] = x * (lo_half(w) * cs);
+      }
+    }
+    if (buf.bad || t < all_first || t + 31 > all_last) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = t + 16 * i + 4 * kq + e;
+          const bool seen = at >= my_first && at <= my_last && !((buf.bad >> i) & 1u);
+          u[4 * i + e] = seen ? u[4 * i + e] : -__builtin_inff();
+          vs[4 * i + e] = seen ? vs[4 * i + e] : 0.0f;
+        }
+      }
+    }
+    float umax = u[0], vmax = vs[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      umax = fmaxf(umax, u[i]);
+      vmax = fmaxf(vmax, vs[i]);
+    }
+    if (__any(umax > top + kSlack || vmax > vlim)) {
+      umax = fmaxf(umax, __shfl_xor(umax, 16, 64));
+      umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
+      vmax = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vmax = fmaxf(vmax, vs[i] <= 65504.0f ? vs[i] : 0.0f);
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
+      top = fmaxf(top, umax);
+      if (vmax > vlim) {                             // uniform; (a step that overflowed counts for none)
+        const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
+        vexp = (float)ex;
+        vlim = __builtin_ldexpf(1.0f, ex);
+      }
+      const float m2 = top + vexp, a = __builtin_amdgcn_exp2f(M - m2);
+      M = m2;
+      l *= a;
+      pz *= a;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] *= a;
+    }
+    float pr[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = __builtin_amdgcn_exp2f(u[i] - M);
+      l += x;
+      pr[i] = x * vs[i];
+      if constexpr (!SYM) pz = __builtin_fmaf(pr[i], vz[i], pz);
+    }
+    u32x4 pb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pb[i] = pack_half2(pr[2 * i], pr[2 * i + 1]);
+    // value operands: byte b of the words of tokens (2j, 2j+1) in the halves
+    // of a word, then each nibble as an exact code - 8
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[4 * i + e] = buf.v[i][e];
+    auto tile = [&](auto byte_of, int n) {
+      u32x4 lo, hi;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t x = byte_of(w[2 * j], w[2 * j + 1]);
+        lo[j] = add_half2((x & dq.lo) | dq.e1024, deq8.nz1024);
+        hi[j] = add_half2((x & dq.hi) | dq.e64, deq8.nz64);
+      }
+      o[n] = mfma32<TagF16>(lo, pb, o[n]);
+      o[n + 1] = mfma32<TagF16>(hi, pb, o[n + 1]);
+    };
+    if constexpr (D == 128) {
+      tile([](uint32_t x, uint32_t y) { return byte_pair<0>(x, y); }, 0);
+      tile([](uint32_t x, uint32_t y) { return byte_pair<1>(x, y); }, 2);
+      tile([](uint32_t x, uint32_t y) { return byte_pair<2>(x, y); }, 4);
+      tile([](uint32_t x, uint32_t y) { return byte_pair<3>(x, y); }, 6);
+    } else {
+      tile([&](uint32_t x, uint32_t y) { return byte_pair(x, y, sel0); }, 0);
+      tile([&](uint32_t x, uint32_t y) { return byte_pair(x, y, sel1); }, 2);
+    }
+  };
+
+  if (i0 < i1) {
+    load_pages((t_lo + 32 * i0) >> p.pshift);
+    DecodeBuf<D> A, B;
+    load(t_lo + 32 * i0, A);
+    int i = i0;
+    for (; i + 1 < i1; i += 2) {
+      load(t_lo + 32 * (i + 1), B);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(A, t_lo + 32 * i);
+      if (i + 2 < i1) load(t_lo + 32 * (i + 2), A);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(B, t_lo + 32 * (i + 1));
+    }
+    if (i < i1) compute(A, t_lo + 32 * i);
+  }
+
+  // ---- join the waves --------------------------------------------------------------
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if constexpr (!SYM) {
+    pz += __shfl_xor(pz, 16, 64);
+    pz += __shfl_xor(pz, 32, 64);
+  }
+  // channel of MFMA tile n, result row 4kq + e (see the operand layouts above)
+  constexpr int kOrder[8] = {0, 2, 4, 6, 1, 3, 5, 7};
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = 4 * kq + e;
+      const int d = D == 128 ? 8 * r + kOrder[n] : 8 * (r & 7) + 2 * n + (r >> 3);
+      red[wave][c][d] = o[n][e] - pz;
+    }
+  if (kq == 0) {
+    red_m[wave][c] = M;
+    red_l[wave][c] = l;
+  }
+  __syncthreads();
+  constexpr int kPer = D / (4 * NW);                 // channels per thread
+  const int r = tid / (4 * NW), d0 = (tid % (4 * NW)) * kPer;
+  if (row0 + r >= rows) return;
+  float m = red_m[0][r];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) m = fmaxf(m, red_m[w][r]);
+  float sum = 0.0f, acc[kPer] = {};
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float a = __builtin_amdgcn_exp2f(red_m[w][r] - m);
+    sum = __builtin_fmaf(red_l[w][r], a, sum);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] = __builtin_fmaf(red[w][r][d0 + i], a, acc[i]);
+  }
+  const bool none = sum == 0.0f;                     // the row sees no key
+  const float inv = none ? 0.0f : 1.0f / sum;
+  const float lse2 = none ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
+  const int rr = row0 + r;
+  const int64_t head_row = (rq.token0 + rr / p.group) * ((int64_t)p.heads * p.group) +
+                           h * p.group + rr % p.group;
+  if (p.splits > 1) {
+    const int64_t at = split * p.T * p.heads * p.group + head_row;
+    float *po = p.part_o + at * D + d0;
+    if (!none) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) po[i] = acc[i] * inv;
+    }
+    if (d0 == 0) p.part_lse[at] = lse2;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float v = none ? 0.0f : acc[i] * inv;
+    if constexpr (BF16) reinterpret_cast<uint16_t *>(p.O)[head_row * D + d0 + i] = float_to_bf16_bits(v);
+    else reinterpret_cast<uint16_t *>(p.O)[head_row * D + d0 + i] = float_to_half_bits(v);
+  }
+  if (p.lse && d0 == 0) p.lse[head_row] = lse2 * 0.69314718055994531f;
+}
+
+// ---- many query rows: the prompt kernel --------------------------------------------------------
+// Bound by the softmax on the VALU next to the matrix products: about ten
+// VALU instructions per pair of row and key and wave lane, at a quarter of
+// the MFMA's width.  A workgroup serves 128 rows (four waves of 32) of one
+// key/value head and walks its keys 64 at a time.  Turning codes into fp16
+// integers costs as much VALU work per wave as the softmax of 32 rows, so it
+// is done once per workgroup: each thread turns 16 bytes of key and of value
+// codes into LDS, one tile ahead of the products, which read them as MFMA
+// operands.  32x32x16 MFMA, transposed as described above: lane (q = l & 31,
+// hh = l >> 5) holds keys 8g + 4hh + e of row q.
+//
+// LDS rows (a key's D channels, or a channel's 64 tokens) are split in
+// 16-byte chunks whose order is XORed with the row number, so that the 16
+// rows of an operand read fall on distinct banks.
+constexpr int kPtRows = 128, kPtKeys = 64, kPtThreads = 256;
+
+template <int D>
+struct PromptSmem {
+  uint16_t k[2][kPtKeys * D];
+  uint16_t v[2][D * kPtKeys];
+  float a[2][kPtKeys];           // key step * scale * log2(e)
+  float vs[2][kPtKeys];          // value step; -1: no such token
+  float vmax[2][4];              // per staging wave: the largest value step
+  uint32_t qmax[4];
+  uint32_t bad[2][4];            // per staging wave: some token of the tile has no page
+};
+
+// 16-byte chunk `chunk` of LDS row `row`, rows of kChunks chunks: byte offset
+template <int kChunks>
+__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
+  const int sw = kChunks == 16 ? (row & 15) : ((row & 7) ^ ((row >> 3) & 7));
+  return (uint32_t)(row * kChunks + (chunk ^ sw)) * 16u;
+}
+
+template <int D, bool SYM, bool BF16>
+__global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
+  constexpr int kSteps = D / 16, kTiles = D / 32;
+  constexpr int kQuads = D / 32;                     // 16-byte pieces of a key's codes
+  constexpr int kWordsT = D / 8;                     // words of a token
+  constexpr bool kBoth = D == 128;                   // every thread stages a key and a value piece
+  __shared__ __attribute__((aligned(16))) PromptSmem<D> sm;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int qc = lane & 31, hh = lane >> 5;
+  const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;     // longest rows first
+  const int h = blockIdx.y % p.heads, split = blockIdx.y / p.heads, b = blockIdx.z;
+  const Request rq = request_of(p, b);
+  const int rows = rq.ql * p.group, row0 = tile * kPtRows;
+  if (row0 >= rows) return;
+  auto clamp_row = [&](int r) { return r < rows ? r : rows - 1; };
+  const int wrow0 = clamp_row(row0 + wave * 32), wrow1 = clamp_row(row0 + wave * 32 + 31);
+  const int row = clamp_row(row0 + wave * 32 + qc);
+  const bool wave_live = row0 + wave * 32 < rows;
+  const int qi = row / p.group;
+  const int my_last = last_key(p, rq, qi), my_first = first_key(p, my_last);
+  const int w_any_last = last_key(p, rq, wrow1 / p.group);
+  const int w_all_last = last_key(p, rq, wrow0 / p.group);
+  const int w_any_first = first_key(p, w_all_last), w_all_first = first_key(p, w_any_last);
+  const int g_last = last_key(p, rq, clamp_row(row0 + kPtRows - 1) / p.group);
+  const int g_first = first_key(p, last_key(p, rq, row0 / p.group));
+  const int t_lo = g_first & ~(kPtKeys - 1);
+  const int nt = g_last >= t_lo ? (g_last - t_lo) / kPtKeys + 1 : 0;
+  const int i0 = (int)((int64_t)nt * split / p.splits), i1 = (int)((int64_t)nt * (split + 1) / p.splits);
+
+  // ---- staging: codes of one tile to registers, then as integers to LDS
+  const int kkey = tid / kQuads, kquad = tid % kQuads;       // D = 64: threads below 128
+  const int vtid = kBoth ? tid : tid - 128;
+  const int vblk = vtid / kWordsT, vword = vtid % kWordsT;   // four tokens, one word
+  const bool do_k = kBoth || wave < 2, do_v = kBoth || wave >= 2;
+  const int pmask = (1 << p.pshift) - 1;
+  const int64_t P = (int64_t)pmask + 1;
+  const int32_t *table = p.table + (int64_t)b * p.max_blocks;
+  auto page_of = [&](int t) { return t < rq.kv ? table[t >> p.pshift] : -1; };
+  int32_t kpage = -1, vpage = -1;                            // of the tile to load next
+  u32x4 kc = {}, vc = {};
+  uint32_t ksc = 0, kzz = 0x0808u;
+  u32x2 vzz = {0x08080808u, 0x08080808u};
+  bool kok = false;
+  auto load_pages = [&](int t0) {
+    if (do_k) kpage = page_of(t0 + kkey);
+    if (do_v) vpage = page_of(t0 + 4 * vblk);
+  };
+  auto load_codes = [&](int t0) {
+    if (do_k) {
+      kok = kpage >= 0 && kpage < p.pages;
+      const int64_t page = kok ? kpage : 0, off = (t0 + kkey) & pmask;
+      kc = *reinterpret_cast<const u32x4 *>(p.codes + ((page * 2 * p.heads + h) * P + off) * (D / 8) + kquad * 4);
+      const int64_t meta = ((page * p.heads + h) * P + off) * 2;
+      ksc = *reinterpret_cast<const uint32_t *>(p.scales + meta);
+      if constexpr (!SYM) kzz = *reinterpret_cast<const uint16_t *>(p.zeros + meta);
+    }
+    if (do_v) {
+      const int64_t page = vpage >= 0 && vpage < p.pages ? vpage : 0, off = (t0 + 4 * vblk) & pmask;
+      vc = *reinterpret_cast<const u32x4 *>(p.codes + ((page * 2 + 1) * p.heads + h) * P * (D / 8) +
+                                            (off >> 2) * (D / 2) + vword * 4);
+      if constexpr (!SYM)
+        vzz = *reinterpret_cast<const u32x2 *>(p.zeros + ((page * p.heads + h) * P + off) * 2);
+    }
+  };
+  const DeqRegs dq;
+  float cs = p.scale_log2;
+  auto stage = [&](int buf) {
+    if (do_k) {
+      const DeqF16 deq(kzz & 0xFFu);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t w = kc[j];
+        *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(sm.k[buf]) +
+                                   chunk_at<D / 8>(kkey, kquad * 4 + j)) = deq(w, dq);
+      }
+      float vstep = kok ? hi_half(ksc) : -1.0f;
+      if (kquad == 0) {
+        sm.a[buf][kkey] = kok ? lo_half(ksc) * cs : 0.0f;
+        // (an overflowed step as a finite one too large for fp16, so that the
+        // zero weight of a row that does not see the key stays zero)
+        sm.vs[buf][kkey] = vstep <= 65504.0f ? vstep : 0x1p127f;
+      }
+      const uint64_t miss = __ballot(!kok);
+      if (!(vstep <= 65504.0f)) vstep = 0.0f;                // (one that overflowed counts for none)
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) vstep = fmaxf(vstep, __shfl_xor(vstep, d, 64));
+      if (lane == 0) {
+        sm.vmax[buf][wave] = vstep;
+        sm.bad[buf][wave] = miss != 0;
+      }
+    }
+    if (do_v) {
+      // word vword of four tokens: channel d's four codes side by side
+      uint32_t z0 = vzz[0], z1 = vzz[1];
+      z0 = (z0 >> 8) & 0x00FF00FFu;                          // value zero points of tokens 0, 1
+      z1 = (z1 >> 8) & 0x00FF00FFu;
+      const uint32_t a0 = z0 | 0xE400E400u, a1 = z1 | 0xE400E400u;
+      const uint32_t b0 = (z0 << 4) | 0xD400D400u, b1 = (z1 << 4) | 0xD400D400u;
+      const uint32_t w0 = vc[0], w1 = vc[1], w2 = vc[2], w3 = vc[3];
+      // tokens 16s + 8x + 4y + e sit at position 16s + 8y + 4x + e of the row
+      const int chunk = (vblk >> 2) * 2 + (vblk & 1), half = (vblk >> 1) & 1;
+      auto put = [&](int ch, uint32_t x0, uint32_t x1) {
+        const int d = 8 * vword + ch;
+        *reinterpret_cast<u32x2 *>(reinterpret_cast<char *>(sm.v[buf]) +
+                                   chunk_at<kPtKeys / 8>(d, chunk) + 8 * half) = u32x2{x0, x1};
+      };
+      auto bytes = [&](auto tag, int lo_ch, int hi_ch) {
+        constexpr int kB = decltype(tag)::value;
+        const uint32_t x0 = byte_pair<kB>(w0, w1), x1 = byte_pair<kB>(w2, w3);
+        put(lo_ch, add_half2((x0 & dq.lo) | dq.e1024, a0), add_half2((x1 & dq.lo) | dq.e1024, a1));
+        put(hi_ch, add_half2((x0 & dq.hi) | dq.e64, b0), add_half2((x1 & dq.hi) | dq.e64, b1));
+      };
+      bytes(std::integral_constant<int, 0>{}, 0, 2);
+      bytes(std::integral_constant<int, 1>{}, 4, 6);
+      bytes(std::integral_constant<int, 2>{}, 1, 3);
+      bytes(std::integral_constant<int, 3>{}, 5, 7);
+    }
+  };
+
+  // ---- queries
+  const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
+                       (int64_t)(h * p.group + row % p.group) * D + 8 * hh;
+  u32x4 q[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
+  if constexpr (!kBoth) {
+    if (tid < 8) {                                           // waves that stage no keys
+      sm.vmax[tid >> 2][tid & 3] = -1.0f;
+      sm.bad[tid >> 2][tid & 3] = 0u;
+    }
+  }
+  if constexpr (BF16) {
+    // one factor for the workgroup's rows: it is part of the keys' steps in LDS
+    uint32_t m = 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const uint32_t x = bf16_magnitude8(q[s]);
+      m = m > x ? m : x;
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      const uint32_t x = (uint32_t)__shfl_xor((int)m, d, 64);
+      m = m > x ? m : x;
+    }
+    if (lane == 0) sm.qmax[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = m > sm.qmax[w] ? m : sm.qmax[w];
+    const float f = half_range_factor(m);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q[s] = bf16_to_half8(q[s], f);
+    cs *= 1.0f / f;
+  }
+  if constexpr (!kBoth) __syncthreads();
+
+  f32x16 o[kTiles];
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
+  float M = kNone, top = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f;
+
+  auto compute = [&](int buf, int t0) {
+    const char *kl = reinterpret_cast<const char *>(sm.k[buf]);
+    const char *vl = reinterpret_cast<const char *>(sm.v[buf]);
+    float u[32];
+    // the four keys 32i + 8g + 4hh + e of result group g
+    auto per_key = [&](const float *x, int i, int g) {
+      return *reinterpret_cast<const f32x4 *>(x + 32 * i + 8 * g + 4 * hh);
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f32x16 s;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st)
+        s = mfma32x16(*reinterpret_cast<const u32x4 *>(kl + chunk_at<D / 8>(32 * i + qc, 2 * st + hh)),
+                      q[st], s);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x4 a = per_key(sm.a[buf], i, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[16 * i + 4 * g + e] = s[4 * g + e] * a[e];
+      }
+    }
+    float vmax = sm.vmax[buf][0];
+    uint32_t bad = sm.bad[buf][0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      vmax = fmaxf(vmax, sm.vmax[buf][w]);
+      bad |= sm.bad[buf][w];
+    }
+    if (__any(bad != 0) || t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = t0 + 8 * j + 4 * hh + e;
+          const bool seen = at >= my_first && at <= my_last && v[e] >= 0.0f;
+          u[4 * j + e] = seen ? u[4 * j + e] : -__builtin_inff();
+        }
+      }
+    }
+    float umax = u[0];
+#pragma unroll
+    for (int j = 1; j < 32; ++j) umax = fmaxf(umax, u[j]);
+    if (__any(umax > top + kSlack || vmax > vlim)) {
+      umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
+      top = fmaxf(top, umax);
+      if (vmax > vlim) {
+        const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
+        vexp = (float)ex;
+        vlim = __builtin_ldexpf(1.0f, ex);
+      }
+      const float m2 = top + vexp, a = __builtin_amdgcn_exp2f(M - m2);
+      M = m2;
+      l *= a;
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[n][e] *= a;
+    }
+    u32x4 pb[4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = __builtin_amdgcn_exp2f(u[4 * j + e] - M);
+        l += x;
+        pr[e] = x * v[e];
+      }
+      pb[j >> 1][2 * (j & 1)] = pack_half2(pr[0], pr[1]);
+      pb[j >> 1][2 * (j & 1) + 1] = pack_half2(pr[2], pr[3]);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+        o[n] = mfma32x16(*reinterpret_cast<const u32x4 *>(vl + chunk_at<kPtKeys / 8>(32 * n + qc, 2 * s + hh)),
+                         pb[s], o[n]);
+  };
+
+  if (i0 < i1) {
+    load_pages(t_lo + kPtKeys * i0);
+    load_codes(t_lo + kPtKeys * i0);
+    load_pages(t_lo + kPtKeys * (i0 + 1));
+    stage(0);
+    __syncthreads();
+    for (int i = i0; i < i1; ++i) {
+      const int t0 = t_lo + kPtKeys * i, buf = (i - i0) & 1;
+      const bool more = i + 1 < i1;
+      if (more) {
+        load_codes(t0 + kPtKeys);
+        load_pages(t0 + 2 * kPtKeys);
+      }
+      if (wave_live && t0 <= w_any_last && t0 + kPtKeys > w_any_first) compute(buf, t0);
+      if (more) stage(buf ^ 1);
+      __syncthreads();
+    }
+  }
+
+  // ---- store: lane (q, hh) holds channels 32n + 8g + 4hh + e of row q
+  l += __shfl_xor(l, 32, 64);
+  if (row0 + wave * 32 + qc >= rows) return;
+  const bool none = l == 0.0f;
+  const float inv = none ? 0.0f : 1.0f / l;
+  const float lse2 = none ? -__builtin_inff() : M + __builtin_amdgcn_logf(l);
+  const int64_t head_row = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + row % p.group;
+  const int64_t at = p.splits > 1 ? split * p.T * p.heads * p.group + head_row : head_row;
+  if (p.splits > 1) {
+    if (hh == 0) p.part_lse[at] = lse2;
+    if (none) return;
+  } else if (p.lse && hh == 0) {
+    p.lse[at] = lse2 * 0.69314718055994531f;
+  }
+#pragma unroll
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : o[n][4 * g + e] * inv;
+      const int64_t d = at * D + 32 * n + 8 * g + 4 * hh;
+      if (p.splits > 1) {
+        *reinterpret_cast<float4 *>(p.part_o + d) = float4{v[0], v[1], v[2], v[3]};
+      } else {
+        u32x2 w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w[i] = BF16 ? (uint32_t)float_to_bf16_bits(v[2 * i]) | ((uint32_t)float_to_bf16_bits(v[2 * i + 1]) << 16)
+                      : pack_half2(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<u32x2 *>(reinterpret_cast<uint16_t *>(p.O) + d) = w;
+      }
+    }
+}
+
+// ---- join the splits ---------------------------------------------------------------------------
+// Row (token, head): weights 2^(lse_s - max lse) over the splits, one wave per
+// row, in split order.  A split in which the row saw no key has written -inf
+// and no O.  Rows that no request serves were not written and are not read.
+template <int D, bool BF16>
+__global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
+  constexpr int kPer = D / 64;
+  const int lane = threadIdx.x & 63;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const Request rq = request_of(p, b);
+  const int r = (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
+  if (r >= rq.ql * p.group) return;
+  const int64_t n = p.T * p.heads * p.group;
+  const int64_t at = (rq.token0 + r / p.group) * ((int64_t)p.heads * p.group) + h * p.group + r % p.group;
+  float m = -__builtin_inff();
+  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_lse[s * n + at]);
+  float sum = 0.0f, acc[kPer] = {};
+  for (int s = 0; s < p.splits; ++s) {
+    const float x = p.part_lse[s * n + at];
+    if (x == -__builtin_inff()) continue;
+    const float w = __builtin_amdgcn_exp2f(x - m);
+    sum += w;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      acc[i] = __builtin_fmaf(p.part_o[(s * n + at) * D + lane * kPer + i], w, acc[i]);
+  }
+  const bool none = sum == 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float v = none ? 0.0f : acc[i] / sum;
+    reinterpret_cast<uint16_t *>(p.O)[at * D + lane * kPer + i] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
+  }
+  if (p.lse && lane == 0)
+    p.lse[at] = none ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+}
+
+// ---- plan and launch ------------------------------------------------------------------------------
+constexpr int kDecodeWaves = 4;
+
+KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
+                             int window) {
+  KvAttnPlan pl{};
+  const int64_t rows = (int64_t)max_q * group;
+  // keys that a tile of rows can see at most
+  int64_t span = max_kv;
+  if (window > 0 && (int64_t)window + max_q < span) span = (int64_t)window + max_q;
+  if (span < 1) span = 1;
+  pl.prompt = rows > 32;
+  const int64_t tiles = pl.prompt ? (rows + kPtRows - 1) / kPtRows : (rows + 15) / 16;
+  const int64_t wgs = (int64_t)B * heads * tiles;
+  int64_t splits;
+  if (pl.prompt) {
+    splits = wgs > 0 ? 512 / wgs : 1;
+    const int64_t most = (span + 255) / 256;
+    splits = splits < most ? splits : most;
+  } else {
+    splits = wgs > 0 ? 1024 / wgs : 1;
+    const int64_t most = (span + 511) / 512;
+    splits = splits < most ? splits : most;
+  }
+  pl.splits = splits < 1 ? 1 : (int)splits;
+  if (pl.splits > 1) {
+    const int64_t n = T * heads * group;
+    pl.lse_offset = (size_t)pl.splits * n * D * 4;
+    pl.workspace_bytes = pl.lse_offset + (size_t)pl.splits * n * 4;
+  }
+  return pl;
+}
+
+namespace {
+template <int D, bool SYM, bool BF16>
+hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st) {
+  const int64_t rows = (int64_t)p.max_q * p.group;
+  if (pl.prompt) {
+    const dim3 grid((unsigned)((rows + kPtRows - 1) / kPtRows), (unsigned)(p.heads * p.splits), (unsigned)B);
+    kv_prompt_kernel<D, SYM, BF16><<<grid, kPtThreads, 0, st>>>(p);
+  } else {
+    const dim3 grid((unsigned)((rows + 15) / 16 * p.heads), (unsigned)p.splits, (unsigned)B);
+    kv_decode_kernel<D, SYM, BF16, kDecodeWaves><<<grid, 64 * kDecodeWaves, 0, st>>>(p);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  kv_join_kernel<D, BF16><<<dim3((unsigned)((rows + 3) / 4), (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
+  return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPlan &pl,
+                               void *workspace, hipStream_t st) {
+  p.splits = pl.splits;
+  if (pl.splits > 1) {
+    p.part_o = reinterpret_cast<float *>(workspace);
+    p.part_lse = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + pl.lse_offset);
+  }
+  const bool sym = p.zeros == nullptr, bf16 = xt == XType::BF16;
+  if (D == 128) {
+    if (sym) return bf16 ? attn_go<128, true, true>(p, B, pl, st) : attn_go<128, true, false>(p, B, pl, st);
+    return bf16 ? attn_go<128, false, true>(p, B, pl, st) : attn_go<128, false, false>(p, B, pl, st);
+  }
+  if (sym) return bf16 ? attn_go<64, true, true>(p, B, pl, st) : attn_go<64, true, false>(p, B, pl, st);
+  return bf16 ? attn_go<64, false, true>(p, B, pl, st) : attn_go<64, false, false>(p, B, pl, st);
+}
+
+}  // namespace awq

@@ -26,8 +26,11 @@
 // Splits of K write fp32 partials that a second kernel sums in split order
 // (deterministic); a single split stores Y directly.
 
+#include <type_traits>
+
 #include "awq_internal.h"
 #include "device_common.h"
+#include "epilogue.h"
 
 namespace awq {
 
@@ -66,12 +69,13 @@ struct BgGeom {
 };
 
 // (four waves per SIMD: two workgroups per CU)
-template <class XT, int GS, int MT, int REFILL>
+// EPI: `epi` follows the sum (of one split; otherwise the split sum applies it).
+template <class XT, int GS, int MT, int REFILL, bool EPI>
 __global__ __launch_bounds__(64 * kBgWaves) __attribute__((amdgpu_waves_per_eu(4, 8)))
 void batched_gemv_kernel(
     const uint16_t *__restrict__ X, const uint32_t *__restrict__ qweight,
     const uint16_t *__restrict__ scales, const uint8_t *__restrict__ zeros, int M, int N, int K,
-    int gps, void *__restrict__ Y, int ytype, uint32_t zfix, float *__restrict__ partial) {
+    int gps, void *Y, int ytype, uint32_t zfix, float *__restrict__ partial, Epilogue epi) {
   using Geo = BgGeom<GS, MT>;
   constexpr int kWpl = GS / 32;            // packed words per lane per group
   constexpr int kMG = Geo::kMaxGroups;
@@ -198,6 +202,15 @@ void batched_gemv_kernel(
   }
 
   if (n >= N) return;
+  if constexpr (EPI) {
+    const float bias = epi.bias ? load_as(epi.bias, n, ytype) : 0.0f;
+    with_activation(epi.act, [&](auto fn) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] = fn(acc[mt][e] + bias);
+    });
+  }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
@@ -205,7 +218,10 @@ void batched_gemv_kernel(
       const int m = 16 * mt + 4 * kq + e;
       if (m >= M) continue;
       const int64_t o = (int64_t)m * N + n;
-      const float v = acc[mt][e];
+      float v = acc[mt][e];
+      if constexpr (EPI) {
+        if (epi.residual) v += load_as(epi.residual, o, ytype);
+      }
       if (partial) {
         partial[(int64_t)split * M * N + o] = v;
       } else if (ytype == (int)YType::F16) {
@@ -224,10 +240,12 @@ void batched_gemv_kernel(
 // multiple of 4 here), or per output when it is not.  The loads of up to
 // eight splits are issued before their adds (a loop that added each split as
 // it arrived waited for them one by one: 4.4 us for 4 splits of 16 x 13824).
-template <int VEC>
+// EPI: `epi` follows the sum of a row of N columns.
+template <int VEC, bool EPI>
 __global__ __launch_bounds__(256) void batched_gemv_reduce_kernel(const float *__restrict__ partial,
-                                                                  int splits, int64_t MN,
-                                                                  void *__restrict__ Y, int ytype) {
+                                                                  int splits, int64_t MN, void *Y,
+                                                                  int ytype, uint32_t N,
+                                                                  Epilogue epi) {
   constexpr int kChunk = 8;
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   if (i >= MN) return;
@@ -251,6 +269,23 @@ __global__ __launch_bounds__(256) void batched_gemv_reduce_kernel(const float *_
 #pragma unroll
       for (int e = 0; e < VEC; ++e) v[e] = s0 + u == 0 ? p[u][e] : v[e] + p[u][e];
     }
+  }
+  if constexpr (EPI) {
+    // M * N < 2^32 here (M <= 64, N < 2^26), so the column is a 32-bit remainder
+    float r[VEC], bias[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      bias[e] = epi.bias ? load_as(epi.bias, ((uint32_t)i + e) % N, ytype) : 0.0f;
+      r[e] = epi.residual ? load_as(epi.residual, i + e, ytype) : 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] += bias[e];
+    with_activation(epi.act, [&](auto fn) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) v[e] = fn(v[e]);
+    });
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] += r[e];
   }
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
@@ -342,62 +377,74 @@ static int bg_refill(const BatchedPlan &p) {
   return 1;
 }
 
-template <class XT, int GS, int MT>
+template <class XT, int GS, int MT, bool EPI>
 static hipError_t bg_go(const void *X, const uint32_t *qw, const uint16_t *sc, const uint8_t *zr,
                         int64_t M, int64_t N, int64_t K, void *Y, YType yt,
-                        const BatchedPlan &p, float *partial, hipStream_t st) {
+                        const BatchedPlan &p, float *partial, const Epilogue &epi, hipStream_t st) {
   using Geo = BgGeom<GS, MT>;
   const dim3 grid((unsigned)((N + Geo::kCols - 1) / Geo::kCols), (unsigned)p.splits);
   const uint32_t zfix = zr ? 0u : 8u;
   float *part = p.splits > 1 ? partial : nullptr;
   const uint16_t *x = reinterpret_cast<const uint16_t *>(X);
   constexpr bool kPairs = (GS == 64 && MT <= 2) || (GS == 128 && MT == 1);
-  if constexpr (kPairs) {
-    if (bg_refill<GS, MT>(p) == 2)
-      batched_gemv_kernel<XT, GS, MT, 2><<<grid, Geo::kThreads, Geo::kBytes, st>>>(
-          x, qw, sc, zr, (int)M, (int)N, (int)K, p.gps, Y, (int)yt, zfix, part);
-    else
-      batched_gemv_kernel<XT, GS, MT, 1><<<grid, Geo::kThreads, Geo::kBytes, st>>>(
-          x, qw, sc, zr, (int)M, (int)N, (int)K, p.gps, Y, (int)yt, zfix, part);
-  } else {
-    batched_gemv_kernel<XT, GS, MT, 1><<<grid, Geo::kThreads, Geo::kBytes, st>>>(
-        x, qw, sc, zr, (int)M, (int)N, (int)K, p.gps, Y, (int)yt, zfix, part);
-  }
+  // with splits the kernel stores plain partial sums
+  auto go = [&](auto refill, auto with_epi) {
+    batched_gemv_kernel<XT, GS, MT, decltype(refill)::value, decltype(with_epi)::value>
+        <<<grid, Geo::kThreads, Geo::kBytes, st>>>(x, qw, sc, zr, (int)M, (int)N, (int)K, p.gps, Y,
+                                                   (int)yt, zfix, part, epi);
+  };
+  auto pick = [&](auto with_epi) {
+    if constexpr (kPairs) {
+      if (bg_refill<GS, MT>(p) == 2) return go(std::integral_constant<int, 2>{}, with_epi);
+    }
+    go(std::integral_constant<int, 1>{}, with_epi);
+  };
+  if (EPI && p.splits == 1) pick(std::bool_constant<EPI>{});
+  else pick(std::bool_constant<false>{});
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t MN = M * N;
   if (MN % 4 == 0)
-    batched_gemv_reduce_kernel<4><<<(unsigned)((MN / 4 + 255) / 256), 256, 0, st>>>(
-        partial, p.splits, MN, Y, (int)yt);
+    batched_gemv_reduce_kernel<4, EPI><<<(unsigned)((MN / 4 + 255) / 256), 256, 0, st>>>(
+        partial, p.splits, MN, Y, (int)yt, (uint32_t)N, epi);
   else
-    batched_gemv_reduce_kernel<1><<<(unsigned)((MN + 255) / 256), 256, 0, st>>>(
-        partial, p.splits, MN, Y, (int)yt);
+    batched_gemv_reduce_kernel<1, EPI><<<(unsigned)((MN + 255) / 256), 256, 0, st>>>(
+        partial, p.splits, MN, Y, (int)yt, (uint32_t)N, epi);
   return hipGetLastError();
 }
 
-template <class XT, int GS>
+template <class XT, int GS, bool EPI>
 static hipError_t bg_mt_go(const void *X, const uint32_t *qw, const uint16_t *sc, const uint8_t *zr,
                            int64_t M, int64_t N, int64_t K, void *Y, YType yt,
-                           const BatchedPlan &p, float *partial, hipStream_t st) {
+                           const BatchedPlan &p, float *partial, const Epilogue &epi, hipStream_t st) {
   switch (bg_mt(M)) {
-    case 1: return bg_go<XT, GS, 1>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, st);
-    case 2: return bg_go<XT, GS, 2>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, st);
-    default: return bg_go<XT, GS, 4>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, st);
+    case 1: return bg_go<XT, GS, 1, EPI>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, epi, st);
+    case 2: return bg_go<XT, GS, 2, EPI>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, epi, st);
+    default: return bg_go<XT, GS, 4, EPI>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, epi, st);
   }
+}
+
+template <class XT, int GS>
+static hipError_t bg_epi_go(const void *X, const uint32_t *qw, const uint16_t *sc, const uint8_t *zr,
+                            int64_t M, int64_t N, int64_t K, void *Y, YType yt,
+                            const BatchedPlan &p, float *partial, const Epilogue &epi,
+                            hipStream_t st) {
+  if (epi.any()) return bg_mt_go<XT, GS, true>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, epi, st);
+  return bg_mt_go<XT, GS, false>(X, qw, sc, zr, M, N, K, Y, yt, p, partial, epi, st);
 }
 
 hipError_t launch_batched_gemv(const void *X, XType xt, const uint32_t *qweight,
                                const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
                                int64_t K, int gs, void *Y, YType yt, const BatchedPlan &plan,
-                               void *workspace, hipStream_t st) {
+                               void *workspace, hipStream_t st, const Epilogue &epi) {
   if (M == 0 || N == 0) return hipSuccess;
   float *partial = reinterpret_cast<float *>(workspace);
   if (xt == XType::F16) {
-    if (gs == 128) return bg_mt_go<TagF16, 128>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, st);
-    return bg_mt_go<TagF16, 64>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, st);
+    if (gs == 128) return bg_epi_go<TagF16, 128>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, epi, st);
+    return bg_epi_go<TagF16, 64>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, epi, st);
   }
-  if (gs == 128) return bg_mt_go<TagBF16, 128>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, st);
-  return bg_mt_go<TagBF16, 64>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, st);
+  if (gs == 128) return bg_epi_go<TagBF16, 128>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, epi, st);
+  return bg_epi_go<TagBF16, 64>(X, qweight, scales, zeros, M, N, K, Y, yt, plan, partial, epi, st);
 }
 
 }  // namespace awq

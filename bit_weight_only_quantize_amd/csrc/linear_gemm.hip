@@ -213,9 +213,9 @@ GemmPlan gemm_plan(int64_t M, int64_t N, int64_t K, XType xt, Scratch sc) {
 hipError_t launch_gemm(const void *X, XType xt, const uint32_t *qweight,
                        const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
                        int64_t K, int gs, void *Y, YType yt, const GemmPlan &plan,
-                       void *workspace, hipStream_t st) {
+                       void *workspace, hipStream_t st, const Epilogue &epi) {
   return launch_gemm_f16(reinterpret_cast<const uint16_t *>(X), xt == XType::BF16, qweight,
-                         scales, zeros, M, N, K, gs, Y, yt, plan, workspace, st);
+                         scales, zeros, M, N, K, gs, Y, yt, plan, workspace, st, epi);
 }
 
 // ---- SiLU(gate) * up: the epilogue of the fused gate/up projections on the GEMM

@@ -22,6 +22,7 @@
 
 #include "awq_internal.h"
 #include "device_common.h"
+#include "epilogue.h"
 
 namespace awq {
 
@@ -113,10 +114,11 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g));
 // round; the staging loops then unroll to that, not to the LDS budget's
 // maximum (8 rounds), and the kernel's code shrinks by up to a third
 // (measured 0.1-0.3 us per launch on the decode layers).
-template <class XT, int GS, int NW, int U, bool STAGE_X, int NP, bool MULTI, bool SMALL>
+// EPI: `epi` follows the sum (one part only).
+template <class XT, int GS, int NW, int U, bool STAGE_X, int NP, bool MULTI, bool SMALL, bool EPI>
 __global__ __launch_bounds__(64 * NW) void gemv_kernel(const uint16_t *__restrict__ X,
                                                        GemvParts parts, int M, int K, int ytype,
-                                                       uint32_t zfix) {
+                                                       uint32_t zfix, Epilogue epi) {
   constexpr int kWpl = GS / 32;            // packed words per lane per group
   constexpr bool kBF16 = __is_same(XT, TagBF16);
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -136,6 +138,7 @@ __global__ __launch_bounds__(64 * NW) void gemv_kernel(const uint16_t *__restric
   // the reduction, its argument load was measured to cost 2-5% per launch
   void *const Y = parts.y[part];
   asm volatile("" : : "s"(Y));
+  if constexpr (EPI) asm volatile("" : : "s"(epi.bias), "s"(epi.residual), "s"((int)epi.act));
   const int n0 = tile * 16;
   const int n = n0 + c;
   const int G = K / GS;
@@ -458,7 +461,12 @@ __global__ __launch_bounds__(64 * NW) void gemv_kernel(const uint16_t *__restric
     for (int w = 1; w < NW; ++w) sum[s] += part[w >> 2][w & 3];
   }
   const int64_t o = (int64_t)om * N + on;
-  const float v = NP == 2 ? silu(sum[0]) * sum[1] : sum[0];
+  float v = NP == 2 ? silu(sum[0]) * sum[1] : sum[0];
+  if constexpr (EPI) {
+    if (epi.bias) v += load_as(epi.bias, on, ytype);
+    v = activate(v, epi.act);
+    if (epi.residual) v += load_as(epi.residual, o, ytype);
+  }
   if (ytype == (int)YType::F16)
     reinterpret_cast<uint16_t *>(Y)[o] = float_to_half_bits(v);
   else if (ytype == (int)YType::BF16)
@@ -468,9 +476,9 @@ __global__ __launch_bounds__(64 * NW) void gemv_kernel(const uint16_t *__restric
 }
 
 
-template <class XT, int GS, int NW, int NP, bool MULTI>
+template <class XT, int GS, int NW, int NP, bool MULTI, bool EPI>
 static void gemv_launch(const uint16_t *X, const GemvParts &parts, int tiles, int M, int64_t K,
-                        YType yt, uint32_t zfix, hipStream_t st) {
+                        YType yt, uint32_t zfix, const Epilogue &epi, hipStream_t st) {
   const dim3 grid((unsigned)tiles);
   const int G = (int)(K / GS);
   const bool stage = (uint64_t)M * (uint64_t)K * 2u <= gemv_stage_budget(NW);
@@ -491,13 +499,13 @@ static void gemv_launch(const uint16_t *X, const GemvParts &parts, int tiles, in
                                       : (16 * G + 64 * NW - 1) / (64 * NW);
   const bool small = xr <= 2 && szr <= 1;
   if (stage && G > 8 * NW)
-    gemv_kernel<XT, GS, NW, 2, true, NP, MULTI, false><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix);
+    gemv_kernel<XT, GS, NW, 2, true, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
   else if (stage && small)
-    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, true><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix);
+    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, true, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
   else if (stage)
-    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, false><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix);
+    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
   else
-    gemv_kernel<XT, GS, NW, 2, false, NP, MULTI, false><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix);
+    gemv_kernel<XT, GS, NW, 2, false, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
 }
 
 // Waves per workgroup.  Every workgroup of a launch should be resident at
@@ -508,19 +516,24 @@ static void gemv_launch(const uint16_t *X, const GemvParts &parts, int tiles, in
 // (every wave's staging loads then queue behind more weight traffic).
 template <class XT, int GS, int NP>
 static void gemv_dispatch(const uint16_t *X, const GemvParts &parts, int tiles, int M, int64_t K,
-                          YType yt, uint32_t zfix, hipStream_t st) {
+                          YType yt, uint32_t zfix, const Epilogue &epi, hipStream_t st) {
   // the gate/up pair always takes 8 waves: with 16, its two sets of staging
   // registers spill under the 1024-thread register budget
-  if (NP == 2)
-    gemv_launch<XT, GS, 8, NP, false>(X, parts, tiles, M, K, yt, zfix, st);
-  else if (parts.count > 1 && gemv_waves_for_tiles(tiles) == 16)
-    gemv_launch<XT, GS, 16, NP, true>(X, parts, tiles, M, K, yt, zfix, st);
-  else if (parts.count > 1)
-    gemv_launch<XT, GS, 8, NP, true>(X, parts, tiles, M, K, yt, zfix, st);
-  else if (gemv_waves_for_tiles(tiles) == 16)
-    gemv_launch<XT, GS, 16, NP, false>(X, parts, tiles, M, K, yt, zfix, st);
-  else
-    gemv_launch<XT, GS, 8, NP, false>(X, parts, tiles, M, K, yt, zfix, st);
+  if constexpr (NP == 2) {
+    gemv_launch<XT, GS, 8, NP, false, false>(X, parts, tiles, M, K, yt, zfix, epi, st);
+  } else {
+    const bool wide = gemv_waves_for_tiles(tiles) == 16;
+    if (epi.any()) {
+      if (wide) gemv_launch<XT, GS, 16, NP, false, true>(X, parts, tiles, M, K, yt, zfix, epi, st);
+      else gemv_launch<XT, GS, 8, NP, false, true>(X, parts, tiles, M, K, yt, zfix, epi, st);
+    } else if (parts.count > 1) {
+      if (wide) gemv_launch<XT, GS, 16, NP, true, false>(X, parts, tiles, M, K, yt, zfix, epi, st);
+      else gemv_launch<XT, GS, 8, NP, true, false>(X, parts, tiles, M, K, yt, zfix, epi, st);
+    } else {
+      if (wide) gemv_launch<XT, GS, 16, NP, false, false>(X, parts, tiles, M, K, yt, zfix, epi, st);
+      else gemv_launch<XT, GS, 8, NP, false, false>(X, parts, tiles, M, K, yt, zfix, epi, st);
+    }
+  }
 }
 
 int64_t gemv_groups_per_wave(int64_t N, int64_t K, int gs) {
@@ -542,29 +555,23 @@ bool gemv_supported(int64_t M, int64_t N, int64_t K, int gs, int np) {
 namespace {
 template <int NP>
 hipError_t gemv_go(const void *X, XType xt, const GemvParts &parts, int tiles, int64_t M,
-                   int64_t K, int gs, YType yt, uint32_t zfix, hipStream_t st) {
+                   int64_t K, int gs, YType yt, uint32_t zfix, const Epilogue &epi,
+                   hipStream_t st) {
   const uint16_t *x = reinterpret_cast<const uint16_t *>(X);
   if (xt == XType::F16) {
-    if (gs == 128) gemv_dispatch<TagF16, 128, NP>(x, parts, tiles, (int)M, K, yt, zfix, st);
-    else gemv_dispatch<TagF16, 64, NP>(x, parts, tiles, (int)M, K, yt, zfix, st);
+    if (gs == 128) gemv_dispatch<TagF16, 128, NP>(x, parts, tiles, (int)M, K, yt, zfix, epi, st);
+    else gemv_dispatch<TagF16, 64, NP>(x, parts, tiles, (int)M, K, yt, zfix, epi, st);
   } else {
-    if (gs == 128) gemv_dispatch<TagBF16, 128, NP>(x, parts, tiles, (int)M, K, yt, zfix, st);
-    else gemv_dispatch<TagBF16, 64, NP>(x, parts, tiles, (int)M, K, yt, zfix, st);
+    if (gs == 128) gemv_dispatch<TagBF16, 128, NP>(x, parts, tiles, (int)M, K, yt, zfix, epi, st);
+    else gemv_dispatch<TagBF16, 64, NP>(x, parts, tiles, (int)M, K, yt, zfix, epi, st);
   }
   return hipGetLastError();
 }
 }  // namespace
 
-hipError_t launch_gemv(const void *X, XType xt, const uint32_t *qweight,
-                       const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
-                       int64_t K, int gs, void *Y, YType yt, hipStream_t st) {
-  const LinearPart one{qweight, scales, zeros, N, Y};
-  return launch_gemv_parts(X, xt, &one, 1, false, M, K, gs, yt, st);
-}
-
-hipError_t launch_gemv_parts(const void *X, XType xt, const LinearPart *p, int count,
-                             bool silu_mul, int64_t M, int64_t K, int gs, YType yt,
-                             hipStream_t st) {
+namespace {
+hipError_t gemv_parts(const void *X, XType xt, const LinearPart *p, int count, bool silu_mul,
+                      int64_t M, int64_t K, int gs, YType yt, const Epilogue &epi, hipStream_t st) {
   if (M == 0 || count <= 0) return hipSuccess;
   GemvParts parts{};
   int tiles = 0;
@@ -580,8 +587,22 @@ hipError_t launch_gemv_parts(const void *X, XType xt, const LinearPart *p, int c
   parts.count = count;
   if (tiles == 0) return hipSuccess;
   const uint32_t zfix = p[0].zeros ? 0u : 8u;
-  if (silu_mul) return gemv_go<2>(X, xt, parts, tiles, M, K, gs, yt, zfix, st);
-  return gemv_go<1>(X, xt, parts, tiles, M, K, gs, yt, zfix, st);
+  if (silu_mul) return gemv_go<2>(X, xt, parts, tiles, M, K, gs, yt, zfix, epi, st);
+  return gemv_go<1>(X, xt, parts, tiles, M, K, gs, yt, zfix, epi, st);
+}
+}  // namespace
+
+hipError_t launch_gemv(const void *X, XType xt, const uint32_t *qweight,
+                       const uint16_t *scales, const uint8_t *zeros, int64_t M, int64_t N,
+                       int64_t K, int gs, void *Y, YType yt, hipStream_t st, const Epilogue &epi) {
+  const LinearPart one{qweight, scales, zeros, N, Y};
+  return gemv_parts(X, xt, &one, 1, false, M, K, gs, yt, epi, st);
+}
+
+hipError_t launch_gemv_parts(const void *X, XType xt, const LinearPart *p, int count,
+                             bool silu_mul, int64_t M, int64_t K, int gs, YType yt,
+                             hipStream_t st) {
+  return gemv_parts(X, xt, p, count, silu_mul, M, K, gs, yt, Epilogue{}, st);
 }
 
 }  // namespace awq

@@ -211,6 +211,38 @@ awq_status awq_linear_ex(const void *X, int32_t x_dtype, const uint32_t *qweight
 size_t awq_linear_workspace_size(int64_t M, int64_t N, int64_t K, awq_config cfg,
                                  int32_t x_dtype, int32_t kernel);
 
+/* Activations of awq_epilogue (int32_t).  GELU is 0.5 x (1 + erf(x / sqrt 2)),
+ * GELU_TANH 0.5 x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))), SILU
+ * x / (1 + e^-x). */
+enum { AWQ_ACT_NONE = 0, AWQ_ACT_RELU = 1, AWQ_ACT_SILU = 2, AWQ_ACT_GELU = 3, AWQ_ACT_GELU_TANH = 4 };
+
+/* What awq_linear_epilogue applies to the layer's sum. */
+typedef struct awq_epilogue {
+    const void *bias;       /* device, [N] of y_dtype, or NULL */
+    const void *residual;   /* device, [M][N] of y_dtype, or NULL; may be Y itself */
+    int32_t activation;     /* AWQ_ACT_* */
+} awq_epilogue;
+
+/*
+ * awq_linear_epilogue - Y = activation(X * deq(W)^T + bias) + residual, in the
+ * launch that awq_linear_ex makes for the layer alone (bias, activation and
+ * residual in fp32 on the layer's fp32 sums, one rounding to y_dtype).
+ *
+ *   epilogue  host; what is absent is left out.  residual may be Y (an update
+ *            of the residual stream in place: each element is read before it
+ *            is written) but may not overlap it otherwise.
+ * Everything else (kernels, arithmetic, workspace of
+ * awq_linear_workspace_size(M, N, K, cfg, x_dtype, kernel) bytes or NULL,
+ * requirements, errors) as awq_linear_ex.  An empty epilogue gives exactly
+ * awq_linear_ex's Y.
+ */
+awq_status awq_linear_epilogue(const void *X, int32_t x_dtype, const uint32_t *qweight,
+                               const uint16_t *scales, const uint8_t *zeros, int64_t M,
+                               int64_t N, int64_t K, awq_config cfg,
+                               const awq_epilogue *epilogue, void *Y, int32_t y_dtype,
+                               int32_t kernel, void *workspace, size_t workspace_bytes,
+                               awq_stream_t stream);
+
 /*
  * awq_linear_ws - awq_linear (automatic kernel choice) with a caller-owned
  * workspace: awq_linear_ex(..., AWQ_KERNEL_AUTO, workspace, workspace_bytes,
@@ -393,6 +425,153 @@ awq_status awq_scale_search_ex(const void *X, const void *W, int64_t M, int64_t 
                                size_t workspace_bytes, int32_t *best_index, double *losses,
                                float *best_s, uint32_t *qweight, uint16_t *scales,
                                uint8_t *zeros, uint8_t *clip_index, awq_stream_t stream);
+
+/* ---- the 4-bit paged key/value cache -------------------------------------
+ *
+ * Keys and values of attention held in the 4-bit group format of the weights:
+ * each token's key, and its value, of one head is one group (group_size =
+ * head_dim), quantized exactly as awq_quantize_pack quantizes a weight group
+ * (asymmetric with a zero point, or symmetric for zero_point = 0).  D/2 bytes
+ * and 2 or 3 bytes of step and zero point per token, head and key or value.
+ *
+ * Pages hold page_size tokens of every head.  A slot is page * page_size +
+ * offset.  Requests own pages through a block table int32 [num_seqs]
+ * [max_blocks]: token t of request b is in page block_table[b][t / page_size]
+ * at offset t % page_size.
+ *
+ * Layout, P = page_size, D = head_dim, H = num_kv_heads (words as in qweight,
+ * 8 channels each, nibble order above):
+ *  - codes   u32 [num_pages][2][H][P * D/8]: keys at index 0, a token's words
+ *            together, [P][D/8]; values at index 1, four tokens interleaved,
+ *            [P/4][D/8][4] (word w of token t at ((t / 4) * D/8 + w) * 4 + t % 4).
+ *  - scales  fp16 bits [num_pages][H][P][2]: step of the key, of the value.
+ *  - zeros   u8 [num_pages][H][P][2]: zero points likewise; absent for
+ *            zero_point = 0, whose zero is 8.
+ * All three 16-byte aligned.  head_dim 64 or 128, page_size a power of two in
+ * [AWQ_KV_MIN_PAGE, AWQ_KV_MAX_PAGE], num_pages * page_size at most 2^31.
+ * Keys and values are expected within fp16's range (a larger group's step
+ * would overflow). */
+#define AWQ_KV_MIN_PAGE 16
+#define AWQ_KV_MAX_PAGE 1024
+#define AWQ_KV_MAX_HEADS 1024
+typedef struct awq_kv_cache {
+    uint32_t *codes;
+    uint16_t *scales;
+    uint8_t *zeros;
+    int64_t num_pages;
+    int32_t page_size;
+    int32_t num_kv_heads;
+    int32_t head_dim;
+} awq_kv_cache;
+
+/*
+ * awq_kv_assign - pages and slots for the tokens that one step adds.
+ *   old_lens     device, int32 [num_seqs]: tokens each request has cached.
+ *   new_lens     device, int32 [num_seqs]: tokens it gets in this step (a
+ *                prompt, a chunk of one, or 1; 0 for none).
+ *   block_table  device, int32 [num_seqs][max_blocks], updated in place: the
+ *                entries of a request's first ceil(old / P) pages are read,
+ *                those of the pages it needs beyond them, up to
+ *                ceil((old + new) / P), are written, the rest left alone.
+ *   free_pages   device, int32 [num_free]: pages to take, from the front, in
+ *                request order.  A request that finds none left gets -1.
+ *   seq_lens     device, int32 [num_seqs], written: old + new.
+ *   query_start  device, int32 [num_seqs + 1], written: the step's tokens laid
+ *                end to end, request b's from query_start[b] on.
+ *   slots        device, int32 [num_slots], written: each token's slot, or -1
+ *                for a token without a page (none free, or past max_blocks)
+ *                and for the entries behind the last token.  num_slots at
+ *                least the number of tokens; tokens past it get no slot, and
+ *                a page that only such tokens open is not entered.
+ *   pages_used   device, int32 [1], written: pages the step needs (more than
+ *                num_free: it did not get them all).
+ * Negative lengths count as 0; sums saturate at 2^31 - 1.  Outputs may not
+ * overlap inputs or each other.  One launch; the result does not depend on
+ * any order of execution.  Requirements: max_blocks * P < 2^31.
+ */
+awq_status awq_kv_assign(const int32_t *old_lens, const int32_t *new_lens, int32_t num_seqs,
+                         int32_t page_size, int32_t *block_table, int32_t max_blocks,
+                         const int32_t *free_pages, int32_t num_free, int32_t *seq_lens,
+                         int32_t *query_start, int32_t *slots, int64_t num_slots,
+                         int32_t *pages_used, awq_stream_t stream);
+
+/*
+ * awq_kv_append - quantize keys and values into their slots.
+ *   K, V     device, [num_tokens][H][D] of x_dtype (AWQ_F16 or AWQ_BF16), the
+ *            heads of a token dense, tokens k_stride / v_stride elements apart
+ *            (a multiple of 8, so slices of a fused QKV output serve); 16-byte
+ *            aligned.
+ *   slots    device, int32 [num_tokens]; a token whose slot is negative or past
+ *            the cache is skipped.  Slots must be distinct (a slot given twice
+ *            ends with unspecified contents).
+ *   nonfinite_count  device int32 or NULL: as in awq_quantize_pack.
+ * The formula is awq_quantize_pack's with s = 1, per token and head.
+ */
+awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t num_tokens,
+                         int64_t k_stride, int64_t v_stride, const awq_kv_cache *cache,
+                         awq_config cfg, const int32_t *slots, int32_t *nonfinite_count,
+                         awq_stream_t stream);
+
+/*
+ * awq_kv_gather - the values that slots stand for, as awq_dequantize gives a
+ * weight's: K, V device [num_tokens][H][D] of out_dtype, dense, 16-byte
+ * aligned; (code - zero) * step, exact for AWQ_F32, rounded once for AWQ_F16 and
+ * AWQ_BF16.  A token whose slot is negative or past the cache gets zeros.
+ */
+awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_t *slots,
+                         int64_t num_tokens, void *K, void *V, int32_t out_dtype,
+                         awq_stream_t stream);
+
+/*
+ * awq_kv_attention - softmax attention of query tokens over the cache.
+ *   Q        device, [num_tokens][num_heads][D] of q_dtype (AWQ_F16 or
+ *            AWQ_BF16), the heads of a token dense, tokens q_stride elements
+ *            apart (a multiple of 8); 16-byte aligned.
+ *            Query heads h * num_heads / H and on share key/value head h.
+ *   block_table, seq_lens  as from awq_kv_assign; seq_lens counts the cached
+ *            tokens, those of this step included.
+ *   query_start  device, int32 [num_seqs + 1]: request b's query tokens, the
+ *            last ones of its seq_lens[b]; or NULL for one token per request
+ *            (then num_tokens = num_seqs and max_query_len = 1).
+ *   max_query_len  host: the most query tokens of a request; of a longer one
+ *            the rest is not computed.
+ *   max_seq_len  host: the expected largest seq_lens.  Only how the work is
+ *            split depends on it, never what is computed: a captured graph may
+ *            be replayed with other lengths.
+ *   causal   1: query token i of n sees keys 0 .. seq_len - n + i; 0: all keys.
+ *   window   > 0 (causal only): of those, the last `window`; 0: all.
+ *   O        device, [num_tokens][num_heads][D] of q_dtype, dense, 16-byte
+ *            aligned, not overlapping Q.
+ *   lse      device, fp32 [num_tokens][num_heads], or NULL: ln sum e^logit.
+ *   workspace  device, 256-byte aligned, awq_kv_attention_workspace_size()
+ *            bytes (NULL when that is 0); scratch as for awq_linear_ex, not to
+ *            be shared by calls that overlap in time.
+ * A row that sees no key gets O = 0 and lse = -inf.  Rows of no request (before
+ * query_start[0], or behind query_start[num_seqs]) are left as they were.
+ * Lengths beyond the table are cut to it; a table entry outside [0, num_pages)
+ * holds no tokens.  What lies in slots that a row does not see, infinities
+ * and NaN included, does not reach it.
+ * Arithmetic: logits are exact integer-times-query products summed in fp32,
+ * times the key's step and `scale`; softmax weights times the value's step are
+ * rounded once to fp16 (2^-11 relative) and multiplied by the exact integers;
+ * all sums, the maximum and the normalizer are fp32.  bfloat16 queries become
+ * fp16 by a power-of-two factor per tile of rows, exactly (below 2^-31 of the
+ * tile's largest value they are truncated).  Results do not change from call
+ * to call.
+ */
+awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, int64_t q_stride,
+                            int32_t num_heads, const awq_kv_cache *cache, awq_config cfg,
+                            const int32_t *block_table, int32_t max_blocks,
+                            const int32_t *seq_lens, const int32_t *query_start,
+                            int32_t num_seqs, int32_t max_query_len, int64_t max_seq_len,
+                            float scale, int32_t causal, int32_t window, void *O, float *lse,
+                            void *workspace, size_t workspace_bytes, awq_stream_t stream);
+
+/* Bytes of workspace that awq_kv_attention needs for these sizes (the cache's
+ * pointers may be NULL here); 0 when it needs none and on invalid arguments. */
+size_t awq_kv_attention_workspace_size(int64_t num_tokens, int32_t num_seqs, int32_t num_heads,
+                                       const awq_kv_cache *cache, awq_config cfg,
+                                       int32_t max_query_len, int64_t max_seq_len, int32_t window);
 
 /* Static description of a status code. */
 const char *awq_status_string(awq_status status);
