@@ -236,17 +236,62 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _device(device):
-    """The C calls launch on the current device: make it the tensors'."""
-    return _torch().cuda.device(device)
+# The calls below serve single tokens, where a few microseconds of Python are
+# the kernel's own time: their checks take the cheap form first (identity of
+# the dtype, comparison of the shape, device index) and come back to the
+# functions above only to say what is wrong.
+
+def _check(t, name, dtype, shape):
+    """_tensor for one dtype and a shape tuple."""
+    try:
+        if t.dtype is dtype and t.shape == shape:
+            return
+    except AttributeError:
+        pass
+    _tensor(t, name, dtype, shape)
 
 
-def _apart(a, a_name, b, b_name):
-    """Contiguous tensors a and b share no memory."""
-    a0, b0 = a.data_ptr(), b.data_ptr()
-    a1, b1 = a0 + a.numel() * a.element_size(), b0 + b.numel() * b.element_size()
-    if a0 < b1 and b0 < a1:
-        raise ValueError(f"{b_name} overlaps {a_name}")
+def _one_gpu(*named):
+    """_placed, as a device index; None entries are skipped."""
+    d = named[0][0].get_device()
+    for pair in named:
+        if pair is not None:
+            t = pair[0]
+            if d < 0 or t.get_device() != d or not t.is_contiguous():
+                _placed(*[p for p in named if p is not None])
+    return d
+
+
+def _launch(fn, device, *args):
+    """fn(*args, current stream) with `device` current, as the C calls want it; its status."""
+    torch = _torch()
+    if torch.cuda.current_device() == device:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device))
+    with torch.cuda.device(device):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device))
+
+
+def _address(t):
+    """The pointer argument of a tensor or None (an empty tensor's is NULL too)."""
+    return None if t is None else t.data_ptr() or None
+
+
+def _scratch(workspace, need, like):
+    """(tensor, bytes) of a workspace argument: 'auto', a tensor or None."""
+    torch = _torch()
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be a tensor, None or 'auto'")
+        if need == 0:
+            return None, 0
+        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    if workspace is None:
+        return None, 0
+    _tensor(workspace, "workspace")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+_CONFIGS = {(g, z): config(g, zero_point=z) for g in (64, 128) for z in (False, True)}
 
 
 def _dtype_code(dt):
@@ -434,39 +479,44 @@ def awq_linear_epilogue(X, qweight, scales, zeros, bias=None, residual=None,
     ACTIVATIONS.  bias [N] and residual [M][N] have the output's dtype (that of
     X unless out or out_dtype says otherwise); residual may be `out` itself.
     Kernel and workspace as in awq_linear_ex."""
-    if activation not in ACTIVATIONS:
+    torch = _torch()
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation {activation!r} is not one of {sorted(ACTIVATIONS)}")
-    if isinstance(workspace, str) and workspace != "auto":
-        raise ValueError("workspace must be a tensor, None or 'auto'")
-    if workspace is not None and not isinstance(workspace, str):
-        _tensor(workspace, "workspace")
-    _tensor(X, "X", (_torch().float16, _torch().bfloat16))
+    _tensor(X, "X", (torch.float16, torch.bfloat16))
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D [M][K]")
+    M, K = X.shape
+    if group_size <= 0 or K % group_size or K % 8:
+        raise ValueError(f"K={K} must be a multiple of 8 and of group_size={group_size}")
+    _tensor(qweight, "qweight", torch.int32)
+    N = qweight.shape[0] if qweight.dim() else 0
+    _check(qweight, "qweight", torch.int32, (N, K // 8))
+    _check(scales, "scales", torch.float16, (N, K // group_size))
+    if zeros is not None:
+        _check(zeros, "zeros", torch.uint8, (N, K // group_size))
     odt = out.dtype if out is not None else X.dtype if out_dtype is None else out_dtype
-    for t, name, dims in ((bias, "bias", 1), (residual, "residual", 2)):
-        if t is not None:
-            _tensor(t, name, odt)
-            if t.dim() != dims:
-                raise ValueError(f"{name} must be {dims}-D")
+    if odt not in (torch.float16, torch.bfloat16, torch.float32):
+        raise TypeError(f"out_dtype {odt} is not float16, bfloat16 or float32")
+    if out is not None:
+        _check(out, "out", odt, (M, N))
     if bias is not None:
-        _tensor(bias, "bias", shape=(qweight.shape[0],))
+        _check(bias, "bias", odt, (N,))
     if residual is not None:
-        _tensor(residual, "residual", shape=(X.shape[0], qweight.shape[0]))
-    M, N, K, out, dev = _linear_args(X, qweight, scales, zeros, group_size, out_dtype, out)
-    _placed((X, "X"), *[(t, name) for t, name in ((bias, "bias"), (residual, "residual"))
-                        if t is not None])
-    if residual is not None and residual.data_ptr() != out.data_ptr():
-        _apart(residual, "residual", out, "out")
-    need = awq_linear_workspace_size(M, N, K, group_size, X.dtype, kernel)
-    epi = awq_epilogue(None if bias is None else bias.data_ptr() or None,
-                       None if residual is None else residual.data_ptr() or None,
-                       ACTIVATIONS[activation])
-    with _device(dev):
-        ws = _workspace_arg(workspace, need, dev)
-        st = lib.awq_linear_epilogue(
-            _ptr(X), _dtype_code(X.dtype), _ptr(qweight), _ptr(scales), _zp_ptr(zeros), M, N, K,
-            config(group_size, zero_point=zeros is not None), ctypes.byref(epi), _ptr(out),
-            _dtype_code(out.dtype), int(kernel), ctypes.c_void_p(0) if ws is None else _ptr(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev))
+        _check(residual, "residual", odt, (M, N))
+    xd, cfg = _dtype_code(X.dtype), config(group_size, zero_point=zeros is not None)
+    need = 0 if workspace is None else lib.awq_linear_workspace_size(M, N, K, cfg, xd, kernel)
+    ws, ws_bytes = _scratch(workspace, need, X)
+    dev = _one_gpu((X, "X"), (qweight, "qweight"), (scales, "scales"),
+                   None if zeros is None else (zeros, "zeros"),
+                   None if bias is None else (bias, "bias"),
+                   None if residual is None else (residual, "residual"),
+                   None if out is None else (out, "out"), None if ws is None else (ws, "workspace"))
+    if out is None:
+        out = torch.empty((M, N), dtype=odt, device=X.device)
+    st = _launch(lib.awq_linear_epilogue, dev, _address(X), xd, _address(qweight), _address(scales),
+                 _address(zeros), M, N, K, cfg, awq_epilogue(_address(bias), _address(residual), act),
+                 _address(out), _dtype_code(odt), kernel, _address(ws), ws_bytes)
     check(st, "awq_linear_epilogue")
     return out
 
@@ -685,7 +735,8 @@ def _check_cache_sizes(num_pages, num_kv_heads, head_dim, page_size):
 
 
 def _cache_arg(cache):
-    """(awq_kv_cache, awq_config, named tensors) of a (codes, scales, zeros) cache."""
+    """(awq_kv_cache, awq_config) of a (codes, scales, zeros) cache; its device
+    and layout are left to _one_gpu."""
     torch = _torch()
     if not isinstance(cache, (tuple, list)) or len(cache) != 3:
         raise TypeError("cache must be (codes, scales, zeros)")
@@ -698,43 +749,47 @@ def _cache_arg(cache):
         raise ValueError("scales must be [pages][heads][page_size][2]")
     pages, _, heads, words = codes.shape
     page = scales.shape[2]
-    _tensor(scales, "scales", shape=(pages, heads, page, 2))
+    meta = (pages, heads, page, 2)
+    _check(scales, "scales", torch.float16, meta)
+    if zeros is not None:
+        _check(zeros, "zeros", torch.uint8, meta)
     if page < 1 or words * 8 % page:
         raise ValueError(f"codes hold {words} words per head and page, not a multiple of "
                          f"page_size={page} / 8")
     D = words * 8 // page
     _check_cache_sizes(pages, heads, D, page)
-    named = [(codes, "codes"), (scales, "scales")]
-    if zeros is not None:
-        _tensor(zeros, "zeros", torch.uint8, (pages, heads, page, 2))
-        named.append((zeros, "zeros"))
-    c = awq_kv_cache(codes.data_ptr() or None, scales.data_ptr() or None,
-                     None if zeros is None else zeros.data_ptr() or None, pages, page, heads, D)
-    return c, config(D, zero_point=zeros is not None), named
+    return (awq_kv_cache(codes.data_ptr(), scales.data_ptr(),
+                         None if zeros is None else zeros.data_ptr(), pages, page, heads, D),
+            _CONFIGS[D, zeros is not None])
 
 
-def _token_rows(t, name, heads, D, dtypes):
-    """[tokens][heads][D] with dense heads; returns the token stride."""
-    _tensor(t, name, dtypes)
+def _cache_tensors(cache):
+    codes, scales, zeros = cache
+    return (codes, "codes"), (scales, "scales"), None if zeros is None else (zeros, "zeros")
+
+
+def _token_rows(t, name, heads, D):
+    """Token stride of a GPU tensor [tokens][heads][D] whose heads are dense."""
     if t.dim() != 3 or t.shape[1:] != (heads, D):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens][{heads}][{D}]")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a GPU device, got {t.device}")
-    if t.shape[0] == 0:
-        return heads * D
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+    T, width = t.shape[0], heads * D
+    if T == 0:
+        return width
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else heads * D
-    if stride < heads * D or stride % 8:
-        raise ValueError(f"{name}: token stride {stride} must be a multiple of 8 of at least "
-                         f"{heads * D}")
-    return stride
+    if T == 1:
+        return width
+    if s0 < width or s0 % 8:
+        raise ValueError(f"{name}: token stride {s0} must be a multiple of 8 of at least {width}")
+    return s0
 
 
-def _same_device(dev, *named):
+def _same_gpu(d, *named):
     for t, name in named:
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev} like the other tensors")
+        if t.get_device() != d:
+            raise ValueError(f"{name} must be on a GPU device, cuda:{d} like the other tensors, "
+                             f"got {t.device}")
 
 
 def awq_kv_assign(old_lens, new_lens, block_table, free_pages, page_size: int, num_slots: int,
@@ -744,35 +799,35 @@ def awq_kv_assign(old_lens, new_lens, block_table, free_pages, page_size: int, n
     place with pages from the front of free_pages (int32).  Returns (seq_lens
     int32 [B], query_start int32 [B + 1], slots int32 [num_slots], pages_used
     int32 [1]), or fills `out`, a tuple of those."""
-    torch = _torch()
-    for t, name, dims in ((old_lens, "old_lens", 1), (new_lens, "new_lens", 1),
-                          (block_table, "block_table", 2), (free_pages, "free_pages", 1)):
-        _tensor(t, name, torch.int32)
-        if t.dim() != dims:
-            raise ValueError(f"{name} must be {dims}-D")
-    B = old_lens.shape[0]
-    _tensor(new_lens, "new_lens", shape=(B,))
-    _tensor(block_table, "block_table", shape=(B, block_table.shape[1]))
+    i32 = _torch().int32
+    _tensor(old_lens, "old_lens", i32)
+    _tensor(block_table, "block_table", i32)
+    _tensor(free_pages, "free_pages", i32)
+    if old_lens.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("old_lens and free_pages must be 1-D")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [B][max_blocks]")
+    B, blocks = old_lens.shape[0], block_table.shape[1]
+    _check(new_lens, "new_lens", i32, (B,))
+    _check(block_table, "block_table", i32, (B, blocks))
     if num_slots < 0:
         raise ValueError(f"num_slots={num_slots} is negative")
-    shapes = ((B,), (B + 1,), (num_slots,), (1,))
-    names = ("seq_lens", "query_start", "slots", "pages_used")
     if out is not None:
         if len(out) != 4:
             raise ValueError("out must be (seq_lens, query_start, slots, pages_used)")
-        for t, name, shape in zip(out, names, shapes):
-            _tensor(t, name, torch.int32, shape)
-    dev = _placed((old_lens, "old_lens"), (new_lens, "new_lens"), (block_table, "block_table"),
-                  (free_pages, "free_pages"))
-    if out is None:
-        out = tuple(torch.empty(s, dtype=torch.int32, device=dev) for s in shapes)
-    _placed((old_lens, "old_lens"), *zip(out, names))
+        for t, name, n in zip(out, ("seq_lens", "query_start", "slots", "pages_used"),
+                              (B, B + 1, num_slots, 1)):
+            _check(t, name, i32, (n,))
+    dev = _one_gpu((old_lens, "old_lens"), (new_lens, "new_lens"), (block_table, "block_table"),
+                   (free_pages, "free_pages"),
+                   *(() if out is None else ((t, "out") for t in out)))
+    if out is None:                                 # one allocation, in four parts
+        out = old_lens.new_empty(2 * B + num_slots + 2).split((B, B + 1, num_slots, 1))
     seq_lens, query_start, slots, used = out
-    with _device(dev):
-        st = lib.awq_kv_assign(_ptr(old_lens), _ptr(new_lens), B, page_size, _ptr(block_table),
-                               block_table.shape[1], _ptr(free_pages), free_pages.shape[0],
-                               _ptr(seq_lens), _ptr(query_start), _ptr(slots), num_slots,
-                               _ptr(used), _stream(dev))
+    st = _launch(lib.awq_kv_assign, dev, _address(old_lens), _address(new_lens), B, page_size,
+                 _address(block_table), blocks, _address(free_pages), free_pages.shape[0],
+                 _address(seq_lens), query_start.data_ptr(), _address(slots), num_slots,
+                 used.data_ptr())
     check(st, "awq_kv_assign")
     return tuple(out)
 
@@ -782,27 +837,24 @@ def awq_kv_append(K, V, cache, slots, nonfinite_count=None):
     as slices of a fused projection's output are) into the cache's slots (int32
     [tokens]; tokens with a negative slot are skipped).  Returns the cache."""
     torch = _torch()
-    c, cfg, named = _cache_arg(cache)
-    H, D = c.num_kv_heads, c.head_dim
-    dts = (torch.float16, torch.bfloat16)
-    ks, vs = _token_rows(K, "K", H, D, dts), _token_rows(V, "V", H, D, dts)
-    if V.dtype != K.dtype or V.shape[0] != K.shape[0]:
-        raise ValueError("K and V must have the same dtype and number of tokens")
+    c, cfg = _cache_arg(cache)
+    _tensor(K, "K", (torch.float16, torch.bfloat16))
+    _tensor(V, "V", K.dtype)
+    ks, vs = (_token_rows(K, "K", c.num_kv_heads, c.head_dim),
+              _token_rows(V, "V", c.num_kv_heads, c.head_dim))
     T = K.shape[0]
-    _tensor(slots, "slots", torch.int32, (T,))
-    named.append((slots, "slots"))
-    cp = ctypes.c_void_p(0)
+    if V.shape[0] != T:
+        raise ValueError("K and V must have the same number of tokens")
+    _check(slots, "slots", torch.int32, (T,))
     if nonfinite_count is not None:
         _tensor(nonfinite_count, "nonfinite_count", torch.int32)
         if nonfinite_count.numel() < 1:
             raise ValueError("nonfinite_count must hold one element")
-        named.append((nonfinite_count, "nonfinite_count"))
-        cp = _ptr(nonfinite_count)
-    dev = _placed(*named)
-    _same_device(dev, (K, "K"), (V, "V"))
-    with _device(dev):
-        st = lib.awq_kv_append(_ptr(K), _ptr(V), _dtype_code(K.dtype), T, ks, vs, ctypes.byref(c),
-                               cfg, _ptr(slots), cp, _stream(dev))
+    dev = _one_gpu(*_cache_tensors(cache), (slots, "slots"),
+                   None if nonfinite_count is None else (nonfinite_count, "nonfinite_count"))
+    _same_gpu(dev, (K, "K"), (V, "V"))
+    st = _launch(lib.awq_kv_append, dev, _address(K), _address(V), _dtype_code(K.dtype), T, ks, vs, c,
+                 cfg, _address(slots), _address(nonfinite_count))
     check(st, "awq_kv_append")
     return cache
 
@@ -812,30 +864,27 @@ def awq_kv_gather(cache, slots, out_dtype=None, out=None):
     [tokens][heads][D] of out_dtype (float16 by default, bfloat16 or float32);
     zeros for negative slots."""
     torch = _torch()
-    c, cfg, named = _cache_arg(cache)
+    c, cfg = _cache_arg(cache)
     _tensor(slots, "slots", torch.int32)
     if slots.dim() != 1:
         raise ValueError("slots must be 1-D")
-    named.append((slots, "slots"))
-    shape = (slots.shape[0], c.num_kv_heads, c.head_dim)
-    dts = (torch.float16, torch.bfloat16, torch.float32)
-    odt = torch.float16 if out_dtype is None else out_dtype
-    if out is not None:
-        if len(out) != 2:
-            raise ValueError("out must be (K, V)")
-        for t, name in zip(out, ("K", "V")):
-            _tensor(t, name, dts, shape)
-        odt = out[0].dtype
-        _tensor(out[1], "V", odt)
-    elif odt not in dts:
+    T = slots.shape[0]
+    shape = (T, c.num_kv_heads, c.head_dim)
+    if out is not None and len(out) != 2:
+        raise ValueError("out must be (K, V)")
+    odt = out[0].dtype if out is not None else torch.float16 if out_dtype is None else out_dtype
+    if odt not in (torch.float16, torch.bfloat16, torch.float32):
         raise TypeError(f"out_dtype {odt} is not float16, bfloat16 or float32")
-    dev = _placed(*named)
+    if out is not None:
+        _check(out[0], "K", odt, shape)
+        _check(out[1], "V", odt, shape)
+    dev = _one_gpu(*_cache_tensors(cache), (slots, "slots"),
+                   *(() if out is None else ((out[0], "K"), (out[1], "V"))))
     if out is None:
-        out = tuple(torch.empty(shape, dtype=odt, device=dev) for _ in range(2))
-    _placed((slots, "slots"), (out[0], "K"), (out[1], "V"))
-    with _device(dev):
-        st = lib.awq_kv_gather(ctypes.byref(c), cfg, _ptr(slots), slots.shape[0], _ptr(out[0]),
-                               _ptr(out[1]), _dtype_code(odt), _stream(dev))
+        out = (torch.empty(shape, dtype=odt, device=slots.device),
+               torch.empty(shape, dtype=odt, device=slots.device))
+    st = _launch(lib.awq_kv_gather, dev, c, cfg, _address(slots), T, _address(out[0]),
+                 _address(out[1]), _dtype_code(odt))
     check(st, "awq_kv_gather")
     return tuple(out)
 
@@ -843,9 +892,9 @@ def awq_kv_gather(cache, slots, out_dtype=None, out=None):
 def awq_kv_attention_workspace_size(num_tokens: int, num_seqs: int, num_heads: int, cache,
                                     max_query_len: int, max_seq_len: int, window: int = 0) -> int:
     """Workspace bytes of awq_kv_attention for these sizes; cache as passed to it."""
-    c, cfg, _ = _cache_arg(cache)
-    return int(lib.awq_kv_attention_workspace_size(num_tokens, num_seqs, num_heads, ctypes.byref(c),
-                                                   cfg, max_query_len, max_seq_len, window))
+    c, cfg = _cache_arg(cache)
+    return int(lib.awq_kv_attention_workspace_size(num_tokens, num_seqs, num_heads, c, cfg,
+                                                   max_query_len, max_seq_len, window))
 
 
 def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_query_len=None,
@@ -865,23 +914,21 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     of tokens of no request are not written (pass `out` to say what they hold).
     ``workspace``: as in awq_linear_ex."""
     torch = _torch()
-    c, cfg, named = _cache_arg(cache)
+    c, cfg = _cache_arg(cache)
     D = c.head_dim
     _tensor(Q, "Q", (torch.float16, torch.bfloat16))
     if Q.dim() != 3 or Q.shape[2] != D:
         raise ValueError(f"Q has shape {tuple(Q.shape)}, expected [tokens][num_heads][{D}]")
-    T, heads = Q.shape[:2]
+    T, heads, _ = Q.shape
     if heads < 1 or heads % c.num_kv_heads:
         raise ValueError(f"{heads} query heads are not a multiple of {c.num_kv_heads} key/value heads")
     _tensor(block_table, "block_table", torch.int32)
     if block_table.dim() != 2:
         raise ValueError("block_table must be 2-D [B][max_blocks]")
     B, blocks = block_table.shape
-    _tensor(seq_lens, "seq_lens", torch.int32, (B,))
-    named += [(block_table, "block_table"), (seq_lens, "seq_lens")]
+    _check(seq_lens, "seq_lens", torch.int32, (B,))
     if query_start is not None:
-        _tensor(query_start, "query_start", torch.int32, (B + 1,))
-        named.append((query_start, "query_start"))
+        _check(query_start, "query_start", torch.int32, (B + 1,))
     elif T != B:
         raise ValueError(f"{T} query tokens for {B} requests need query_start")
     if max_query_len is None:
@@ -891,31 +938,21 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     if max_seq_len is None:
         max_seq_len = blocks * c.page_size
     if out is not None:
-        _tensor(out, "out", Q.dtype, (T, heads, D))
-    if isinstance(workspace, str) and workspace != "auto":
-        raise ValueError("workspace must be a tensor, None or 'auto'")
-    if workspace is not None and not isinstance(workspace, str):
-        _tensor(workspace, "workspace")
-    stride = _token_rows(Q, "Q", heads, D, Q.dtype)
-    dev = _placed(*named)
-    _same_device(dev, (Q, "Q"))
+        _check(out, "out", Q.dtype, (T, heads, D))
+    stride = _token_rows(Q, "Q", heads, D)
+    need = 0 if workspace is None else lib.awq_kv_attention_workspace_size(
+        T, B, heads, c, cfg, max_query_len, max_seq_len, window)
+    ws, ws_bytes = _scratch(workspace, need, seq_lens)
+    dev = _one_gpu(*_cache_tensors(cache), (block_table, "block_table"), (seq_lens, "seq_lens"),
+                   None if query_start is None else (query_start, "query_start"),
+                   None if out is None else (out, "out"), None if ws is None else (ws, "workspace"))
+    _same_gpu(dev, (Q, "Q"))
     if out is None:
-        out = torch.empty((T, heads, D), dtype=Q.dtype, device=dev)
-    _placed((seq_lens, "seq_lens"), (out, "out"))
-    lse = None
-    if return_lse:
-        lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
-    need = int(lib.awq_kv_attention_workspace_size(T, B, heads, ctypes.byref(c), cfg,
-                                                   max_query_len, max_seq_len, window))
-    with _device(dev):
-        ws = _workspace_arg(workspace, need, dev)
-        st = lib.awq_kv_attention(
-            _ptr(Q), _dtype_code(Q.dtype), T, stride, heads, ctypes.byref(c), cfg,
-            _ptr(block_table), blocks, _ptr(seq_lens),
-            ctypes.c_void_p(0) if query_start is None else _ptr(query_start), B, max_query_len,
-            max_seq_len, D ** -0.5 if scale is None else float(scale), int(bool(causal)), window,
-            _ptr(out), ctypes.c_void_p(0) if lse is None else _ptr(lse),
-            ctypes.c_void_p(0) if ws is None else _ptr(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), _stream(dev))
+        out = torch.empty((T, heads, D), dtype=Q.dtype, device=Q.device)
+    lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device) if return_lse else None
+    st = _launch(lib.awq_kv_attention, dev, _address(Q), _dtype_code(Q.dtype), T, stride, heads, c,
+                 cfg, _address(block_table), blocks, _address(seq_lens), _address(query_start), B,
+                 max_query_len, max_seq_len, D ** -0.5 if scale is None else scale, int(causal),
+                 window, _address(out), _address(lse), _address(ws), ws_bytes)
     check(st, "awq_kv_attention")
     return (out, lse) if return_lse else out

@@ -360,6 +360,12 @@ awq_status awq_linear_epilogue(const void *X, int32_t x_dtype, const uint32_t *q
   const size_t a = y_dtype == AWQ_F32 ? 4 : 2;
   if (!aligned(epilogue->bias, a) || !aligned(epilogue->residual, a))
     return fail(AWQ_ERR_INVALID_ARG, "%s: bias and residual must be aligned to y_dtype's size", who);
+  if (M > 0 && N > 0 && M <= ((int64_t)1 << 31) && N <= ((int64_t)1 << 31)) {
+    const size_t y_bytes = (size_t)M * (size_t)N * a;
+    if ((epilogue->bias && !apart(epilogue->bias, (size_t)N * a, Y, y_bytes)) ||
+        (epilogue->residual && epilogue->residual != Y && !apart(epilogue->residual, y_bytes, Y, y_bytes)))
+      return fail(AWQ_ERR_INVALID_ARG, "%s: Y overlaps the bias, or the residual without being it", who);
+  }
   const awq::Epilogue epi{epilogue->bias, epilogue->residual, (awq::Act)epilogue->activation};
   return linear_impl(who, X, x_dtype, qweight, scales, zeros, M, N, K, cfg, Y, y_dtype, kernel,
                      workspace, workspace_bytes, stream, epi);

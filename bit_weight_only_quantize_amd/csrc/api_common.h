@@ -14,6 +14,11 @@ awq_status ok();
 awq_status hip_status(hipError_t e, const char *where);
 
 inline bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Bytes [p, p + n) and [q, q + m) share none.
+inline bool apart(const void *p, size_t n, const void *q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return n == 0 || m == 0 || a + n <= b || b + m <= a;
+}
 inline hipStream_t as_stream(awq_stream_t s) { return reinterpret_cast<hipStream_t>(s); }
 
 constexpr size_t kAlign = 256;      // of workspaces and their regions

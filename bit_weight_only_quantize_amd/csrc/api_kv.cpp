@@ -23,12 +23,6 @@ awq_status check_page(const char *who, int32_t page_size) {
   return AWQ_OK;
 }
 
-// Bytes [p, p + n) and [q, q + m) share none.
-bool apart(const void *p, size_t n, const void *q, size_t m) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return n == 0 || m == 0 || a + n <= b || b + m <= a;
-}
-
 awq_status check_cache(const char *who, const awq_kv_cache *c, awq_config cfg, bool need_ptrs) {
   if (!c) return fail(AWQ_ERR_INVALID_ARG, "%s: cache is NULL", who);
   if (cfg.w_bit != 4) return fail(AWQ_ERR_UNSUPPORTED, "%s: w_bit=%d: only 4 is supported", who, cfg.w_bit);

@@ -52,6 +52,15 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// a * (half h of w) with the half widened by the instruction (v_fma_mix_f32).
+__device__ __forceinline__ float mul_lo_half(float a, uint32_t w) { return __builtin_fmaf(a, lo_half(w), 0.0f); }
+__device__ __forceinline__ float mul_hi_half(float a, uint32_t w) { return __builtin_fmaf(a, hi_half(w), 0.0f); }
+
+__device__ __forceinline__ uint32_t max_half2(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(f16x2, a),
+                                                                __builtin_bit_cast(f16x2, b)));
+}
+
 // Bytes b of x and y as the low bytes of the two halves of a word.
 template <int B>
 __device__ __forceinline__ uint32_t byte_pair(uint32_t x, uint32_t y) {
@@ -106,6 +115,14 @@ __device__ __forceinline__ uint32_t bf16_magnitude8(u32x4 raw) {
   return m;
 }
 
+// The logits' scale times log2(e) as the kernels use it: positive (a scale of 0
+// as one too small to matter), so that -inf times it stays -inf.
+__device__ __forceinline__ float positive_scale(float cs) { return cs > 0x1p-120f ? cs : 0x1p-120f; }
+// top * cs + vexp; kNone while no key was seen.
+__device__ __forceinline__ float running_max(float top, float cs, float vexp) {
+  return top == kNone ? kNone : __builtin_fmaf(top, cs, vexp);
+}
+
 // What a workgroup knows about its request.
 struct Request {
   int64_t token0;        // first query token
@@ -153,22 +170,36 @@ __device__ __forceinline__ int first_key(const KvAttn &p, int last) {
 // codes (D = 128: words 4kq.. of token c; 1 KiB per wave, one run), one of
 // value codes (word c of tokens 4kq..4kq+3), one of their steps, and 8 bytes
 // of zero points.  S^T comes out as keys 4kq + e of row c.
+//
+// Registers hold one tile: key codes are refilled with the next tile's as soon
+// as they are dequantized, steps and zero points after the softmax, value codes
+// after their dequantization, so a load has most of a tile's work to arrive in
+// while four waves share a SIMD.  (Two register sets, two waves per SIMD,
+// measured 128 us where this takes 97 on 48 requests of up to 4096 tokens, 32
+// heads of 128.)
 template <int D>
-struct DecodeBuf {
+struct DecodeTile {
   static constexpr int kWords = D / 32;              // key words per lane and token
   uint32_t k[2][kWords];
   u32x4 v[2];
   u32x4 sc[2];
   u32x2 z[2];
-  uint32_t bad;                                      // bit i: tokens of half i have no page
+};
+// Where a tile's halves lie, in bytes of codes and of zero points (steps take
+// twice that); bit i of bad: half i has no page (it reads page 0's).
+struct DecodeAt {
+  int64_t code[2], meta[2];
+  uint32_t bad;
 };
 
 template <int D, bool SYM, bool BF16, int NW>
-__global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(3, 3)))
+void kv_decode_kernel(KvAttn p) {
   constexpr int kWords = D / 32, kTiles = D / 16;
   constexpr int kRow = D + 4;                        // floats per row in LDS
   __shared__ __attribute__((aligned(16))) float red[NW][16][kRow];
   __shared__ float red_m[NW][16], red_l[NW][16];
+  __shared__ u32x4 sq[kWords][64];                   // the queries as MFMA operands, per lane
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, kq = lane >> 4;
@@ -191,13 +222,14 @@ __global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
   const int i0 = (int)((int64_t)nt * part / parts), i1 = (int)((int64_t)nt * (part + 1) / parts);
 
   // queries: lane (c, kq) holds channels 32kq.. (D = 128) or 16kq.. (D = 64)
-  // of row c, the channels of the key words that it will load
+  // of row c, the channels of the key words that it will load; negated for a
+  // negative scale, so that larger sums are larger logits
   const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
                        (int64_t)(h * p.group + row % p.group) * D + kq * (8 * kWords);
   u32x4 q[kWords];
 #pragma unroll
   for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
-  float cs = p.scale_log2;
+  float cs = __builtin_fabsf(p.scale_log2);
   if constexpr (BF16) {
     uint32_t m = 0;
 #pragma unroll
@@ -215,7 +247,20 @@ __global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
     for (int j = 0; j < kWords; ++j) q[j] = bf16_to_half8(q[j], f);
     cs *= 1.0f / f;
   }
-  // sum of the row's queries, for the zero points: S = s (codes - 8) . q + (8 - z) sum q
+  cs = positive_scale(cs);
+  if (p.scale_log2 < 0.0f) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[j][i] ^= 0x80008000u;
+  }
+  // (every wave has the same 16 rows; in registers they would cost the loop 16
+  // of them, and with those a wave per SIMD)
+  if (wave == 0) {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) sq[j][lane] = q[j];
+  }
+  // sum of the row's queries, for the zero points: sum q (code - z) = sum q code - z sum q
   float qsum = 0.0f;
   if constexpr (!SYM) {
 #pragma unroll
@@ -238,108 +283,154 @@ __global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
     const int at = first + lane;
     page_ids = at < p.max_blocks ? table[at] : -1;
   };
-  // lane offsets within a page's key words, value words, steps, zero points
-  const uint32_t k_lane = D == 128 ? c * 16 + kq * 4 : c * 8 + kq * 2;       // words
-  const uint32_t v_lane = kq * (D / 2) + (c & (D / 8 - 1)) * 4;              // words
-  auto load = [&](int t, DecodeBuf<D> &buf) {
-    buf.bad = 0;
+  // A load's address is a uniform base (the tile's place) plus the lane's byte
+  // offset within 16 tokens' key words, value words, and steps (zero points:
+  // half of that).
+  const uint32_t k_lane = D == 128 ? c * 64 + kq * 16 : c * 32 + kq * 8;
+  const uint32_t v_lane = kq * (2 * D) + (c & (D / 8 - 1)) * 16, s_lane = kq * 16;
+  const int64_t P = (int64_t)pmask + 1;
+  const int64_t code_stride = (int64_t)p.heads * P * D, meta_stride = (int64_t)p.heads * P * 2;
+  const int64_t v_offset = code_stride / 2;
+  const char *codes = reinterpret_cast<const char *>(p.codes) + h * P * (D / 2);
+  const char *scales = reinterpret_cast<const char *>(p.scales) + h * P * 4;
+  const char *zeros = reinterpret_cast<const char *>(p.zeros) + h * P * 2;
+  const int pages = p.pages < 0x7FFFFFFF ? (int)p.pages : 0x7FFFFFFF;
+  auto place = [&](int t) {
+    DecodeAt at;
+    at.bad = 0;
     // the pages of both halves lie within 64 of page_base, or are fetched
-    const int last = (t + 31) >> p.pshift;
-    if (last - page_base > 63) load_pages(t >> p.pshift);
+    if (((t + 31) >> p.pshift) - page_base > 63) load_pages(t >> p.pshift);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int tt = t + 16 * i;
-      const int id = __builtin_amdgcn_readlane(page_ids, (tt >> p.pshift) - page_base);
-      const bool ok = id >= 0 && id < p.pages;
-      if (!ok) buf.bad |= 1u << i;
-      const int64_t page = ok ? id : 0;
-      const int64_t off = tt & pmask;
-      const int64_t P = (int64_t)pmask + 1;
-      const uint32_t *kb = p.codes + ((page * 2 * p.heads + h) * P + off) * (D / 8);
-      const uint32_t *vb = kb + (int64_t)p.heads * P * (D / 8);
-      const int64_t meta = ((page * p.heads + h) * P + off) * 2;
-      if constexpr (D == 128) {
-        const u32x4 w = *reinterpret_cast<const u32x4 *>(kb + k_lane);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) buf.k[i][j] = w[j];
-      } else {
-        const u32x2 w = *reinterpret_cast<const u32x2 *>(kb + k_lane);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) buf.k[i][j] = w[j];
+      int id = __builtin_amdgcn_readlane(page_ids, (tt >> p.pshift) - page_base);
+      if ((uint32_t)id >= (uint32_t)pages) {
+        at.bad |= 1u << i;
+        id = 0;
       }
-      buf.v[i] = *reinterpret_cast<const u32x4 *>(vb + v_lane);
-      buf.sc[i] = *reinterpret_cast<const u32x4 *>(p.scales + meta + kq * 8);
-      if constexpr (!SYM) buf.z[i] = *reinterpret_cast<const u32x2 *>(p.zeros + meta + kq * 8);
+      at.code[i] = id * code_stride + (tt & pmask) * (D / 2);
+      at.meta[i] = id * meta_stride + (tt & pmask) * 2;
+    }
+    return at;
+  };
+  DecodeTile<D> T;
+  auto load_keys = [&](const DecodeAt &at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const char *src = codes + at.code[i];
+      if constexpr (D == 128) {
+        const u32x4 w = *reinterpret_cast<const u32x4 *>(src + k_lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) T.k[i][j] = w[j];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2 *>(src + k_lane);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) T.k[i][j] = w[j];
+      }
+    }
+  };
+  auto load_meta = [&](const DecodeAt &at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const char *src = scales + 2 * at.meta[i];
+      T.sc[i] = *reinterpret_cast<const u32x4 *>(src + s_lane);
+      if constexpr (!SYM) {
+        const char *zsrc = zeros + at.meta[i];
+        T.z[i] = *reinterpret_cast<const u32x2 *>(zsrc + s_lane / 2);
+      }
+    }
+  };
+  auto load_values = [&](const DecodeAt &at) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const char *src = codes + (at.code[i] + v_offset);
+      T.v[i] = *reinterpret_cast<const u32x4 *>(src + v_lane);
     }
   };
 
   f32x4 o[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float M = kNone, top = kNone, vlim = 0.0f, l = 0.0f, pz = 0.0f;
-  float vexp = 0.0f;                                 // M = top + vexp, 2^vexp = vlim
+  // M = top * cs + vexp, top the largest sum so far (times the key's step), 2^vexp = vlim
+  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f, pz = 0.0f;
+  const float slack_width = kSlack / cs;
   const DeqRegs dq;
-  const DeqF16 deq8(8u);
+  const DeqF16 deq8(8u), deqk(SYM ? 8u : 0u);
   // D = 64 has 8 words per token but an MFMA operand 16 rows: lanes c and
   // c + 8 take the same word, the first its even channels (bytes 0, 1), the
   // second its odd ones (bytes 2, 3)
   const uint32_t sel0 = D == 128 ? 0u : (c < 8 ? 0x0C040C00u : 0x0C060C02u);
   const uint32_t sel1 = D == 128 ? 0u : (c < 8 ? 0x0C050C01u : 0x0C070C03u);
 
-  auto compute = [&](const DecodeBuf<D> &buf, int t) {
-    float u[8], vs[8], kz[8], vz[8];
+  // One tile of 32 tokens at t (in T, placed at `at`); `next`: the tile to refill T with.
+  auto tile = [&](int t, const DecodeAt &at, const DecodeAt &next, auto more_tag) {
+    constexpr bool kMore = decltype(more_tag)::value;
+    f32x4 s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f32x4 s = {0.f, 0.f, 0.f, 0.f};
+      s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < kWords; ++j) s = mfma32<TagF16>(deq8(buf.k[i][j], dq), q[j], s);
+      for (int j = 0; j < kWords; ++j)
+        s[i] = mfma32<TagF16>(deqk(T.k[i][j], dq), sq[j][lane], s[i]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kMore) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_keys(next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t w = buf.sc[i][e];
-        float x = s[e];
+        const uint32_t w = T.sc[i][e];
+        float x = s[i][e];
         if constexpr (!SYM) {
-          const uint32_t zz = buf.z[i][e >> 1] >> (16 * (e & 1));
-          kz[4 * i + e] = 8.0f - (float)(zz & 0xFFu);
-          vz[4 * i + e] = (float)((zz >> 8) & 0xFFu) - 8.0f;
-          x = __builtin_fmaf(kz[4 * i + e], qsum, x);
+          const uint32_t zz = T.z[i][e >> 1];
+          x = __builtin_fmaf(-(float)((zz >> (16 * (e & 1))) & 0xFFu), qsum, x);
         }
-        vs[4 * i + e] = hi_half(w);
-        u[4 * i + e] = x * (lo_half(w) * cs);
+        u[4 * i + e] = mul_lo_half(x, w);
       }
-    }
-    if (buf.bad || t < all_first || t + 31 > all_last) {
+    if (at.bad || t < all_first || t + 31 > all_last) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int at = t + 16 * i + 4 * kq + e;
-          const bool seen = at >= my_first && at <= my_last && !((buf.bad >> i) & 1u);
+          const int k = t + 16 * i + 4 * kq + e;
+          const bool seen = k >= my_first && k <= my_last && !((at.bad >> i) & 1u);
           u[4 * i + e] = seen ? u[4 * i + e] : -__builtin_inff();
-          vs[4 * i + e] = seen ? vs[4 * i + e] : 0.0f;
+          T.sc[i][e] = seen ? T.sc[i][e] : 0u;
         }
-      }
     }
-    float umax = u[0], vmax = vs[0];
+    float umax = u[0];
+    uint32_t smax = T.sc[0][0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
+      const uint32_t w = T.sc[i >> 2][i & 3];
       umax = fmaxf(umax, u[i]);
-      vmax = fmaxf(vmax, vs[i]);
+      smax = max_half2(smax, w);
     }
-    if (__any(umax > top + kSlack || vmax > vlim)) {
+    if (__any(umax > slack || hi_half(smax) > vlim)) {
       umax = fmaxf(umax, __shfl_xor(umax, 16, 64));
       umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
-      vmax = 0.0f;
+      // (a step that overflowed counts for none)
+      float vmax = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) vmax = fmaxf(vmax, vs[i] <= 65504.0f ? vs[i] : 0.0f);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w = T.sc[i >> 2][i & 3];
+        vmax = fmaxf(vmax, hi_half(w) <= 65504.0f ? hi_half(w) : 0.0f);
+      }
 #pragma unroll
       for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
       top = fmaxf(top, umax);
-      if (vmax > vlim) {                             // uniform; (a step that overflowed counts for none)
+      slack = top + slack_width;
+      if (vmax > vlim) {                             // uniform
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         vexp = (float)ex;
         vlim = __builtin_ldexpf(1.0f, ex);
       }
-      const float m2 = top + vexp, a = __builtin_amdgcn_exp2f(M - m2);
+      const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
       l *= a;
       pz *= a;
@@ -348,25 +439,37 @@ __global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] *= a;
     }
-    float pr[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = __builtin_amdgcn_exp2f(u[i] - M);
-      l += x;
-      pr[i] = x * vs[i];
-      if constexpr (!SYM) pz = __builtin_fmaf(pr[i], vz[i], pz);
-    }
     u32x4 pb;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pb[i] = pack_half2(pr[2 * i], pr[2 * i + 1]);
+    for (int i = 0; i < 2; ++i) {
+      float pr[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(u[4 * i + e], cs, -M));
+        l += x;
+        const uint32_t w = T.sc[i][e];
+        pr[e] = mul_hi_half(x, w);
+        if constexpr (!SYM) {
+          const uint32_t zz = T.z[i][e >> 1];
+          pz = __builtin_fmaf(pr[e], (float)((zz >> (16 * (e & 1) + 8)) & 0xFFu) - 8.0f, pz);
+        }
+      }
+      pb[2 * i] = pack_half2(pr[0], pr[1]);
+      pb[2 * i + 1] = pack_half2(pr[2], pr[3]);
+    }
+    if constexpr (kMore) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_meta(next);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // value operands: byte b of the words of tokens (2j, 2j+1) in the halves
     // of a word, then each nibble as an exact code - 8
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[4 * i + e] = buf.v[i][e];
-    auto tile = [&](auto byte_of, int n) {
+      for (int e = 0; e < 4; ++e) w[4 * i + e] = T.v[i][e];
+    auto product = [&](auto byte_of, int n) {
       u32x4 lo, hi;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -376,32 +479,38 @@ __global__ __launch_bounds__(64 * NW) void kv_decode_kernel(KvAttn p) {
       }
       o[n] = mfma32<TagF16>(lo, pb, o[n]);
       o[n + 1] = mfma32<TagF16>(hi, pb, o[n + 1]);
+      __builtin_amdgcn_sched_barrier(0);             // (bounds the registers in use)
     };
     if constexpr (D == 128) {
-      tile([](uint32_t x, uint32_t y) { return byte_pair<0>(x, y); }, 0);
-      tile([](uint32_t x, uint32_t y) { return byte_pair<1>(x, y); }, 2);
-      tile([](uint32_t x, uint32_t y) { return byte_pair<2>(x, y); }, 4);
-      tile([](uint32_t x, uint32_t y) { return byte_pair<3>(x, y); }, 6);
+      product([](uint32_t x, uint32_t y) { return byte_pair<0>(x, y); }, 0);
+      product([](uint32_t x, uint32_t y) { return byte_pair<1>(x, y); }, 2);
+      product([](uint32_t x, uint32_t y) { return byte_pair<2>(x, y); }, 4);
+      product([](uint32_t x, uint32_t y) { return byte_pair<3>(x, y); }, 6);
     } else {
-      tile([&](uint32_t x, uint32_t y) { return byte_pair(x, y, sel0); }, 0);
-      tile([&](uint32_t x, uint32_t y) { return byte_pair(x, y, sel1); }, 2);
+      product([&](uint32_t x, uint32_t y) { return byte_pair(x, y, sel0); }, 0);
+      product([&](uint32_t x, uint32_t y) { return byte_pair(x, y, sel1); }, 2);
+    }
+    if constexpr (kMore) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_values(next);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
 
+  __syncthreads();
   if (i0 < i1) {
-    load_pages((t_lo + 32 * i0) >> p.pshift);
-    DecodeBuf<D> A, B;
-    load(t_lo + 32 * i0, A);
-    int i = i0;
-    for (; i + 1 < i1; i += 2) {
-      load(t_lo + 32 * (i + 1), B);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(A, t_lo + 32 * i);
-      if (i + 2 < i1) load(t_lo + 32 * (i + 2), A);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(B, t_lo + 32 * (i + 1));
+    int t = t_lo + 32 * i0;
+    load_pages(t >> p.pshift);
+    DecodeAt at = place(t);
+    load_keys(at);
+    load_meta(at);
+    load_values(at);
+    for (int i = i0; i + 1 < i1; ++i, t += 32) {
+      const DecodeAt next = place(t + 32);
+      tile(t, at, next, std::true_type{});
+      at = next;
     }
-    if (i < i1) compute(A, t_lo + 32 * i);
+    tile(t, at, at, std::false_type{});
   }
 
   // ---- join the waves --------------------------------------------------------------
@@ -801,39 +910,61 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
 }
 
 // ---- join the splits ---------------------------------------------------------------------------
-// Row (token, head): weights 2^(lse_s - max lse) over the splits, one wave per
-// row, in split order.  A split in which the row saw no key has written -inf
-// and no O.  Rows that no request serves were not written and are not read.
+// Row (token, head): weights 2^(lse_s - max lse) over at most kMaxSplits splits,
+// one workgroup per row: lane s of every wave reads split s's lse, wave w sums
+// the splits s = w mod 4, their rows loaded eight at a time, and the four sums
+// meet in LDS.  (One wave per row, a split at a time, took 24 us where this
+// takes 4 for 32 splits of 256 rows.)  A split in which the row saw no key has
+// written -inf and no O.  Rows that no request serves were not written and are
+// not read.
+constexpr int kMaxSplits = 64;
+
 template <int D, bool BF16>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
-  constexpr int kPer = D / 64;
+  constexpr int kPer = D / 64, kChunk = 8;
+  __shared__ float part[4][D], part_sum[4];
   const int lane = threadIdx.x & 63;
-  const int b = blockIdx.z, h = blockIdx.y;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int b = blockIdx.z, h = blockIdx.y, r = blockIdx.x;
   const Request rq = request_of(p, b);
-  const int r = (int)blockIdx.x * 4 + (int)(threadIdx.x >> 6);
   if (r >= rq.ql * p.group) return;
   const int64_t n = p.T * p.heads * p.group;
   const int64_t at = (rq.token0 + r / p.group) * ((int64_t)p.heads * p.group) + h * p.group + r % p.group;
-  float m = -__builtin_inff();
-  for (int s = 0; s < p.splits; ++s) m = fmaxf(m, p.part_lse[s * n + at]);
+  const float x = lane < p.splits ? p.part_lse[lane * n + at] : -__builtin_inff();
+  float m = x;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+  const float w = x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x - m);
   float sum = 0.0f, acc[kPer] = {};
-  for (int s = 0; s < p.splits; ++s) {
-    const float x = p.part_lse[s * n + at];
-    if (x == -__builtin_inff()) continue;
-    const float w = __builtin_amdgcn_exp2f(x - m);
-    sum += w;
+  for (int s0 = wave; s0 < p.splits; s0 += 4 * kChunk) {
+    float v[kChunk][kPer], ws[kChunk];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      acc[i] = __builtin_fmaf(p.part_o[(s * n + at) * D + lane * kPer + i], w, acc[i]);
-  }
-  const bool none = sum == 0.0f;
+    for (int u = 0; u < kChunk; ++u) {
+      const int s = s0 + 4 * u < p.splits ? s0 + 4 * u : s0;
+      ws[u] = s0 + 4 * u < p.splits ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s)) : 0.0f;
+      const float *src = p.part_o + (s * n + at) * D + lane * kPer;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const float v = none ? 0.0f : acc[i] / sum;
-    reinterpret_cast<uint16_t *>(p.O)[at * D + lane * kPer + i] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
+      for (int i = 0; i < kPer; ++i) v[u][i] = src[i];
+    }
+#pragma unroll
+    for (int u = 0; u < kChunk; ++u) {
+      sum += ws[u];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = ws[u] != 0.0f ? __builtin_fmaf(v[u][i], ws[u], acc[i]) : acc[i];
+    }
   }
-  if (p.lse && lane == 0)
-    p.lse[at] = none ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) part[wave][lane * kPer + i] = acc[i];
+  if (lane == 0) part_sum[wave] = sum;
+  __syncthreads();
+  const float total = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+  const int d = threadIdx.x;
+  if (d < D) {
+    const float v = total == 0.0f ? 0.0f : ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) / total;
+    reinterpret_cast<uint16_t *>(p.O)[at * D + d] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
+  }
+  if (p.lse && d == 0)
+    p.lse[at] = total == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(total)) * 0.69314718055994531f;
 }
 
 // ---- plan and launch ------------------------------------------------------------------------------
@@ -860,6 +991,7 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
     const int64_t most = (span + 511) / 512;
     splits = splits < most ? splits : most;
   }
+  splits = splits < kMaxSplits ? splits : kMaxSplits;
   pl.splits = splits < 1 ? 1 : (int)splits;
   if (pl.splits > 1) {
     const int64_t n = T * heads * group;
@@ -882,7 +1014,7 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  kv_join_kernel<D, BF16><<<dim3((unsigned)((rows + 3) / 4), (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
+  kv_join_kernel<D, BF16><<<dim3((unsigned)rows, (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 }  // namespace

@@ -33,7 +33,7 @@ namespace awq {
 constexpr int kAssignThreads = 256;
 constexpr int kAssignPer = 4;                               // requests per thread and chunk
 constexpr int kAssignChunk = kAssignThreads * kAssignPer;
-constexpr int kAssignTokens = 1024;                         // slots per workgroup
+constexpr int kAssignTokens = 256;                          // slots per workgroup
 
 __device__ __forceinline__ int32_t saturate32(int64_t v) {
   return v > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)v;

@@ -147,6 +147,8 @@ def test_epilogue_refusals():
     fine = ctypes.byref(E(0x10000, 0x20000, 3))
     assert call(fine, K=200) == INVALID and call(fine, yt=9) == INVALID and call(fine, Y=None) == INVALID
     assert call(fine, M=17, kernel=1) == INVALID
+    assert call(ctypes.byref(E(addr(5).value + 16, None, 0))) == INVALID     # bias within Y
+    assert call(ctypes.byref(E(None, addr(5).value + 2, 0))) == INVALID      # residual across Y
     assert call(fine, M=0) == binding.AWQ_OK
 
 
@@ -224,7 +226,8 @@ def test_binding_refuses_wrong_epilogues():
     for kw, e in ((dict(activation="tanh"), ValueError), (dict(bias=h(17)), ValueError),
                   (dict(bias=h(16).float()), TypeError), (dict(bias=h(16, 1)), ValueError),
                   (dict(residual=h(3, 17)), ValueError), (dict(residual=h(3, 16).float()), TypeError),
-                  (dict(residual=h(48)), ValueError), (dict(workspace="x"), ValueError)):
+                  (dict(residual=h(48)), ValueError), (dict(workspace="x"), ValueError),
+                  (dict(out=h(3, 17)), ValueError), (dict(out_dtype=torch.int32), TypeError)):
         with pytest.raises(e):
             binding.awq_linear_epilogue(X, *w, **kw)
     with pytest.raises(ValueError, match="GPU"):
