@@ -585,20 +585,19 @@ void kv_decode_kernel(KvAttn p) {
 // operands.  32x32x16 MFMA, transposed as described above: lane (q = l & 31,
 // hh = l >> 5) holds keys 8g + 4hh + e of row q.
 //
+// A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
+//
 // LDS rows (a key's D channels, or a channel's 64 tokens) are split in
 // 16-byte chunks whose order is XORed with the row number, so that the 16
 // rows of an operand read fall on distinct banks.
-constexpr int kPtRows = 128, kPtKeys = 64, kPtThreads = 256;
+constexpr int kPtKeys = 64;
 
 template <int D>
 struct PromptSmem {
   uint16_t k[2][kPtKeys * D];
   uint16_t v[2][D * kPtKeys];
-  float a[2][kPtKeys];           // key step * scale * log2(e)
+  float ks[2][kPtKeys];          // key step
   float vs[2][kPtKeys];          // value step; -1: no such token
-  float vmax[2][4];              // per staging wave: the largest value step
-  uint32_t qmax[4];
-  uint32_t bad[2][4];            // per staging wave: some token of the tile has no page
 };
 
 // 16-byte chunk `chunk` of LDS row `row`, rows of kChunks chunks: byte offset
@@ -608,12 +607,10 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return (uint32_t)(row * kChunks + (chunk ^ sw)) * 16u;
 }
 
-template <int D, bool SYM, bool BF16>
-__global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
+template <int D, bool SYM, bool BF16, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
+  constexpr int kRows = 32 * NW;
   constexpr int kSteps = D / 16, kTiles = D / 32;
-  constexpr int kQuads = D / 32;                     // 16-byte pieces of a key's codes
-  constexpr int kWordsT = D / 8;                     // words of a token
-  constexpr bool kBoth = D == 128;                   // every thread stages a key and a value piece
   __shared__ __attribute__((aligned(16))) PromptSmem<D> sm;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -621,7 +618,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;     // longest rows first
   const int h = blockIdx.y % p.heads, split = blockIdx.y / p.heads, b = blockIdx.z;
   const Request rq = request_of(p, b);
-  const int rows = rq.ql * p.group, row0 = tile * kPtRows;
+  const int rows = rq.ql * p.group, row0 = tile * kRows;
   if (row0 >= rows) return;
   auto clamp_row = [&](int r) { return r < rows ? r : rows - 1; };
   const int wrow0 = clamp_row(row0 + wave * 32), wrow1 = clamp_row(row0 + wave * 32 + 31);
@@ -632,49 +629,64 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   const int w_any_last = last_key(p, rq, wrow1 / p.group);
   const int w_all_last = last_key(p, rq, wrow0 / p.group);
   const int w_any_first = first_key(p, w_all_last), w_all_first = first_key(p, w_any_last);
-  const int g_last = last_key(p, rq, clamp_row(row0 + kPtRows - 1) / p.group);
+  const int g_last = last_key(p, rq, clamp_row(row0 + kRows - 1) / p.group);
   const int g_first = first_key(p, last_key(p, rq, row0 / p.group));
   const int t_lo = g_first & ~(kPtKeys - 1);
   const int nt = g_last >= t_lo ? (g_last - t_lo) / kPtKeys + 1 : 0;
   const int i0 = (int)((int64_t)nt * split / p.splits), i1 = (int)((int64_t)nt * (split + 1) / p.splits);
 
-  // ---- staging: codes of one tile to registers, then as integers to LDS
-  const int kkey = tid / kQuads, kquad = tid % kQuads;       // D = 64: threads below 128
-  const int vtid = kBoth ? tid : tid - 128;
-  const int vblk = vtid / kWordsT, vword = vtid % kWordsT;   // four tokens, one word
-  const bool do_k = kBoth || wave < 2, do_v = kBoth || wave >= 2;
+  // ---- staging: codes of one tile to registers, then as integers to LDS.  The
+  // pieces (16 bytes of a key's codes; one word of four tokens' value codes)
+  // are dealt out by groups of 16 tokens, which lie in one page: with D = 128
+  // a wave (of the first four) takes a group's 64 pieces of either kind, with
+  // D = 64 lanes below 32 of it the keys' 32, the others the values'.
+  const bool stager = NW == 4 || wave < 4;
+  const bool do_k = D == 128 || hh == 0, do_v = D == 128 || hh == 1;
+  const int piece = D == 128 ? lane : qc;
+  const int kkey = 16 * (wave & 3) + piece / (D / 32), kquad = piece % (D / 32);
+  const int vblk = 4 * (wave & 3) + piece / (D / 8), vword = piece % (D / 8);
   const int pmask = (1 << p.pshift) - 1;
   const int64_t P = (int64_t)pmask + 1;
+  const int64_t code_stride = (int64_t)p.heads * P * D, meta_stride = (int64_t)p.heads * P * 2;
+  const char *codes = reinterpret_cast<const char *>(p.codes) + h * P * (D / 2);
+  const char *scales = reinterpret_cast<const char *>(p.scales) + h * P * 4;
+  const char *zeros = reinterpret_cast<const char *>(p.zeros) + h * P * 2;
+  const uint32_t k_lane = (piece / (D / 32)) * (D / 2) + kquad * 16;
+  const uint32_t v_lane = (piece / (D / 8)) * (2 * D) + vword * 16;
+  const uint32_t key_lane = piece / (D / 32), blk_lane = (piece / (D / 8)) * 8;
+  const int pages = p.pages < 0x7FFFFFFF ? (int)p.pages : 0x7FFFFFFF;
   const int32_t *table = p.table + (int64_t)b * p.max_blocks;
-  auto page_of = [&](int t) { return t < rq.kv ? table[t >> p.pshift] : -1; };
-  int32_t kpage = -1, vpage = -1;                            // of the tile to load next
+  int page_id = -1;                                          // of the tile to load next (uniform)
+  int page_left = 0;                                         // its tokens of this wave's group
   u32x4 kc = {}, vc = {};
   uint32_t ksc = 0, kzz = 0x0808u;
   u32x2 vzz = {0x08080808u, 0x08080808u};
-  bool kok = false;
-  auto load_pages = [&](int t0) {
-    if (do_k) kpage = page_of(t0 + kkey);
-    if (do_v) vpage = page_of(t0 + 4 * vblk);
+  int left = 0;                                              // tokens of the loaded group
+  auto load_page = [&](int t0) {
+    const int t = t0 + 16 * (wave & 3);
+    page_id = t < rq.kv ? table[t >> p.pshift] : -1;
+    page_left = rq.kv - t;
   };
   auto load_codes = [&](int t0) {
+    int id = __builtin_amdgcn_readfirstlane(page_id);
+    left = (uint32_t)id < (uint32_t)pages ? page_left : 0;
+    if ((uint32_t)id >= (uint32_t)pages) id = 0;
+    const int off = (t0 + 16 * (wave & 3)) & pmask;
+    const char *kp = codes + (id * code_stride + off * (D / 2));
+    const char *vp = kp + code_stride / 2;
+    const char *sp = scales + (id * meta_stride + off * 2) * 2;
+    const char *zp = zeros + (id * meta_stride + off * 2);
     if (do_k) {
-      kok = kpage >= 0 && kpage < p.pages;
-      const int64_t page = kok ? kpage : 0, off = (t0 + kkey) & pmask;
-      kc = *reinterpret_cast<const u32x4 *>(p.codes + ((page * 2 * p.heads + h) * P + off) * (D / 8) + kquad * 4);
-      const int64_t meta = ((page * p.heads + h) * P + off) * 2;
-      ksc = *reinterpret_cast<const uint32_t *>(p.scales + meta);
-      if constexpr (!SYM) kzz = *reinterpret_cast<const uint16_t *>(p.zeros + meta);
+      kc = *reinterpret_cast<const u32x4 *>(kp + k_lane);
+      ksc = *reinterpret_cast<const uint32_t *>(sp + key_lane * 4);
+      if constexpr (!SYM) kzz = *reinterpret_cast<const uint16_t *>(zp + key_lane * 2);
     }
     if (do_v) {
-      const int64_t page = vpage >= 0 && vpage < p.pages ? vpage : 0, off = (t0 + 4 * vblk) & pmask;
-      vc = *reinterpret_cast<const u32x4 *>(p.codes + ((page * 2 + 1) * p.heads + h) * P * (D / 8) +
-                                            (off >> 2) * (D / 2) + vword * 4);
-      if constexpr (!SYM)
-        vzz = *reinterpret_cast<const u32x2 *>(p.zeros + ((page * p.heads + h) * P + off) * 2);
+      vc = *reinterpret_cast<const u32x4 *>(vp + v_lane);
+      if constexpr (!SYM) vzz = *reinterpret_cast<const u32x2 *>(zp + blk_lane);
     }
   };
   const DeqRegs dq;
-  float cs = p.scale_log2;
   auto stage = [&](int buf) {
     if (do_k) {
       const DeqF16 deq(kzz & 0xFFu);
@@ -684,20 +696,13 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
         *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(sm.k[buf]) +
                                    chunk_at<D / 8>(kkey, kquad * 4 + j)) = deq(w, dq);
       }
-      float vstep = kok ? hi_half(ksc) : -1.0f;
       if (kquad == 0) {
-        sm.a[buf][kkey] = kok ? lo_half(ksc) * cs : 0.0f;
+        const bool held = (int)key_lane < left;
+        const float vstep = hi_half(ksc);
+        sm.ks[buf][kkey] = held ? lo_half(ksc) : 0.0f;
         // (an overflowed step as a finite one too large for fp16, so that the
         // zero weight of a row that does not see the key stays zero)
-        sm.vs[buf][kkey] = vstep <= 65504.0f ? vstep : 0x1p127f;
-      }
-      const uint64_t miss = __ballot(!kok);
-      if (!(vstep <= 65504.0f)) vstep = 0.0f;                // (one that overflowed counts for none)
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) vstep = fmaxf(vstep, __shfl_xor(vstep, d, 64));
-      if (lane == 0) {
-        sm.vmax[buf][wave] = vstep;
-        sm.bad[buf][wave] = miss != 0;
+        sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
       }
     }
     if (do_v) {
@@ -734,15 +739,9 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   u32x4 q[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
-  if constexpr (!kBoth) {
-    if (tid < 8) {                                           // waves that stage no keys
-      sm.vmax[tid >> 2][tid & 3] = -1.0f;
-      sm.bad[tid >> 2][tid & 3] = 0u;
-    }
-  }
+  float cs = __builtin_fabsf(p.scale_log2);
   if constexpr (BF16) {
-    // one factor for the workgroup's rows: it is part of the keys' steps in LDS
-    uint32_t m = 0;
+    uint32_t m = 0;                                          // one factor for the wave's rows
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const uint32_t x = bf16_magnitude8(q[s]);
@@ -753,56 +752,89 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
       const uint32_t x = (uint32_t)__shfl_xor((int)m, d, 64);
       m = m > x ? m : x;
     }
-    if (lane == 0) sm.qmax[wave] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) m = m > sm.qmax[w] ? m : sm.qmax[w];
     const float f = half_range_factor(m);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = bf16_to_half8(q[s], f);
     cs *= 1.0f / f;
   }
-  if constexpr (!kBoth) __syncthreads();
+  cs = positive_scale(cs);
+  if (p.scale_log2 < 0.0f) {
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[s][i] ^= 0x80008000u;
+  }
 
   f32x16 o[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
-  float M = kNone, top = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f;
+  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f;
+  const float slack_width = kSlack / cs;
 
+  // The order of a tile's instructions is spelled out for the scheduler: left
+  // to itself it keeps one operand register and waits out the LDS latency
+  // before every MFMA (915 us on 8192 tokens of 32 heads over 8, D = 128).
+  constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100;
   auto compute = [&](int buf, int t0) {
     const char *kl = reinterpret_cast<const char *>(sm.k[buf]);
     const char *vl = reinterpret_cast<const char *>(sm.v[buf]);
-    float u[32];
     // the four keys 32i + 8g + 4hh + e of result group g
     auto per_key = [&](const float *x, int i, int g) {
       return *reinterpret_cast<const f32x4 *>(x + 32 * i + 8 * g + 4 * hh);
     };
+    auto key_frag = [&](int i, int st) {
+      return *reinterpret_cast<const u32x4 *>(kl + chunk_at<D / 8>(32 * i + qc, 2 * st + hh));
+    };
+    auto value_frag = [&](int s, int n) {
+      return *reinterpret_cast<const u32x4 *>(vl + chunk_at<kPtKeys / 8>(32 * n + qc, 2 * s + hh));
+    };
+    const float vstep = sm.vs[buf][lane];                    // (of the tile's key `lane`)
+    f32x16 s[2];
+    u32x4 kf[kSteps];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      f32x16 s;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = 0.0f;
+      for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
 #pragma unroll
-      for (int st = 0; st < kSteps; ++st)
-        s = mfma32x16(*reinterpret_cast<const u32x4 *>(kl + chunk_at<D / 8>(32 * i + qc, 2 * st + hh)),
-                      q[st], s);
+    for (int st = 0; st < kSteps; ++st) kf[st] = key_frag(0, st);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      s[0] = mfma32x16(kf[st], q[st], s[0]);
+      kf[st] = key_frag(1, st);
+    }
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    float u[32];
+    auto scaled = [&](int i) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const f32x4 a = per_key(sm.a[buf], i, g);
+        const f32x4 a = per_key(sm.ks[buf], i, g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) u[16 * i + 4 * g + e] = s[4 * g + e] * a[e];
+        for (int e = 0; e < 4; ++e) u[16 * i + 4 * g + e] = s[i][4 * g + e] * a[e];
       }
-    }
-    float vmax = sm.vmax[buf][0];
-    uint32_t bad = sm.bad[buf][0];
+    };
 #pragma unroll
-    for (int w = 1; w < 4; ++w) {
-      vmax = fmaxf(vmax, sm.vmax[buf][w]);
-      bad |= sm.bad[buf][w];
+    for (int st = 0; st < kSteps; ++st) s[1] = mfma32x16(kf[st], q[st], s[1]);
+    scaled(0);
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 4, 0);
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kValu, 16 / kSteps, 0);
     }
-    if (__any(bad != 0) || t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last) {
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4 vf[2][kTiles];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) vf[0][n] = value_frag(0, n);
+    scaled(1);
+    if (t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last || __any(vstep < 0.0f)) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
@@ -817,15 +849,20 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     float umax = u[0];
 #pragma unroll
     for (int j = 1; j < 32; ++j) umax = fmaxf(umax, u[j]);
-    if (__any(umax > top + kSlack || vmax > vlim)) {
+    if (__any(umax > slack || vstep > vlim)) {
       umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
       top = fmaxf(top, umax);
+      slack = top + slack_width;
+      // (a step that overflowed counts for none)
+      float vmax = vstep <= 65504.0f ? vstep : 0.0f;
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
       if (vmax > vlim) {
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         vexp = (float)ex;
         vlim = __builtin_ldexpf(1.0f, ex);
       }
-      const float m2 = top + vexp, a = __builtin_amdgcn_exp2f(M - m2);
+      const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
       l *= a;
 #pragma unroll
@@ -833,40 +870,64 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[n][e] *= a;
     }
-    u32x4 pb[4];
+    // weights of 16 keys, then their products, with the next 16's weights and
+    // operands under way between the MFMAs
+    auto weights = [&](int st) {
+      u32x4 pb;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
-      float pr[4];
+      for (int g = 0; g < 2; ++g) {
+        const f32x4 v = per_key(sm.vs[buf], st >> 1, 2 * (st & 1) + g);
+        float pr[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = __builtin_amdgcn_exp2f(u[4 * j + e] - M);
-        l += x;
-        pr[e] = x * v[e];
+        for (int e = 0; e < 4; ++e) {
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(u[8 * st + 4 * g + e], cs, -M));
+          l += x;
+          pr[e] = x * v[e];
+        }
+        pb[2 * g] = pack_half2(pr[0], pr[1]);
+        pb[2 * g + 1] = pack_half2(pr[2], pr[3]);
       }
-      pb[j >> 1][2 * (j & 1)] = pack_half2(pr[0], pr[1]);
-      pb[j >> 1][2 * (j & 1) + 1] = pack_half2(pr[2], pr[3]);
+      return pb;
+    };
+    u32x4 pb = weights(0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int st = 0; st < 4; ++st) {
+      u32x4 next = pb;
+      if (st < 3) {
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) vf[(st + 1) & 1][n] = value_frag(st + 1, n);
+        next = weights(st + 1);
+      }
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) o[n] = mfma32x16(vf[st & 1][n], pb, o[n]);
+      if (st < 3) {
+        __builtin_amdgcn_sched_group_barrier(kLdsRead, kTiles + 2, 0);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+          __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(kValu, (36 + kTiles - 1) / kTiles, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      pb = next;
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-        o[n] = mfma32x16(*reinterpret_cast<const u32x4 *>(vl + chunk_at<kPtKeys / 8>(32 * n + qc, 2 * s + hh)),
-                         pb[s], o[n]);
   };
 
   if (i0 < i1) {
-    load_pages(t_lo + kPtKeys * i0);
-    load_codes(t_lo + kPtKeys * i0);
-    load_pages(t_lo + kPtKeys * (i0 + 1));
-    stage(0);
+    if (stager) {
+      load_page(t_lo + kPtKeys * i0);
+      load_codes(t_lo + kPtKeys * i0);
+      load_page(t_lo + kPtKeys * (i0 + 1));
+      stage(0);
+    }
     __syncthreads();
     for (int i = i0; i < i1; ++i) {
       const int t0 = t_lo + kPtKeys * i, buf = (i - i0) & 1;
-      const bool more = i + 1 < i1;
+      const bool more = i + 1 < i1 && stager;
       if (more) {
         load_codes(t0 + kPtKeys);
-        load_pages(t0 + 2 * kPtKeys);
+        load_page(t0 + 2 * kPtKeys);
       }
       if (wave_live && t0 <= w_any_last && t0 + kPtKeys > w_any_first) compute(buf, t0);
       if (more) stage(buf ^ 1);
@@ -969,6 +1030,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
 
 // ---- plan and launch ------------------------------------------------------------------------------
 constexpr int kDecodeWaves = 4;
+constexpr int kPtWaves = 4, kPtRows = 32 * kPtWaves;
 
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
                              int window) {
@@ -1007,7 +1069,7 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   const int64_t rows = (int64_t)p.max_q * p.group;
   if (pl.prompt) {
     const dim3 grid((unsigned)((rows + kPtRows - 1) / kPtRows), (unsigned)(p.heads * p.splits), (unsigned)B);
-    kv_prompt_kernel<D, SYM, BF16><<<grid, kPtThreads, 0, st>>>(p);
+    kv_prompt_kernel<D, SYM, BF16, kPtWaves><<<grid, 64 * kPtWaves, 0, st>>>(p);
   } else {
     const dim3 grid((unsigned)((rows + 15) / 16 * p.heads), (unsigned)p.splits, (unsigned)B);
     kv_decode_kernel<D, SYM, BF16, kDecodeWaves><<<grid, 64 * kDecodeWaves, 0, st>>>(p);
