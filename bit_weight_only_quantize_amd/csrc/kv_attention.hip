@@ -586,32 +586,27 @@ void kv_decode_kernel(KvAttn p) {
 // hh = l >> 5) holds keys 8g + 4hh + e of row q.
 //
 // A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
-//
-// LDS rows (a key's D channels, or a channel's 64 tokens) are split in
-// 16-byte chunks whose order is XORed with the row number, so that the 16
-// rows of an operand read fall on distinct banks.
-constexpr int kPtKeys = 64;
+constexpr int kPtKeys = 64, kPtRows = 128, kPtThreads = 256;
 
+// LDS rows end in 16 spare bytes, which puts the 16 rows of an operand read on
+// distinct banks with the operand's place in the row as the instruction's
+// offset (an XOR swizzle needs a register per place).
 template <int D>
 struct PromptSmem {
-  uint16_t k[2][kPtKeys * D];
-  uint16_t v[2][D * kPtKeys];
-  float ks[2][kPtKeys];          // key step
+  static constexpr int kKeyRow = 2 * D + 16, kValueRow = 2 * kPtKeys + 16;   // bytes
+  char k[2][kPtKeys * kKeyRow];
+  char v[2][D * kValueRow];      // row ch * D/8 + word: channel 8 word + ch
+  float ks[2][kPtKeys];          // key step * scale * log2(e)
   float vs[2][kPtKeys];          // value step; -1: no such token
+  uint32_t qmax[4];
 };
 
-// 16-byte chunk `chunk` of LDS row `row`, rows of kChunks chunks: byte offset
-template <int kChunks>
-__device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
-  const int sw = kChunks == 16 ? (row & 15) : ((row & 7) ^ ((row >> 3) & 7));
-  return (uint32_t)(row * kChunks + (chunk ^ sw)) * 16u;
-}
-
-template <int D, bool SYM, bool BF16, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
-  constexpr int kRows = 32 * NW;
+template <int D, bool SYM, bool BF16>
+__global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
+  constexpr int kRows = kPtRows;
+  using Smem = PromptSmem<D>;
   constexpr int kSteps = D / 16, kTiles = D / 32;
-  __shared__ __attribute__((aligned(16))) PromptSmem<D> sm;
+  __shared__ __attribute__((aligned(16))) Smem sm;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qc = lane & 31, hh = lane >> 5;
@@ -638,13 +633,12 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
   // ---- staging: codes of one tile to registers, then as integers to LDS.  The
   // pieces (16 bytes of a key's codes; one word of four tokens' value codes)
   // are dealt out by groups of 16 tokens, which lie in one page: with D = 128
-  // a wave (of the first four) takes a group's 64 pieces of either kind, with
+  // a wave takes a group's 64 pieces of either kind, with
   // D = 64 lanes below 32 of it the keys' 32, the others the values'.
-  const bool stager = NW == 4 || wave < 4;
   const bool do_k = D == 128 || hh == 0, do_v = D == 128 || hh == 1;
   const int piece = D == 128 ? lane : qc;
-  const int kkey = 16 * (wave & 3) + piece / (D / 32), kquad = piece % (D / 32);
-  const int vblk = 4 * (wave & 3) + piece / (D / 8), vword = piece % (D / 8);
+  const int kkey = 16 * wave + piece / (D / 32), kquad = piece % (D / 32);
+  const int vblk = 4 * wave + piece / (D / 8), vword = piece % (D / 8);
   const int pmask = (1 << p.pshift) - 1;
   const int64_t P = (int64_t)pmask + 1;
   const int64_t code_stride = (int64_t)p.heads * P * D, meta_stride = (int64_t)p.heads * P * 2;
@@ -663,7 +657,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
   u32x2 vzz = {0x08080808u, 0x08080808u};
   int left = 0;                                              // tokens of the loaded group
   auto load_page = [&](int t0) {
-    const int t = t0 + 16 * (wave & 3);
+    const int t = t0 + 16 * wave;
     page_id = t < rq.kv ? table[t >> p.pshift] : -1;
     page_left = rq.kv - t;
   };
@@ -671,7 +665,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
     int id = __builtin_amdgcn_readfirstlane(page_id);
     left = (uint32_t)id < (uint32_t)pages ? page_left : 0;
     if ((uint32_t)id >= (uint32_t)pages) id = 0;
-    const int off = (t0 + 16 * (wave & 3)) & pmask;
+    const int off = (t0 + 16 * wave) & pmask;
     const char *kp = codes + (id * code_stride + off * (D / 2));
     const char *vp = kp + code_stride / 2;
     const char *sp = scales + (id * meta_stride + off * 2) * 2;
@@ -687,19 +681,19 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
     }
   };
   const DeqRegs dq;
+  float cs = __builtin_fabsf(p.scale_log2);
   auto stage = [&](int buf) {
     if (do_k) {
       const DeqF16 deq(kzz & 0xFFu);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t w = kc[j];
-        *reinterpret_cast<u32x4 *>(reinterpret_cast<char *>(sm.k[buf]) +
-                                   chunk_at<D / 8>(kkey, kquad * 4 + j)) = deq(w, dq);
+        *reinterpret_cast<u32x4 *>(sm.k[buf] + kkey * Smem::kKeyRow + kquad * 64 + 16 * j) = deq(w, dq);
       }
       if (kquad == 0) {
         const bool held = (int)key_lane < left;
         const float vstep = hi_half(ksc);
-        sm.ks[buf][kkey] = held ? lo_half(ksc) : 0.0f;
+        sm.ks[buf][kkey] = held ? lo_half(ksc) * cs : 0.0f;
         // (an overflowed step as a finite one too large for fp16, so that the
         // zero weight of a row that does not see the key stays zero)
         sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
@@ -716,9 +710,8 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
       // tokens 16s + 8x + 4y + e sit at position 16s + 8y + 4x + e of the row
       const int chunk = (vblk >> 2) * 2 + (vblk & 1), half = (vblk >> 1) & 1;
       auto put = [&](int ch, uint32_t x0, uint32_t x1) {
-        const int d = 8 * vword + ch;
-        *reinterpret_cast<u32x2 *>(reinterpret_cast<char *>(sm.v[buf]) +
-                                   chunk_at<kPtKeys / 8>(d, chunk) + 8 * half) = u32x2{x0, x1};
+        *reinterpret_cast<u32x2 *>(sm.v[buf] + vword * Smem::kValueRow + chunk * 16 + 8 * half +
+                                   ch * (D / 8) * Smem::kValueRow) = u32x2{x0, x1};
       };
       auto bytes = [&](auto tag, int lo_ch, int hi_ch) {
         constexpr int kB = decltype(tag)::value;
@@ -739,9 +732,8 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
   u32x4 q[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
-  float cs = __builtin_fabsf(p.scale_log2);
   if constexpr (BF16) {
-    uint32_t m = 0;                                          // one factor for the wave's rows
+    uint32_t m = 0;                                          // one factor: it is part of the keys' steps in LDS
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const uint32_t x = bf16_magnitude8(q[s]);
@@ -752,6 +744,10 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
       const uint32_t x = (uint32_t)__shfl_xor((int)m, d, 64);
       m = m > x ? m : x;
     }
+    if (lane == 0) sm.qmax[wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = m > sm.qmax[w] ? m : sm.qmax[w];
     const float f = half_range_factor(m);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = bf16_to_half8(q[s], f);
@@ -771,24 +767,23 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
   float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f;
-  const float slack_width = kSlack / cs;
 
   // The order of a tile's instructions is spelled out for the scheduler: left
   // to itself it keeps one operand register and waits out the LDS latency
   // before every MFMA (915 us on 8192 tokens of 32 heads over 8, D = 128).
   constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100;
   auto compute = [&](int buf, int t0) {
-    const char *kl = reinterpret_cast<const char *>(sm.k[buf]);
-    const char *vl = reinterpret_cast<const char *>(sm.v[buf]);
+    const char *kl = sm.k[buf] + qc * Smem::kKeyRow + 16 * hh;
+    const char *vl = sm.v[buf] + qc * Smem::kValueRow + 16 * hh;
     // the four keys 32i + 8g + 4hh + e of result group g
     auto per_key = [&](const float *x, int i, int g) {
       return *reinterpret_cast<const f32x4 *>(x + 32 * i + 8 * g + 4 * hh);
     };
     auto key_frag = [&](int i, int st) {
-      return *reinterpret_cast<const u32x4 *>(kl + chunk_at<D / 8>(32 * i + qc, 2 * st + hh));
+      return *reinterpret_cast<const u32x4 *>(kl + 32 * i * Smem::kKeyRow + 32 * st);
     };
     auto value_frag = [&](int s, int n) {
-      return *reinterpret_cast<const u32x4 *>(vl + chunk_at<kPtKeys / 8>(32 * n + qc, 2 * s + hh));
+      return *reinterpret_cast<const u32x4 *>(vl + 32 * n * Smem::kValueRow + 32 * s);
     };
     const float vstep = sm.vs[buf][lane];                    // (of the tile's key `lane`)
     f32x16 s[2];
@@ -852,7 +847,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
     if (__any(umax > slack || vstep > vlim)) {
       umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
       top = fmaxf(top, umax);
-      slack = top + slack_width;
+      slack = top + kSlack;
       // (a step that overflowed counts for none)
       float vmax = vstep <= 65504.0f ? vstep : 0.0f;
 #pragma unroll
@@ -862,7 +857,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
         vexp = (float)ex;
         vlim = __builtin_ldexpf(1.0f, ex);
       }
-      const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
+      const float m2 = running_max(top, 1.0f, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
       l *= a;
 #pragma unroll
@@ -880,7 +875,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
         float pr[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(u[8 * st + 4 * g + e], cs, -M));
+          const float x = __builtin_amdgcn_exp2f(u[8 * st + 4 * g + e] - M);
           l += x;
           pr[e] = x * v[e];
         }
@@ -915,16 +910,14 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
   };
 
   if (i0 < i1) {
-    if (stager) {
-      load_page(t_lo + kPtKeys * i0);
-      load_codes(t_lo + kPtKeys * i0);
-      load_page(t_lo + kPtKeys * (i0 + 1));
-      stage(0);
-    }
+    load_page(t_lo + kPtKeys * i0);
+    load_codes(t_lo + kPtKeys * i0);
+    load_page(t_lo + kPtKeys * (i0 + 1));
+    stage(0);
     __syncthreads();
     for (int i = i0; i < i1; ++i) {
       const int t0 = t_lo + kPtKeys * i, buf = (i - i0) & 1;
-      const bool more = i + 1 < i1 && stager;
+      const bool more = i + 1 < i1;
       if (more) {
         load_codes(t0 + kPtKeys);
         load_page(t0 + 2 * kPtKeys);
@@ -935,7 +928,8 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
     }
   }
 
-  // ---- store: lane (q, hh) holds channels 32n + 8g + 4hh + e of row q
+  // ---- store: lane (q, hh) holds LDS rows 32n + 8g + 4hh + e of row q, all
+  // eight channels of D/16 of its words
   l += __shfl_xor(l, 32, 64);
   if (row0 + wave * 32 + qc >= rows) return;
   const bool none = l == 0.0f;
@@ -950,24 +944,29 @@ __global__ __launch_bounds__(64 * NW, 2) void kv_prompt_kernel(KvAttn p) {
     p.lse[at] = lse2 * 0.69314718055994531f;
   }
 #pragma unroll
-  for (int n = 0; n < kTiles; ++n)
+  for (int x = 0; x < D / 16; ++x) {
+    const int word = D == 128 ? 8 * (x >> 2) + 4 * hh + (x & 3) : 4 * hh + x;
+    float v[8];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = none ? 0.0f : o[n][4 * g + e] * inv;
-      const int64_t d = at * D + 32 * n + 8 * g + 4 * hh;
-      if (p.splits > 1) {
-        *reinterpret_cast<float4 *>(p.part_o + d) = float4{v[0], v[1], v[2], v[3]};
-      } else {
-        u32x2 w;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          w[i] = BF16 ? (uint32_t)float_to_bf16_bits(v[2 * i]) | ((uint32_t)float_to_bf16_bits(v[2 * i + 1]) << 16)
-                      : pack_half2(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<u32x2 *>(reinterpret_cast<uint16_t *>(p.O) + d) = w;
-      }
+    for (int ch = 0; ch < 8; ++ch) {
+      const int n = D == 128 ? ch >> 1 : ch >> 2;
+      const int g = D == 128 ? 2 * (ch & 1) + (x >> 2) : ch & 3;
+      v[ch] = none ? 0.0f : o[n][4 * g + (x & 3)] * inv;
     }
+    const int64_t d = at * D + 8 * word;
+    if (p.splits > 1) {
+      float4 *po = reinterpret_cast<float4 *>(p.part_o + d);
+      po[0] = float4{v[0], v[1], v[2], v[3]};
+      po[1] = float4{v[4], v[5], v[6], v[7]};
+    } else {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = BF16 ? (uint32_t)float_to_bf16_bits(v[2 * i]) | ((uint32_t)float_to_bf16_bits(v[2 * i + 1]) << 16)
+                    : pack_half2(v[2 * i], v[2 * i + 1]);
+      *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(p.O) + d) = w;
+    }
+  }
 }
 
 // ---- join the splits ---------------------------------------------------------------------------
@@ -1030,7 +1029,6 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
 
 // ---- plan and launch ------------------------------------------------------------------------------
 constexpr int kDecodeWaves = 4;
-constexpr int kPtWaves = 4, kPtRows = 32 * kPtWaves;
 
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
                              int window) {
@@ -1069,7 +1067,7 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   const int64_t rows = (int64_t)p.max_q * p.group;
   if (pl.prompt) {
     const dim3 grid((unsigned)((rows + kPtRows - 1) / kPtRows), (unsigned)(p.heads * p.splits), (unsigned)B);
-    kv_prompt_kernel<D, SYM, BF16, kPtWaves><<<grid, 64 * kPtWaves, 0, st>>>(p);
+    kv_prompt_kernel<D, SYM, BF16><<<grid, kPtThreads, 0, st>>>(p);
   } else {
     const dim3 grid((unsigned)((rows + 15) / 16 * p.heads), (unsigned)p.splits, (unsigned)B);
     kv_decode_kernel<D, SYM, BF16, kDecodeWaves><<<grid, 64 * kDecodeWaves, 0, st>>>(p);
