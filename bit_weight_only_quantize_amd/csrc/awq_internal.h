@@ -200,7 +200,7 @@ hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int64_t T, v
                             YType ot, hipStream_t st);
 
 // ---- kv_attention.hip -------------------------------------------------------------
-// Arguments of one attention call (the last three are the launcher's).
+// Arguments of one attention call (from `splits` on the launcher's).
 struct KvAttn {
   const uint16_t *Q;
   int64_t q_stride;           // elements between query tokens
@@ -216,13 +216,15 @@ struct KvAttn {
   const int32_t *seq_lens, *query_start;
   int max_q, causal, window;
   float scale_log2;           // softmax scale * log2(e)
-  int splits;
+  int splits, chunk;          // at most this many parts of a row's keys, of this length
+  int tile_rows;              // rows that share their parts
   float *part_o, *part_lse;   // [splits][T * heads * group][D] and [splits][T * heads * group]
 };
-// Kernel, number of parts of the keys, and workspace of a call.
+// Kernel, its tile of rows, waves (decode) and parts of the keys, and the
+// workspace of a call.
 struct KvAttnPlan {
   bool prompt;
-  int splits;
+  int tile_rows, waves, chunk, splits;
   size_t lse_offset, workspace_bytes;   // 0 when splits == 1
 };
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,

@@ -91,6 +91,19 @@ __device__ __forceinline__ uint32_t finite_magnitude(float x) {
   return b < 0x7F800000u ? b : 0u;
 }
 
+// Largest finite magnitude of eight fp16 values, as fp32 bits.
+__device__ __forceinline__ uint32_t half_magnitude8(u32x4 raw) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t r = raw[i];
+    const uint32_t a = finite_magnitude(lo_half(r)), b = finite_magnitude(hi_half(r));
+    m = m > a ? m : a;
+    m = m > b ? m : b;
+  }
+  return m;
+}
+
 // Eight bfloat16 values as fp16 after multiplication by f.
 __device__ __forceinline__ u32x4 bf16_to_half8(u32x4 raw, float f) {
   u32x4 out;
@@ -157,6 +170,25 @@ __device__ __forceinline__ int first_key(const KvAttn &p, int last) {
   return f > 0 ? f : 0;
 }
 
+// The keys of a tile of rows row0 .. row1, from `lo` (a multiple of `align`) to
+// `end`, and how they are cut: into equal parts of `each` (a multiple of 64), as
+// many as keep p.chunk keys each but at most p.splits.  Short requests of a
+// batch thus take fewer parts, and a row with one part needs no join.
+struct Keys {
+  int lo, end, parts, each;
+};
+__device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int row0, int row1, int align) {
+  Keys k;
+  k.lo = first_key(p, last_key(p, r, row0 / p.group)) & -align;
+  k.end = last_key(p, r, row1 / p.group) + 1;
+  const int n = k.end > k.lo ? k.end - k.lo : 1;
+  const int most = (n - 1) / p.chunk + 1;
+  const int want = most < p.splits ? most : p.splits;
+  k.each = ((n - 1) / want + 64) & -64;
+  k.parts = (n - 1) / k.each + 1;
+  return k;
+}
+
 // ---- few query rows: the decode kernel ------------------------------------------------------
 // Bound by reading the cache: D/2 bytes of key and of value codes and 4 to 6
 // bytes of steps and zero points per token and key/value head.  A workgroup
@@ -212,66 +244,64 @@ void kv_decode_kernel(KvAttn p) {
   const int row = row0 + c < rows ? row0 + c : rows - 1;
   const int qi = row / p.group;
   const int my_last = last_key(p, rq, qi), my_first = first_key(p, my_last);
-  // keys that any row sees, and keys that all rows see
-  const int any_last = last_key(p, rq, row_last / p.group);
+  // keys that all rows see
   const int all_last = last_key(p, rq, row0 / p.group);
-  const int any_first = first_key(p, all_last), all_first = first_key(p, any_last);
-  const int t_lo = any_first & ~31;
-  const int nt = any_last >= t_lo ? (any_last - t_lo) / 32 + 1 : 0;
-  const int64_t parts = (int64_t)p.splits * NW, part = (int64_t)split * NW + wave;
-  const int i0 = (int)((int64_t)nt * part / parts), i1 = (int)((int64_t)nt * (part + 1) / parts);
+  const int all_first = first_key(p, last_key(p, rq, row_last / p.group));
+  const Keys keys = keys_of(p, rq, row0, row_last, 32);
+  if (split >= keys.parts) return;
+  const int t_lo = keys.lo + split * keys.each;
+  const int t_hi = split + 1 < keys.parts ? t_lo + keys.each : keys.end;
+  const int nt = t_hi > t_lo ? (t_hi - t_lo + 31) / 32 : 0;
+  const int i0 = nt * wave / NW, i1 = nt * (wave + 1) / NW;
 
   // queries: lane (c, kq) holds channels 32kq.. (D = 128) or 16kq.. (D = 64)
-  // of row c, the channels of the key words that it will load; negated for a
-  // negative scale, so that larger sums are larger logits
+  // of row c, the channels of the key words that it will load
   const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
                        (int64_t)(h * p.group + row % p.group) * D + kq * (8 * kWords);
   u32x4 q[kWords];
 #pragma unroll
   for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
-  float cs = __builtin_fabsf(p.scale_log2);
-  if constexpr (BF16) {
-    uint32_t m = 0;
+  // The key operand is the nibble pair as it lies in the word, a subnormal fp16:
+  // code * 2^-24 for channels 0, 1, 4, 5 of a word, 16 times that for the others
+  // (the MFMA takes subnormals exactly).  The queries make up for it: scaled by a
+  // power of two into [2^14, 2^15) at most, those of the other channels by a
+  // sixteenth of it.  (Values below 2^-24 of the tile's largest lose bits.)
+  uint32_t qmax = 0;
 #pragma unroll
-    for (int j = 0; j < kWords; ++j) {
-      const uint32_t a = bf16_magnitude8(q[j]);
-      m = m > a ? m : a;
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const uint32_t o = (uint32_t)__shfl_xor((int)m, d, 64);
-      m = m > o ? m : o;
-    }
-    const float f = half_range_factor(m);
-#pragma unroll
-    for (int j = 0; j < kWords; ++j) q[j] = bf16_to_half8(q[j], f);
-    cs *= 1.0f / f;
+  for (int j = 0; j < kWords; ++j) {
+    const uint32_t x = BF16 ? bf16_magnitude8(q[j]) : half_magnitude8(q[j]);
+    qmax = qmax > x ? qmax : x;
   }
-  cs = positive_scale(cs);
-  if (p.scale_log2 < 0.0f) {
 #pragma unroll
-    for (int j = 0; j < kWords; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[j][i] ^= 0x80008000u;
+  for (int d = 32; d > 0; d >>= 1) {
+    const uint32_t x = (uint32_t)__shfl_xor((int)qmax, d, 64);
+    qmax = qmax > x ? qmax : x;
   }
+  const float f = half_range_factor(qmax);
+  // (negated for a negative scale, so that larger sums are larger logits)
+  const float fs = p.scale_log2 < 0.0f ? -f : f;
+  const float cs = positive_scale(__builtin_fabsf(p.scale_log2) * (1.0f / f) * 0x1p24f);
+  // sum of the row's queries, for the zero points: sum q (code - z) = sum q code - z sum q
+  float qsum = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kWords; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = q[j][i];
+      const float g = i & 1 ? fs * 0x1p-4f : fs;
+      const uint32_t x = BF16 ? pack_half2(__builtin_bit_cast(float, w << 16) * g,
+                                           __builtin_bit_cast(float, w & 0xFFFF0000u) * g)
+                              : pack_half2(lo_half(w) * g, hi_half(w) * g);
+      q[j][i] = x;
+      qsum += (lo_half(x) + hi_half(x)) * (i & 1 ? 0x1p-20f : 0x1p-24f);
+    }
+  qsum += __shfl_xor(qsum, 16, 64);
+  qsum += __shfl_xor(qsum, 32, 64);
   // (every wave has the same 16 rows; in registers they would cost the loop 16
   // of them, and with those a wave per SIMD)
   if (wave == 0) {
 #pragma unroll
     for (int j = 0; j < kWords; ++j) sq[j][lane] = q[j];
-  }
-  // sum of the row's queries, for the zero points: sum q (code - z) = sum q code - z sum q
-  float qsum = 0.0f;
-  if constexpr (!SYM) {
-#pragma unroll
-    for (int j = 0; j < kWords; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t w = q[j][i];
-        qsum += lo_half(w) + hi_half(w);
-      }
-    qsum += __shfl_xor(qsum, 16, 64);
-    qsum += __shfl_xor(qsum, 32, 64);
   }
 
   const int pmask = (1 << p.pshift) - 1;
@@ -354,8 +384,8 @@ void kv_decode_kernel(KvAttn p) {
   // M = top * cs + vexp, top the largest sum so far (times the key's step), 2^vexp = vlim
   float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f, pz = 0.0f;
   const float slack_width = kSlack / cs;
-  const DeqRegs dq;
-  const DeqF16 deq8(8u), deqk(SYM ? 8u : 0u);
+  // The nibble pairs of word w (of shifted words, the next two): subnormal fp16
+  constexpr uint32_t kLoNibbles = 0x000F000Fu, kHiNibbles = 0x00F000F0u;
   // D = 64 has 8 words per token but an MFMA operand 16 rows: lanes c and
   // c + 8 take the same word, the first its even channels (bytes 0, 1), the
   // second its odd ones (bytes 2, 3)
@@ -368,10 +398,14 @@ void kv_decode_kernel(KvAttn p) {
     f32x4 s[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      const float s0 = SYM ? -8.0f * qsum : 0.0f;    // without zeros every zero is 8
+      s[i] = f32x4{s0, s0, s0, s0};
 #pragma unroll
-      for (int j = 0; j < kWords; ++j)
-        s[i] = mfma32<TagF16>(deqk(T.k[i][j], dq), sq[j][lane], s[i]);
+      for (int j = 0; j < kWords; ++j) {
+        const uint32_t w = T.k[i][j], w8 = w >> 8;
+        s[i] = mfma32<TagF16>(u32x4{w & kLoNibbles, w & kHiNibbles, w8 & kLoNibbles, w8 & kHiNibbles},
+                              sq[j][lane], s[i]);
+      }
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (kMore) {
@@ -449,13 +483,22 @@ void kv_decode_kernel(KvAttn p) {
         l += x;
         const uint32_t w = T.sc[i][e];
         pr[e] = mul_hi_half(x, w);
-        if constexpr (!SYM) {
-          const uint32_t zz = T.z[i][e >> 1];
-          pz = __builtin_fmaf(pr[e], (float)((zz >> (16 * (e & 1) + 8)) & 0xFFu) - 8.0f, pz);
-        }
       }
       pb[2 * i] = pack_half2(pr[0], pr[1]);
       pb[2 * i + 1] = pack_half2(pr[2], pr[3]);
+      // the zero points' share, sum P' z, with the weights as they are rounded:
+      // sum P' code - sum P' z then has the rounding of sum P' (code - z)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const uint32_t w = pb[2 * i + g];
+        if constexpr (SYM) {
+          pz = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, w), f16x2{(_Float16)8.0f, (_Float16)8.0f}, pz, false);
+        } else {
+          const uint32_t zz = T.z[i][g];
+          pz = __builtin_fmaf(lo_half(w), (float)((zz >> 8) & 0xFFu), pz);
+          pz = __builtin_fmaf(hi_half(w), (float)(zz >> 24), pz);
+        }
+      }
     }
     if constexpr (kMore) {
       __builtin_amdgcn_sched_barrier(0);
@@ -463,7 +506,7 @@ void kv_decode_kernel(KvAttn p) {
       __builtin_amdgcn_sched_barrier(0);
     }
     // value operands: byte b of the words of tokens (2j, 2j+1) in the halves
-    // of a word, then each nibble as an exact code - 8
+    // of a word, then each nibble, again as subnormals
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -474,8 +517,8 @@ void kv_decode_kernel(KvAttn p) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t x = byte_of(w[2 * j], w[2 * j + 1]);
-        lo[j] = add_half2((x & dq.lo) | dq.e1024, deq8.nz1024);
-        hi[j] = add_half2((x & dq.hi) | dq.e64, deq8.nz64);
+        lo[j] = x & kLoNibbles;
+        hi[j] = x & kHiNibbles;
       }
       o[n] = mfma32<TagF16>(lo, pb, o[n]);
       o[n + 1] = mfma32<TagF16>(hi, pb, o[n + 1]);
@@ -516,10 +559,8 @@ void kv_decode_kernel(KvAttn p) {
   // ---- join the waves --------------------------------------------------------------
   l += __shfl_xor(l, 16, 64);
   l += __shfl_xor(l, 32, 64);
-  if constexpr (!SYM) {
-    pz += __shfl_xor(pz, 16, 64);
-    pz += __shfl_xor(pz, 32, 64);
-  }
+  pz += __shfl_xor(pz, 16, 64);
+  pz += __shfl_xor(pz, 32, 64);
   // channel of MFMA tile n, result row 4kq + e (see the operand layouts above)
   constexpr int kOrder[8] = {0, 2, 4, 6, 1, 3, 5, 7};
 #pragma unroll
@@ -528,7 +569,7 @@ void kv_decode_kernel(KvAttn p) {
     for (int e = 0; e < 4; ++e) {
       const int r = 4 * kq + e;
       const int d = D == 128 ? 8 * r + kOrder[n] : 8 * (r & 7) + 2 * n + (r >> 3);
-      red[wave][c][d] = o[n][e] - pz;
+      red[wave][c][d] = o[n][e] * (n & 1 ? 0x1p20f : 0x1p24f) - pz;
     }
   if (kq == 0) {
     red_m[wave][c] = M;
@@ -555,7 +596,7 @@ void kv_decode_kernel(KvAttn p) {
   const int rr = row0 + r;
   const int64_t head_row = (rq.token0 + rr / p.group) * ((int64_t)p.heads * p.group) +
                            h * p.group + rr % p.group;
-  if (p.splits > 1) {
+  if (keys.parts > 1) {
     const int64_t at = split * p.T * p.heads * p.group + head_row;
     float *po = p.part_o + at * D + d0;
     if (!none) {
@@ -624,11 +665,11 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   const int w_any_last = last_key(p, rq, wrow1 / p.group);
   const int w_all_last = last_key(p, rq, wrow0 / p.group);
   const int w_any_first = first_key(p, w_all_last), w_all_first = first_key(p, w_any_last);
-  const int g_last = last_key(p, rq, clamp_row(row0 + kRows - 1) / p.group);
-  const int g_first = first_key(p, last_key(p, rq, row0 / p.group));
-  const int t_lo = g_first & ~(kPtKeys - 1);
-  const int nt = g_last >= t_lo ? (g_last - t_lo) / kPtKeys + 1 : 0;
-  const int i0 = (int)((int64_t)nt * split / p.splits), i1 = (int)((int64_t)nt * (split + 1) / p.splits);
+  const Keys keys = keys_of(p, rq, row0, clamp_row(row0 + kRows - 1), kPtKeys);
+  if (split >= keys.parts) return;
+  const int t_lo = keys.lo + split * keys.each;
+  const int t_hi = split + 1 < keys.parts ? t_lo + keys.each : keys.end;
+  const int i0 = 0, i1 = t_hi > t_lo ? (t_hi - t_lo + kPtKeys - 1) / kPtKeys : 0;
 
   // ---- staging: codes of one tile to registers, then as integers to LDS.  The
   // pieces (16 bytes of a key's codes; one word of four tokens' value codes)
@@ -936,8 +977,8 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   const float inv = none ? 0.0f : 1.0f / l;
   const float lse2 = none ? -__builtin_inff() : M + __builtin_amdgcn_logf(l);
   const int64_t head_row = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + row % p.group;
-  const int64_t at = p.splits > 1 ? split * p.T * p.heads * p.group + head_row : head_row;
-  if (p.splits > 1) {
+  const int64_t at = keys.parts > 1 ? split * p.T * p.heads * p.group + head_row : head_row;
+  if (keys.parts > 1) {
     if (hh == 0) p.part_lse[at] = lse2;
     if (none) return;
   } else if (p.lse && hh == 0) {
@@ -954,7 +995,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
       v[ch] = none ? 0.0f : o[n][4 * g + (x & 3)] * inv;
     }
     const int64_t d = at * D + 8 * word;
-    if (p.splits > 1) {
+    if (keys.parts > 1) {
       float4 *po = reinterpret_cast<float4 *>(p.part_o + d);
       po[0] = float4{v[0], v[1], v[2], v[3]};
       po[1] = float4{v[4], v[5], v[6], v[7]};
@@ -987,21 +1028,25 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int b = blockIdx.z, h = blockIdx.y, r = blockIdx.x;
   const Request rq = request_of(p, b);
-  if (r >= rq.ql * p.group) return;
+  const int rows = rq.ql * p.group;
+  if (r >= rows) return;
+  const int row0 = r - r % p.tile_rows, row1 = row0 + p.tile_rows <= rows ? row0 + p.tile_rows - 1 : rows - 1;
+  const int parts = keys_of(p, rq, row0, row1, p.tile_rows == 16 ? 32 : kPtKeys).parts;
+  if (parts == 1) return;                            // stored by its one workgroup
   const int64_t n = p.T * p.heads * p.group;
   const int64_t at = (rq.token0 + r / p.group) * ((int64_t)p.heads * p.group) + h * p.group + r % p.group;
-  const float x = lane < p.splits ? p.part_lse[lane * n + at] : -__builtin_inff();
+  const float x = lane < parts ? p.part_lse[lane * n + at] : -__builtin_inff();
   float m = x;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
   const float w = x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x - m);
   float sum = 0.0f, acc[kPer] = {};
-  for (int s0 = wave; s0 < p.splits; s0 += 4 * kChunk) {
+  for (int s0 = wave; s0 < parts; s0 += 4 * kChunk) {
     float v[kChunk][kPer], ws[kChunk];
 #pragma unroll
     for (int u = 0; u < kChunk; ++u) {
-      const int s = s0 + 4 * u < p.splits ? s0 + 4 * u : s0;
-      ws[u] = s0 + 4 * u < p.splits ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s)) : 0.0f;
+      const int s = s0 + 4 * u < parts ? s0 + 4 * u : s0;
+      ws[u] = s0 + 4 * u < parts ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s)) : 0.0f;
       const float *src = p.part_o + (s * n + at) * D + lane * kPer;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[u][i] = src[i];
@@ -1028,8 +1073,6 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
 }
 
 // ---- plan and launch ------------------------------------------------------------------------------
-constexpr int kDecodeWaves = 4;
-
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
                              int window) {
   KvAttnPlan pl{};
@@ -1037,20 +1080,29 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
   // keys that a tile of rows can see at most
   int64_t span = max_kv;
   if (window > 0 && (int64_t)window + max_q < span) span = (int64_t)window + max_q;
-  if (span < 1) span = 1;
+  span = span < 1 ? 1 : span > 0x7FFFFF00 ? 0x7FFFFF00 : span;
   pl.prompt = rows > 32;
-  const int64_t tiles = pl.prompt ? (rows + kPtRows - 1) / kPtRows : (rows + 15) / 16;
-  const int64_t wgs = (int64_t)B * heads * tiles;
+  pl.tile_rows = pl.prompt ? kPtRows : 16;
+  const int64_t wgs = (int64_t)B * heads * ((rows + pl.tile_rows - 1) / pl.tile_rows);
+  pl.waves = 4;
   int64_t splits;
   if (pl.prompt) {
-    splits = wgs > 0 ? 512 / wgs : 1;
-    const int64_t most = (span + 255) / 256;
-    splits = splits < most ? splits : most;
+    // enough workgroups for every CU's two
+    pl.chunk = 256;
+    splits = wgs > 0 && wgs < 512 ? 512 / wgs : 1;
+  } else if (span <= 1024 && wgs < 512) {
+    // short contexts of few requests: eight waves and no join
+    pl.waves = 8;
+    pl.chunk = 1024;
+    splits = 1;
   } else {
-    splits = wgs > 0 ? 1024 / wgs : 1;
-    const int64_t most = (span + 511) / 512;
-    splits = splits < most ? splits : most;
+    // four workgroups to a CU; with as many rows as that anyway, two parts for
+    // the long requests of a batch, which would otherwise finish last
+    pl.chunk = wgs < 1024 ? 512 : 1024;
+    splits = wgs > 0 && wgs < 1024 ? 1024 / wgs : 2;
   }
+  const int64_t most = (span + pl.chunk - 1) / pl.chunk;
+  splits = splits < most ? splits : most;
   splits = splits < kMaxSplits ? splits : kMaxSplits;
   pl.splits = splits < 1 ? 1 : (int)splits;
   if (pl.splits > 1) {
@@ -1070,7 +1122,8 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
     kv_prompt_kernel<D, SYM, BF16><<<grid, kPtThreads, 0, st>>>(p);
   } else {
     const dim3 grid((unsigned)((rows + 15) / 16 * p.heads), (unsigned)p.splits, (unsigned)B);
-    kv_decode_kernel<D, SYM, BF16, kDecodeWaves><<<grid, 64 * kDecodeWaves, 0, st>>>(p);
+    if (pl.waves == 8) kv_decode_kernel<D, SYM, BF16, 8><<<grid, 512, 0, st>>>(p);
+    else kv_decode_kernel<D, SYM, BF16, 4><<<grid, 256, 0, st>>>(p);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
@@ -1082,6 +1135,8 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
 hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPlan &pl,
                                void *workspace, hipStream_t st) {
   p.splits = pl.splits;
+  p.chunk = pl.chunk;
+  p.tile_rows = pl.tile_rows;
   if (pl.splits > 1) {
     p.part_o = reinterpret_cast<float *>(workspace);
     p.part_lse = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + pl.lse_offset);

@@ -134,11 +134,10 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
                                                   halved, times |c| <= 8 or 15, where the
                                                   largest weight is at least 2^-1 max vs
       fp32 logits of D products, the zero term    dl = (D + 8) 2^-24 a scale, a = ks sum |q|
-      and the scaling                             (code + zero), or |code - 8| without
-                                                  zeros; moves p by 2 dl at most
-      fp32 sums over n keys (and exp2)            (n + 64) 2^-24 sum p vs (|c| + |z|)
+      and the scaling                             (code + zero); moves p by 2 dl at most
+      fp32 sums over n keys (and exp2)            (n + 64) 2^-24 sum p vs (code + zero)
     """
-    codes, scales, zeros = cache
+    codes, scales, _ = cache
     pages, page = codes.shape[0], scales.shape[2]
     T, heads, D = Q.shape
     Hkv = scales.shape[1]
@@ -173,8 +172,7 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
                 p /= l
                 o = p @ val[1, at, h]
                 O[q0 + i, j], lse[q0 + i, j] = o, m + np.log(l)
-                operand = np.abs(c[0, at, h]) if zeros is None else c[0, at, h] + z[0, at, h][:, None] + 16
-                mag = s[0, at, h] * (operand @ np.abs(q))
+                mag = s[0, at, h] * ((c[0, at, h] + z[0, at, h][:, None] + 16) @ np.abs(q))
                 dl = (D + 8) * 2.0 ** -24 * abs(scale) * mag.max()
                 vs = s[1, at, h]
                 cv = np.maximum(np.abs(c[1, at, h]), np.abs(c[1, at, h] - z[1, at, h][:, None]))
@@ -183,5 +181,5 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
                 bound[q0 + i, j] = (out_eps * np.abs(o) + 2.0 ** -11 * ((p * vs) @ cv)
                                     + n * 2.0 ** -21 * vs.max()
                                     + 2 * dl * (p @ np.abs(val[1, at, h]))
-                                    + (n + 64) * 2.0 ** -24 * ((p * vs) @ (cv + np.abs(z[1, at, h])[:, None])))
+                                    + (n + 64) * 2.0 ** -24 * ((p * vs) @ (c[1, at, h] + z[1, at, h][:, None] + 16)))
     return O, lse, bound, lse_bound
