@@ -26,5 +26,6 @@ __all__ = list(_API)
 def __getattr__(name):
     if name in _API:
         from . import binding
-        return getattr(binding, name)
+        value = globals()[name] = getattr(binding, name)      # (later accesses find it at once)
+        return value
     raise AttributeError(name)

@@ -4,10 +4,20 @@
 // layer without one keeps its code.
 #pragma once
 
+#include <type_traits>
+
 #include "awq_internal.h"
 #include "device_common.h"
 
 namespace awq {
+
+// The kernels' epilogue argument: nothing where there is none (24 bytes more of
+// arguments cost the single-token kernel 0.1 us).
+struct NoEpilogue {
+  __host__ __device__ NoEpilogue(const Epilogue &) {}
+};
+template <bool EPI>
+using EpilogueArg = std::conditional_t<EPI, Epilogue, NoEpilogue>;
 
 // Element i of an array of output type YT (bias and residual have Y's type).
 template <int YT>

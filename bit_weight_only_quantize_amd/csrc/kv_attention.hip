@@ -1012,21 +1012,24 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
 
 // ---- join the splits ---------------------------------------------------------------------------
 // Row (token, head): weights 2^(lse_s - max lse) over at most kMaxSplits splits,
-// one workgroup per row: lane s of every wave reads split s's lse, wave w sums
-// the splits s = w mod 4, their rows loaded eight at a time, and the four sums
-// meet in LDS.  (One wave per row, a split at a time, took 24 us where this
-// takes 4 for 32 splits of 256 rows.)  A split in which the row saw no key has
-// written -inf and no O.  Rows that no request serves were not written and are
-// not read.
+// WPR waves of a workgroup of four per row: lane s reads split s's lse, wave w of
+// the row sums the splits s = w mod WPR, their rows loaded eight at a time, and
+// the waves' sums meet in LDS.  (Many splits of few rows, a decode step's, want
+// the waves on one row: 32 splits of 256 rows took one wave per row 24 us, four
+// 4.  Few splits of many rows, a prompt's, want a wave each: 2 splits of 12360
+// rows of 64 took four waves per row 38 us.)  A split in which the row saw no
+// key has written -inf and no O.  Rows that no request serves were not written
+// and are not read.
 constexpr int kMaxSplits = 64;
 
-template <int D, bool BF16>
+template <int D, bool BF16, int WPR>
 __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
   constexpr int kPer = D / 64, kChunk = 8;
   __shared__ float part[4][D], part_sum[4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int b = blockIdx.z, h = blockIdx.y, r = blockIdx.x;
+  const int b = blockIdx.z, h = blockIdx.y;
+  const int w0 = WPR == 4 ? wave : 0, r = WPR == 4 ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave;
   const Request rq = request_of(p, b);
   const int rows = rq.ql * p.group;
   if (r >= rows) return;
@@ -1041,12 +1044,12 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
   for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
   const float w = x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x - m);
   float sum = 0.0f, acc[kPer] = {};
-  for (int s0 = wave; s0 < parts; s0 += 4 * kChunk) {
+  for (int s0 = w0; s0 < parts; s0 += WPR * kChunk) {
     float v[kChunk][kPer], ws[kChunk];
 #pragma unroll
     for (int u = 0; u < kChunk; ++u) {
-      const int s = s0 + 4 * u < parts ? s0 + 4 * u : s0;
-      ws[u] = s0 + 4 * u < parts ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s)) : 0.0f;
+      const int s = s0 + WPR * u < parts ? s0 + WPR * u : s0;
+      ws[u] = s0 + WPR * u < parts ? __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), s)) : 0.0f;
       const float *src = p.part_o + (s * n + at) * D + lane * kPer;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[u][i] = src[i];
@@ -1058,18 +1061,26 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
       for (int i = 0; i < kPer; ++i) acc[i] = ws[u] != 0.0f ? __builtin_fmaf(v[u][i], ws[u], acc[i]) : acc[i];
     }
   }
+  if constexpr (WPR == 4) {
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) part[wave][lane * kPer + i] = acc[i];
-  if (lane == 0) part_sum[wave] = sum;
-  __syncthreads();
-  const float total = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
-  const int d = threadIdx.x;
-  if (d < D) {
-    const float v = total == 0.0f ? 0.0f : ((part[0][d] + part[1][d]) + (part[2][d] + part[3][d])) / total;
-    reinterpret_cast<uint16_t *>(p.O)[at * D + d] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
+    for (int i = 0; i < kPer; ++i) part[wave][lane * kPer + i] = acc[i];
+    if (lane == 0) part_sum[wave] = sum;
+    __syncthreads();
+    if (wave != 0) return;
+    sum = (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int d = lane * kPer + i;
+      acc[i] = (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]);
+    }
   }
-  if (p.lse && d == 0)
-    p.lse[at] = total == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(total)) * 0.69314718055994531f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const float v = sum == 0.0f ? 0.0f : acc[i] / sum;
+    reinterpret_cast<uint16_t *>(p.O)[at * D + lane * kPer + i] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
+  }
+  if (p.lse && lane == 0 && w0 == 0)
+    p.lse[at] = sum == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
 // ---- plan and launch ------------------------------------------------------------------------------
@@ -1127,7 +1138,10 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  kv_join_kernel<D, BF16><<<dim3((unsigned)rows, (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
+  if (p.splits > 8)
+    kv_join_kernel<D, BF16, 4><<<dim3((unsigned)rows, (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
+  else
+    kv_join_kernel<D, BF16, 1><<<dim3((unsigned)((rows + 3) / 4), (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 }  // namespace

@@ -75,7 +75,8 @@ __global__ __launch_bounds__(64 * kBgWaves) __attribute__((amdgpu_waves_per_eu(4
 void batched_gemv_kernel(
     const uint16_t *__restrict__ X, const uint32_t *__restrict__ qweight,
     const uint16_t *__restrict__ scales, const uint8_t *__restrict__ zeros, int M, int N, int K,
-    int gps, void *Y, int ytype, uint32_t zfix, float *__restrict__ partial, Epilogue epi) {
+    int gps, void *Y, int ytype, uint32_t zfix, float *__restrict__ partial,
+    EpilogueArg<EPI> epi) {
   using Geo = BgGeom<GS, MT>;
   constexpr int kWpl = GS / 32;            // packed words per lane per group
   constexpr int kMG = Geo::kMaxGroups;
@@ -245,7 +246,7 @@ template <int VEC, bool EPI>
 __global__ __launch_bounds__(256) void batched_gemv_reduce_kernel(const float *__restrict__ partial,
                                                                   int splits, int64_t MN, void *Y,
                                                                   int ytype, uint32_t N,
-                                                                  Epilogue epi) {
+                                                                  EpilogueArg<EPI> epi) {
   constexpr int kChunk = 8;
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * VEC;
   if (i >= MN) return;
@@ -391,7 +392,8 @@ static hipError_t bg_go(const void *X, const uint32_t *qw, const uint16_t *sc, c
   auto go = [&](auto refill, auto with_epi) {
     batched_gemv_kernel<XT, GS, MT, decltype(refill)::value, decltype(with_epi)::value>
         <<<grid, Geo::kThreads, Geo::kBytes, st>>>(x, qw, sc, zr, (int)M, (int)N, (int)K, p.gps, Y,
-                                                   (int)yt, zfix, part, epi);
+                                                   (int)yt, zfix, part,
+                                                   EpilogueArg<decltype(with_epi)::value>(epi));
   };
   auto pick = [&](auto with_epi) {
     if constexpr (kPairs) {
@@ -406,10 +408,10 @@ static hipError_t bg_go(const void *X, const uint32_t *qw, const uint16_t *sc, c
   const int64_t MN = M * N;
   if (MN % 4 == 0)
     batched_gemv_reduce_kernel<4, EPI><<<(unsigned)((MN / 4 + 255) / 256), 256, 0, st>>>(
-        partial, p.splits, MN, Y, (int)yt, (uint32_t)N, epi);
+        partial, p.splits, MN, Y, (int)yt, (uint32_t)N, EpilogueArg<EPI>(epi));
   else
     batched_gemv_reduce_kernel<1, EPI><<<(unsigned)((MN + 255) / 256), 256, 0, st>>>(
-        partial, p.splits, MN, Y, (int)yt, (uint32_t)N, epi);
+        partial, p.splits, MN, Y, (int)yt, (uint32_t)N, EpilogueArg<EPI>(epi));
   return hipGetLastError();
 }
 

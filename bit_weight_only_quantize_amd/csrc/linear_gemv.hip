@@ -118,7 +118,7 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g));
 template <class XT, int GS, int NW, int U, bool STAGE_X, int NP, bool MULTI, bool SMALL, bool EPI>
 __global__ __launch_bounds__(64 * NW) void gemv_kernel(const uint16_t *__restrict__ X,
                                                        GemvParts parts, int M, int K, int ytype,
-                                                       uint32_t zfix, Epilogue epi) {
+                                                       uint32_t zfix, EpilogueArg<EPI> epi) {
   constexpr int kWpl = GS / 32;            // packed words per lane per group
   constexpr bool kBF16 = __is_same(XT, TagBF16);
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -499,13 +499,13 @@ static void gemv_launch(const uint16_t *X, const GemvParts &parts, int tiles, in
                                       : (16 * G + 64 * NW - 1) / (64 * NW);
   const bool small = xr <= 2 && szr <= 1;
   if (stage && G > 8 * NW)
-    gemv_kernel<XT, GS, NW, 2, true, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
+    gemv_kernel<XT, GS, NW, 2, true, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, EpilogueArg<EPI>(epi));
   else if (stage && small)
-    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, true, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
+    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, true, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, EpilogueArg<EPI>(epi));
   else if (stage)
-    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
+    gemv_kernel<XT, GS, NW, 1, true, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, EpilogueArg<EPI>(epi));
   else
-    gemv_kernel<XT, GS, NW, 2, false, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, epi);
+    gemv_kernel<XT, GS, NW, 2, false, NP, MULTI, false, EPI><<<grid, 64 * NW, bytes, st>>>(X, parts, M, (int)K, (int)yt, zfix, EpilogueArg<EPI>(epi));
 }
 
 // Waves per workgroup.  Every workgroup of a launch should be resident at
