@@ -165,9 +165,7 @@ __device__ __forceinline__ int last_key(const KvAttn &p, const Request &r, int q
   return p.causal ? r.kv - r.qn + qi : r.kv - 1;
 }
 __device__ __forceinline__ int first_key(const KvAttn &p, int last) {
-  if (!p.window) return 0;
-  const int f = last - p.window + 1;
-  return f > 0 ? f : 0;
+  return p.window && last >= p.window ? last - p.window + 1 : 0;
 }
 
 // The keys of a tile of rows row0 .. row1, from `lo` (a multiple of `align`) to

@@ -373,6 +373,15 @@ def test_infinite_values_of_keys_behind_a_row(n):
     assert not torch.isfinite(got[-1].float()).any()
 
 
+@pytest.mark.parametrize("n", [3, 40])
+def test_largest_window(n):
+    """A window of 2^31 - 1 is none, also where the first rows see no key."""
+    a = Attend([n, n], [n - 2, n + 9], 4, 2, 64, 16, True, "float16", seed=17)
+    want, _ = a.check(window=0)
+    got, _ = a.check(window=2 ** 31 - 1)
+    assert torch_mod().equal(got, want)
+
+
 def test_rows_of_no_request_are_left_alone():
     import bit_weight_only_quantize_amd as awq
     torch = torch_mod()
