@@ -13,6 +13,12 @@ using namespace awq;
 namespace {
 
 constexpr int64_t kMaxGrid = 65535;          // HIP's limit on grid y and z
+// Tokens of an append or gather: 16 or more to a workgroup of 256, and a grid
+// holds less than 2^32 threads.
+constexpr int64_t kMaxTokens = (int64_t)1 << 27;
+// Tokens of a request that attention reads: key numbers stay within 32 bits, a
+// tile or two past the last key included.
+constexpr int64_t kMaxContext = (int64_t)1 << 30;
 
 bool power_of_two(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -137,7 +143,7 @@ awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t 
   if (x_dtype != AWQ_F16 && x_dtype != AWQ_BF16)
     return fail(AWQ_ERR_INVALID_ARG, "%s: x_dtype=%d: must be AWQ_F16 or AWQ_BF16", who, x_dtype);
   if (num_tokens < 0) return fail(AWQ_ERR_INVALID_ARG, "%s: num_tokens=%lld is negative", who, (long long)num_tokens);
-  if (num_tokens > ((int64_t)1 << 31) - 1) return fail(AWQ_ERR_INVALID_ARG, "%s: too many tokens", who);
+  if (num_tokens > kMaxTokens) return fail(AWQ_ERR_INVALID_ARG, "%s: more than 2^27 tokens", who);
   const int64_t width = (int64_t)cache->num_kv_heads * cache->head_dim;
   if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
     return fail(AWQ_ERR_INVALID_ARG,
@@ -165,11 +171,13 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
   if (out_dtype != AWQ_F16 && out_dtype != AWQ_BF16 && out_dtype != AWQ_F32)
     return fail(AWQ_ERR_INVALID_ARG, "%s: out_dtype=%d: must be AWQ_F16, AWQ_BF16 or AWQ_F32", who, out_dtype);
   if (num_tokens < 0) return fail(AWQ_ERR_INVALID_ARG, "%s: num_tokens=%lld is negative", who, (long long)num_tokens);
-  if (num_tokens > ((int64_t)1 << 31) - 1) return fail(AWQ_ERR_INVALID_ARG, "%s: too many tokens", who);
+  if (num_tokens > kMaxTokens) return fail(AWQ_ERR_INVALID_ARG, "%s: more than 2^27 tokens", who);
   if (num_tokens == 0) return ok();
   if (!K || !V || !slots) return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 4))
     return fail(AWQ_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned, slots 4", who);
+  const size_t bytes = (size_t)num_tokens * cache->num_kv_heads * cache->head_dim * (out_dtype == AWQ_F32 ? 4 : 2);
+  if (!apart(K, bytes, V, bytes)) return fail(AWQ_ERR_INVALID_ARG, "%s: K and V overlap", who);
   const YType ot = out_dtype == AWQ_F16 ? YType::F16 : out_dtype == AWQ_BF16 ? YType::BF16 : YType::F32;
   return hip_status(launch_kv_gather(kv_cache(cache, cfg), slots, num_tokens, K, V, ot, as_stream(stream)), who);
 }
@@ -181,6 +189,7 @@ size_t awq_kv_attention_workspace_size(int64_t num_tokens, int32_t num_seqs, int
                             max_query_len, max_seq_len, window, false) != AWQ_OK)
     return 0;
   if (num_tokens == 0 || num_seqs == 0 || max_query_len == 0) return 0;
+  if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
   return kv_attention_plan(num_tokens, num_seqs, cache->num_kv_heads, num_heads / cache->num_kv_heads,
                            cache->head_dim, max_query_len, max_seq_len, window)
       .workspace_bytes;
@@ -205,8 +214,8 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
   if (causal != 0 && causal != 1) return fail(AWQ_ERR_INVALID_ARG, "%s: causal=%d: must be 0 or 1", who, causal);
   if (window > 0 && !causal) return fail(AWQ_ERR_INVALID_ARG, "%s: a window needs causal = 1", who);
   if (!std::isfinite(scale)) return fail(AWQ_ERR_INVALID_ARG, "%s: scale is not finite", who);
-  if (max_blocks < 0 || (int64_t)max_blocks * cache->page_size > ((int64_t)1 << 31) - 1)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: max_blocks=%d: negative, or beyond 2^31 - 1 tokens", who, max_blocks);
+  if (max_blocks < 0 || (int64_t)max_blocks * cache->page_size > kMaxContext)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: max_blocks=%d: negative, or beyond 2^30 tokens", who, max_blocks);
   if (!query_start && (num_tokens != num_seqs || max_query_len > 1))
     return fail(AWQ_ERR_INVALID_ARG, "%s: without query_start every request has one query token", who);
   if (workspace && !aligned(workspace, kAlign))
@@ -220,12 +229,18 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
   const size_t o_bytes = (size_t)num_tokens * num_heads * cache->head_dim * 2;
   if (!apart(Q, ((size_t)(num_tokens - 1) * q_stride + (size_t)num_heads * cache->head_dim) * 2, O, o_bytes))
     return fail(AWQ_ERR_INVALID_ARG, "%s: O overlaps Q", who);
+  const size_t lse_bytes = lse ? (size_t)num_tokens * num_heads * 4 : 0;
+  if (!apart(lse, lse_bytes, O, o_bytes)) return fail(AWQ_ERR_INVALID_ARG, "%s: lse overlaps O", who);
+  // (no request has more query tokens than there are; the same in ..._workspace_size)
+  if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
   const int group = num_heads / cache->num_kv_heads;
   const KvAttnPlan plan = kv_attention_plan(num_tokens, num_seqs, cache->num_kv_heads, group, cache->head_dim,
                                             max_query_len, max_seq_len, window);
   if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
     return fail(AWQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed (awq_kv_attention_workspace_size)", who,
                 workspace ? workspace_bytes : 0, plan.workspace_bytes);
+  if (!apart(workspace, plan.workspace_bytes, O, o_bytes) || !apart(workspace, plan.workspace_bytes, lse, lse_bytes))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: the workspace overlaps O or lse", who);
   KvAttn p{};
   p.Q = reinterpret_cast<const uint16_t *>(Q);
   p.q_stride = q_stride;

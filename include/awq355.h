@@ -503,7 +503,7 @@ awq_status awq_kv_assign(const int32_t *old_lens, const int32_t *new_lens, int32
  *            aligned.
  *   slots    device, int32 [num_tokens]; a token whose slot is negative or past
  *            the cache is skipped.  Slots must be distinct (a slot given twice
- *            ends with unspecified contents).
+ *            ends with unspecified contents).  num_tokens at most 2^27.
  *   nonfinite_count  device int32 or NULL: as in awq_quantize_pack.
  * The formula is awq_quantize_pack's with s = 1, per token and head.
  */
@@ -516,7 +516,8 @@ awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t 
  * awq_kv_gather - the values that slots stand for, as awq_dequantize gives a
  * weight's: K, V device [num_tokens][H][D] of out_dtype, dense, 16-byte
  * aligned; (code - zero) * step, exact for AWQ_F32, rounded once for AWQ_F16 and
- * AWQ_BF16.  A token whose slot is negative or past the cache gets zeros.
+ * AWQ_BF16.  A token whose slot is negative or past the cache gets zeros.  K
+ * and V may not overlap; num_tokens at most 2^27.
  */
 awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_t *slots,
                          int64_t num_tokens, void *K, void *V, int32_t out_dtype,
@@ -545,11 +546,12 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
  *   lse      device, fp32 [num_tokens][num_heads], or NULL: ln sum e^logit.
  *   workspace  device, 256-byte aligned, awq_kv_attention_workspace_size()
  *            bytes (NULL when that is 0); scratch as for awq_linear_ex, not to
- *            be shared by calls that overlap in time.
+ *            be shared by calls that overlap in time.  (Outputs and workspace
+ *            may not overlap each other.)
  * A row that sees no key gets O = 0 and lse = -inf.  Rows of no request (before
  * query_start[0], or behind query_start[num_seqs]) are left as they were.
  * Lengths beyond the table are cut to it; a table entry outside [0, num_pages)
- * holds no tokens.  What lies in slots that a row does not see, infinities
+ * holds no tokens.  max_blocks * P at most 2^30.  What lies in slots that a row does not see, infinities
  * and NaN included, does not reach it.
  * Arithmetic: logits are exact integer-times-query products summed in fp32,
  * times the key's step and `scale`; softmax weights times the value's step are

@@ -122,6 +122,28 @@ def test_attention_refusals(kw, status):
     assert "awq_kv_attention" in lib.awq_last_error().decode()
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(blocks=2 ** 26 + 1), INVALID),                     # 2^30 tokens and a page
+    (dict(lse=P(addr(10).value + 1024)), INVALID),           # lse within O
+    (dict(T=1, B=1, mk=60000, ws=P(addr(10).value - 4096), wsb=1 << 40), INVALID),
+    (dict(T=1, B=1, mk=60000, ws=P(addr(9).value - 65536), wsb=1 << 40, lse=addr(9), lens=addr(12)), INVALID),
+])
+def test_attention_refuses_long_tables_and_overlaps(kw, status):
+    assert attend(**kw) == status
+    assert "awq_kv_attention" in lib.awq_last_error().decode()
+
+
+def test_append_and_gather_refuse_what_a_grid_cannot_hold():
+    assert append(T=2 ** 27 + 1) == INVALID and gather(T=2 ** 27 + 1) == INVALID
+    assert gather(V=P(addr(4).value + 16)) == INVALID        # over K
+
+
+def test_attention_workspace_of_no_more_query_tokens_than_there_are():
+    size = lambda n, m: lib.awq_kv_attention_workspace_size(n, 1, 4, cache(), cfg(64), m, 60000, 0)  # noqa: E731
+    for n in (1, 5, 40, 700):
+        assert size(n, n) == size(n, 10 ** 8) > 0
+
+
 def test_attention_workspace():
     size = lambda *a: lib.awq_kv_attention_workspace_size(a[0], a[1], 4, cache(), cfg(64), *a[2:])  # noqa: E731
     need = size(1, 1, 1, 60000, 0)
