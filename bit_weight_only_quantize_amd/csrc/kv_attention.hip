@@ -453,11 +453,11 @@ void kv_decode_kernel(KvAttn p) {
         const uint32_t w = T.sc[i >> 2][i & 3];
         vmax = fmaxf(vmax, hi_half(w) <= 65504.0f ? hi_half(w) : 0.0f);
       }
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
+      vmax = fmaxf(vmax, __shfl_xor(vmax, 16, 64));
+      vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
       top = fmaxf(top, umax);
       slack = top + slack_width;
-      if (vmax > vlim) {                             // uniform
+      if (vmax > vlim) {
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         vexp = (float)ex;
         vlim = __builtin_ldexpf(1.0f, ex);
@@ -806,6 +806,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
   float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f;
+  float vleast = 0.0f;                                       // the least vlim of the wave's rows
 
   // The order of a tile's instructions is spelled out for the scheduler: left
   // to itself it keeps one operand register and waits out the LDS latency
@@ -868,7 +869,8 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) vf[0][n] = value_frag(0, n);
     scaled(1);
-    if (t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last || __any(vstep < 0.0f)) {
+    const bool partial = t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last || __any(vstep < 0.0f);
+    if (partial) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
@@ -883,18 +885,32 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     float umax = u[0];
 #pragma unroll
     for (int j = 1; j < 32; ++j) umax = fmaxf(umax, u[j]);
-    if (__any(umax > slack || vstep > vlim)) {
+    if (__any(umax > slack || vstep > vleast)) {
       umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
       top = fmaxf(top, umax);
       slack = top + kSlack;
-      // (a step that overflowed counts for none)
-      float vmax = vstep <= 65504.0f ? vstep : 0.0f;
+      if (__any(vstep > vleast)) {
+        // the largest step of the keys that the row sees (one that overflowed counts for none)
+        float vmax = vstep <= 65504.0f ? vstep : 0.0f;
+        if (partial) {
+          vmax = 0.0f;
 #pragma unroll
-      for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
-      if (vmax > vlim) {
+          for (int j = 0; j < 8; ++j) {
+            const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              vmax = fmaxf(vmax, (u[4 * j + e] > -__builtin_inff()) & (v[e] <= 65504.0f) ? v[e] : 0.0f);
+          }
+          vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
+        } else {
+#pragma unroll
+          for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
+        }
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
-        vexp = (float)ex;
-        vlim = __builtin_ldexpf(1.0f, ex);
+        const float lim = vmax > 0.0f ? __builtin_ldexpf(1.0f, ex) : 0.0f;
+        vexp = lim > vlim ? (float)ex : vexp;
+        vlim = fmaxf(vlim, lim);
+        if (!partial) vleast = fmaxf(vleast, lim);           // (every row has seen the tile)
       }
       const float m2 = running_max(top, 1.0f, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
