@@ -37,7 +37,7 @@ namespace awq {
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kSlack = 8.0f;         // log2 of the largest P' between rescalings
-constexpr float kNone = -1e30f;        // "no key yet": finite, so kNone - kNone is 0
+constexpr float kNone = -__FLT_MAX__;  // "no key yet": finite, so kNone - kNone is 0
 
 __device__ __forceinline__ f32x16 mfma32x16(u32x4 a, u32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
@@ -135,6 +135,11 @@ __device__ __forceinline__ float positive_scale(float cs) { return cs > 0x1p-120
 __device__ __forceinline__ float running_max(float top, float cs, float vexp) {
   return top == kNone ? kNone : __builtin_fmaf(top, cs, vexp);
 }
+
+// Logits so large that fp32 does not hold their fractions.  M is then not
+// top * cs + vexp to within a factor of two in 2^M, so weights are taken
+// relative to the largest logit itself, and no logit may exceed it.
+__device__ __forceinline__ bool past_fractions(float M) { return __builtin_fabsf(M) >= 0x1p24f && M != kNone; }
 
 // What a workgroup knows about its request.
 struct Request {
@@ -261,9 +266,9 @@ void kv_decode_kernel(KvAttn p) {
   for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
   // The key operand is the nibble pair as it lies in the word, a subnormal fp16:
   // code * 2^-24 for channels 0, 1, 4, 5 of a word, 16 times that for the others
-  // (the MFMA takes subnormals exactly).  The queries make up for it: scaled by a
-  // power of two into [2^14, 2^15) at most, those of the other channels by a
-  // sixteenth of it.  (Values below 2^-24 of the tile's largest lose bits.)
+  // (the MFMA takes subnormals exactly).  The queries make up for it: each row's
+  // scaled by a power of two into [2^14, 2^15) at most, those of the other channels
+  // by a sixteenth of it.  (Values below 2^-24 of the row's largest lose bits.)
   uint32_t qmax = 0;
 #pragma unroll
   for (int j = 0; j < kWords; ++j) {
@@ -271,7 +276,7 @@ void kv_decode_kernel(KvAttn p) {
     qmax = qmax > x ? qmax : x;
   }
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
+  for (int d = 32; d > 8; d >>= 1) {                 // (the row's lanes)
     const uint32_t x = (uint32_t)__shfl_xor((int)qmax, d, 64);
     qmax = qmax > x ? qmax : x;
   }
@@ -382,6 +387,7 @@ void kv_decode_kernel(KvAttn p) {
   // M = top * cs + vexp, top the largest sum so far (times the key's step), 2^vexp = vlim
   float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f, pz = 0.0f;
   const float slack_width = kSlack / cs;
+  bool any_past = false;                             // a row of the wave is past_fractions (uniform)
   // The nibble pairs of word w (of shifted words, the next two): subnormal fp16
   constexpr uint32_t kLoNibbles = 0x000F000Fu, kHiNibbles = 0x00F000F0u;
   // D = 64 has 8 words per token but an MFMA operand 16 rows: lanes c and
@@ -456,7 +462,6 @@ void kv_decode_kernel(KvAttn p) {
       vmax = fmaxf(vmax, __shfl_xor(vmax, 16, 64));
       vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
       top = fmaxf(top, umax);
-      slack = top + slack_width;
       if (vmax > vlim) {
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         vexp = (float)ex;
@@ -464,6 +469,9 @@ void kv_decode_kernel(KvAttn p) {
       }
       const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
+      const bool past = past_fractions(M);
+      slack = past ? top : top + slack_width;
+      any_past = __any(past);
       l *= a;
       pz *= a;
 #pragma unroll
@@ -471,13 +479,20 @@ void kv_decode_kernel(KvAttn p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] *= a;
     }
+    float ref = M;
+    if (any_past) {
+      const bool past = past_fractions(M);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] -= past ? top : 0.0f;
+      ref = past ? vexp : M;
+    }
     u32x4 pb;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float pr[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(u[4 * i + e], cs, -M));
+        const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(u[4 * i + e], cs, -ref));
         l += x;
         const uint32_t w = T.sc[i][e];
         pr[e] = mul_hi_half(x, w);
@@ -637,7 +652,6 @@ struct PromptSmem {
   char v[2][D * kValueRow];      // row ch * D/8 + word: channel 8 word + ch
   float ks[2][kPtKeys];          // key step * scale * log2(e)
   float vs[2][kPtKeys];          // value step; -1: no such token
-  uint32_t qmax[4];
 };
 
 template <int D, bool SYM, bool BF16>
@@ -720,7 +734,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     }
   };
   const DeqRegs dq;
-  float cs = __builtin_fabsf(p.scale_log2);
+  const float scale = positive_scale(__builtin_fabsf(p.scale_log2));
   auto stage = [&](int buf) {
     if (do_k) {
       const DeqF16 deq(kzz & 0xFFu);
@@ -732,7 +746,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
       if (kquad == 0) {
         const bool held = (int)key_lane < left;
         const float vstep = hi_half(ksc);
-        sm.ks[buf][kkey] = held ? lo_half(ksc) * cs : 0.0f;
+        sm.ks[buf][kkey] = held ? lo_half(ksc) * scale : 0.0f;
         // (an overflowed step as a finite one too large for fp16, so that the
         // zero weight of a row that does not see the key stays zero)
         sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
@@ -765,34 +779,28 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     }
   };
 
-  // ---- queries
+  // ---- queries, and the power of two that undoes their factor
+  float cs = 1.0f;
   const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
                        (int64_t)(h * p.group + row % p.group) * D + 8 * hh;
   u32x4 q[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
   if constexpr (BF16) {
-    uint32_t m = 0;                                          // one factor: it is part of the keys' steps in LDS
+    uint32_t m = 0;                                          // the row's largest
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const uint32_t x = bf16_magnitude8(q[s]);
       m = m > x ? m : x;
     }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const uint32_t x = (uint32_t)__shfl_xor((int)m, d, 64);
-      m = m > x ? m : x;
-    }
-    if (lane == 0) sm.qmax[wave] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) m = m > sm.qmax[w] ? m : sm.qmax[w];
+    const uint32_t x = (uint32_t)__shfl_xor((int)m, 32, 64);
+    m = m > x ? m : x;
     const float f = half_range_factor(m);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = bf16_to_half8(q[s], f);
-    cs *= 1.0f / f;
+    cs = 1.0f / f;
   }
-  cs = positive_scale(cs);
+  const float slack_width = kSlack / cs;
   if (p.scale_log2 < 0.0f) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
@@ -888,7 +896,6 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     if (__any(umax > slack || vstep > vleast)) {
       umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
       top = fmaxf(top, umax);
-      slack = top + kSlack;
       if (__any(vstep > vleast)) {
         // the largest step of the keys that the row sees (one that overflowed counts for none)
         float vmax = vstep <= 65504.0f ? vstep : 0.0f;
@@ -912,8 +919,11 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
         vlim = fmaxf(vlim, lim);
         if (!partial) vleast = fmaxf(vleast, lim);           // (every row has seen the tile)
       }
-      const float m2 = running_max(top, 1.0f, vexp), a = __builtin_amdgcn_exp2f(M - m2);
+      // (top * cs is exact, so for logits past_fractions M is off by vexp at most,
+      // and 2^(u cs - M) times a step stays an fp16 number)
+      const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
+      slack = past_fractions(M) ? top : top + slack_width;
       l *= a;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
@@ -930,7 +940,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
         float pr[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x = __builtin_amdgcn_exp2f(u[8 * st + 4 * g + e] - M);
+          const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(u[8 * st + 4 * g + e], cs, -M));
           l += x;
           pr[e] = x * v[e];
         }

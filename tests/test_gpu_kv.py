@@ -329,6 +329,16 @@ def test_steps_and_logits_of_many_sizes(n, spread, size, scale):
 
 
 @pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("scale", [1e4, 1e6, 3e7, 2e8, 1e9, 1e12, 1e30])
+def test_logits_past_the_fractions_of_fp32(n, dtype, scale):
+    """Up to 1e33: one key takes all, or several whose logits fp32 cannot tell
+    apart; nothing overflows."""
+    for size in (1.0, 1e-4, 1e4):
+        Attend([n, n], [150, 67], 4, 2, 64, 16, True, dtype, seed=20, size=size).check(scale=scale)
+
+
+@pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("gain", [1e-30, 1e5, 1e30])
 def test_bfloat16_queries_outside_fp16(n, gain):
     a = Attend([n], [100], 4, 2, 64, 16, True, "bfloat16", seed=9)
@@ -396,6 +406,18 @@ def test_large_steps_behind_a_row(n, step):
         a.cache[1][a.table[b, last // 16], :, last % 16, 1] = np.float16(step)
     a.check()
     a.check(window=5)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+@pytest.mark.parametrize("dtype,large,small", [("float16", 1e4, 1e-4), ("bfloat16", 1e20, 1e-10)])
+def test_queries_of_many_sizes_in_one_request(n, dtype, large, small):
+    """Rows whose queries differ by orders of magnitude keep their own precision."""
+    torch = torch_mod()
+    a = Attend([n], [60 + n], 4, 2, 64, 16, True, dtype, seed=19)
+    gain = np.where(np.arange(n) % 2 == 0, large, small)
+    a.Q = (a.Q.float() * torch.tensor(gain, dtype=torch.float32, device=dev())[:, None, None]).to(a.Q.dtype)
+    a.q64 = out_to_f64(a.Q)
+    a.check(scale=0.125 / small)
 
 
 def test_rows_of_no_request_are_left_alone():
