@@ -78,7 +78,7 @@ struct ActSilu { __device__ __forceinline__ float operator()(float x) const { re
 struct ActGelu {
   __device__ __forceinline__ float operator()(float x) const {
     const float half = 0.5f * x * erfc_nonneg(__builtin_fabsf(x) * 0.70710678118654752f);
-    return x < 0.0f ? half : x - half;
+    return x < 0.0f ? half : x - __builtin_fminf(half, 1.0f);   // (half <= 0.17; inf * 0 at infinity)
   }
 };
 struct ActGeluTanh {

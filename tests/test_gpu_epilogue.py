@@ -163,3 +163,21 @@ def test_activations_at_the_ends():
                                     residual=torch.zeros((len(x), 1), device=dev()))
         # fp32 activations: 2^-19 relative (e^-z of |z| <= 100 carries 100 2^-24), flushed below 1e-30
         assert (np.abs(out_to_f64(y)[:, 0] - want) <= 2.0 ** -17 * np.abs(want) + 1e-30).all(), act
+
+
+def test_infinite_pre_activation():
+    """A bias of infinity passes every activation as their limit, and stays in
+    its column."""
+    import bit_weight_only_quantize_amd as awq
+    torch = torch_mod()
+    M, N, K, g = 40, 136, 128, 128
+    pd, pk, Xd, x64, bias, _ = _case(M, N, K, g, "float16", "float16", True, 3)
+    for m in (1, 20, 40):
+        for act in ACTS:
+            want = awq.awq_linear_epilogue(Xd[:m], *pd, bias=bias, activation=act)
+            b = bias.clone()
+            b[[0, 70]] = float("inf")
+            y = awq.awq_linear_epilogue(Xd[:m], *pd, bias=b, activation=act)
+            assert torch.isposinf(y[:, [0, 70]]).all(), (m, act)
+            keep = [n for n in range(N) if n not in (0, 70)]
+            assert torch.equal(y[:, keep], want[:, keep])
