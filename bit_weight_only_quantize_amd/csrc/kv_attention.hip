@@ -5,16 +5,16 @@
 //   u_t = S_t * ks_t * scale * log2(e)
 //   O   = sum_t 2^(u_t) vs_t (vc_t - vz_t) / sum_t 2^(u_t)
 // with codes c, zero points z and steps s of the key and value of token t.
-// Codes reach the matrix cores as exact small integers in fp16 and queries as
-// fp16 (bfloat16 ones after an exact power-of-two scaling), so the only
-// operand that is rounded is the weight P'_t = 2^(u_t - M) vs_t, once, to fp16
-// (2^-11 relative, a quarter of what the fp16 output's own rounding adds in
-// quadrature with it); sums, the running maximum and the normalizer are fp32.
-// M is the running maximum of u plus the exponent of the largest value step
-// seen, so that P' <= 2^kSlack whatever the steps: it neither overflows nor
-// sinks into fp16's subnormals because a layer's values are small.  M moves
-// only when a logit exceeds it by kSlack, which makes the rescaling of O (and
-// the exchange between lanes that it needs) rare: a wave tests one ballot.
+// Codes reach the matrix cores as exact small integers in fp16 (or as exact
+// subnormals, below) and queries as fp16, after a power-of-two factor per row
+// where needed, so the only operand that is rounded is the weight
+// P'_t = 2^(u_t - M) vs_t, once, to fp16 (2^-11 relative); sums, the running
+// maximum and the normalizer are fp32.  M is the row's running maximum of u plus
+// the exponent of the largest value step that it has seen, so that P' <= 2^kSlack
+// whatever the steps: it neither overflows nor sinks into fp16's subnormals
+// because a layer's values are small.  M moves only when a logit exceeds it by
+// kSlack, which makes the rescaling of O (and the exchange between lanes that it
+// needs) rare: a wave tests one ballot.
 //
 // Rows of one key/value head are packed: row r of a request is query token
 // r / group, head r % group of the `group` query heads that share the
@@ -75,16 +75,15 @@ __device__ __forceinline__ uint32_t add_half2(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) + __builtin_bit_cast(f16x2, b));
 }
 
-// Power of two that brings a tile's largest finite magnitude (fp32 bits of a
+// Power of two that brings a row's largest finite magnitude (fp32 bits of a
 // non-negative value) into [2^14, 2^15): bfloat16 queries times it are fp16
-// numbers, exactly, unless they are below 2^-31 of the largest.  Kept within
-// 2^+-100 so that its inverse is normal.
+// numbers, exactly, unless they are below 2^-31 of the largest.  At most 2^100,
+// so that its inverse is normal.
 __device__ __forceinline__ float half_range_factor(uint32_t max_bits) {
   const int e = (int)(max_bits >> 23);
   if (e == 0) return 1.0f;
-  int k = 268 - e;                                   // biased exponent of 2^(14 - (e - 127))
-  k = k > 227 ? 227 : k < 27 ? 27 : k;
-  return __builtin_bit_cast(float, (uint32_t)k << 23);
+  const int k = 268 - e;                             // biased exponent of 2^(14 - (e - 127))
+  return __builtin_bit_cast(float, (uint32_t)(k > 227 ? 227 : k) << 23);
 }
 __device__ __forceinline__ uint32_t finite_magnitude(float x) {
   const uint32_t b = __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu;
@@ -193,13 +192,20 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 }
 
 // ---- few query rows: the decode kernel ------------------------------------------------------
-// Bound by reading the cache: D/2 bytes of key and of value codes and 4 to 6
-// bytes of steps and zero points per token and key/value head.  A workgroup
-// serves 16 query rows of one key/value head; each of its waves streams its
-// own run of tokens, 32 at a time, straight from memory into MFMA operands
-// (no LDS, no barrier until the end), the next 32 in flight meanwhile.  The
-// waves' results meet in LDS; with few requests the tokens are split over
-// several workgroups as well, whose results a second kernel joins.
+// Bound by reading the cache, D/2 bytes of key and of value codes and 4 to 6
+// bytes of steps and zero points per token and key/value head, and close behind
+// by the VALU that turns codes into operands.  A workgroup serves 16 query rows
+// of one key/value head; each of its waves streams its own run of tokens, 32 at a
+// time, straight from memory into MFMA operands (no LDS but for the queries, no
+// barrier until the end), the next 32 in flight meanwhile.  The waves' results
+// meet in LDS; with few requests the tokens are split over several workgroups as
+// well, whose results a second kernel joins.
+//
+// The operands are the code nibbles as they lie in the cache, masked to subnormal
+// fp16 numbers (code * 2^-24 or 2^-20), which the MFMA multiplies exactly: two
+// operations per pair of codes fewer than exact integers code - zero.  The zero
+// points come off the sums: sum q (code - z) = sum q code - z sum q, and for the
+// values sum P' code - sum P' z, with the weights as they were rounded.
 //
 // Lane (c = l & 15, kq = l >> 4).  Per 16 tokens: one 16-byte load of key
 // codes (D = 128: words 4kq.. of token c; 1 KiB per wave, one run), one of
@@ -207,11 +213,17 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 // of zero points.  S^T comes out as keys 4kq + e of row c.
 //
 // Registers hold one tile: key codes are refilled with the next tile's as soon
-// as they are dequantized, steps and zero points after the softmax, value codes
-// after their dequantization, so a load has most of a tile's work to arrive in
-// while four waves share a SIMD.  (Two register sets, two waves per SIMD,
-// measured 128 us where this takes 97 on 48 requests of up to 4096 tokens, 32
-// heads of 128.)
+// as they are used, steps and zero points after the softmax, value codes after
+// their products, so a load has most of a tile's work to arrive in while three
+// waves share a SIMD.  (Two register sets, two waves per SIMD, measured 128 us
+// where this took 113 on 48 requests of up to 4096 tokens, 32 heads of 128.)
+//
+// Measured there (429.6 MB): 96 us from an idle card, 4.5 TB/s of the 5.0 that a
+// copy reaches, and 111 - 117 repeated back to back, when the card's power limit
+// lowers the clock: the VALU is active 69% of the time, the MFMA 14%, and memory
+// delivers 1.01 times the bytes.  Four requests of up to 65536 tokens, 64 heads
+// over 8 (158.3 MB, symmetric): 30.1 us, 5.3 TB/s, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 10.4 us, which is latency:
+// lengths, table, codes, and the waves' join, one after the other.
 template <int D>
 struct DecodeTile {
   static constexpr int kWords = D / 32;              // key words per lane and token
@@ -629,9 +641,9 @@ void kv_decode_kernel(KvAttn p) {
 }
 
 // ---- many query rows: the prompt kernel --------------------------------------------------------
-// Bound by the softmax on the VALU next to the matrix products: about ten
-// VALU instructions per pair of row and key and wave lane, at a quarter of
-// the MFMA's width.  A workgroup serves 128 rows (four waves of 32) of one
+// Bound by the VALU next to the matrix products: per row and key the softmax
+// takes seven operations (one an exp2 at a quarter of the rate) and turning codes
+// into operands three more.  A workgroup serves 128 rows (four waves of 32) of one
 // key/value head and walks its keys 64 at a time.  Turning codes into fp16
 // integers costs as much VALU work per wave as the softmax of 32 rows, so it
 // is done once per workgroup: each thread turns 16 bytes of key and of value
@@ -640,6 +652,16 @@ void kv_decode_kernel(KvAttn p) {
 // hh = l >> 5) holds keys 8g + 4hh + e of row q.
 //
 // A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
+//
+// Measured: a prompt of 8192 tokens, 32 heads over 8, D = 128, bfloat16 (550
+// Gflop causal): 715 us from an idle card, 745 repeated, 740 - 770 Tflop/s; the
+// VALU is active 58% of the time, the MFMA 38%, the LDS 48% (a fifth of that
+// conflicts).  Six requests of up to 515 new tokens after up to 3000, 16 heads
+// over 4, D = 64: 40 us; there the longest request's 47 tiles, one after another,
+// are the time.  Slower on the long prompt: eight waves and 256 rows (993 us when
+// this took 834), a pipeline of half tiles (1376), the running maximum from a
+// bound in LDS (1115), 64 rows per wave at one wave per SIMD (the accumulators
+// travel between register files at every branch; D = 64: 1102 us for 630).
 constexpr int kPtKeys = 64, kPtRows = 128, kPtThreads = 256;
 
 // LDS rows end in 16 spare bytes, which puts the 16 rows of an operand read on
@@ -650,7 +672,7 @@ struct PromptSmem {
   static constexpr int kKeyRow = 2 * D + 16, kValueRow = 2 * kPtKeys + 16;   // bytes
   char k[2][kPtKeys * kKeyRow];
   char v[2][D * kValueRow];      // row ch * D/8 + word: channel 8 word + ch
-  float ks[2][kPtKeys];          // key step * scale * log2(e)
+  float ks[2][kPtKeys];          // key step * step_scale
   float vs[2][kPtKeys];          // value step; -1: no such token
 };
 
@@ -734,7 +756,11 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     }
   };
   const DeqRegs dq;
-  const float scale = positive_scale(__builtin_fabsf(p.scale_log2));
+  // scale * log2(e) = step_scale * row_scale: the mantissa goes into the key steps
+  // in LDS, the power of two (and the inverse of the row's factor) into the exponent
+  const uint32_t scale_bits = __builtin_bit_cast(uint32_t, __builtin_fabsf(p.scale_log2));
+  const float step_scale = __builtin_bit_cast(float, (scale_bits & 0x007FFFFFu) | 0x3F800000u);
+  const float row_scale = __builtin_bit_cast(float, scale_bits & 0x7F800000u);
   auto stage = [&](int buf) {
     if (do_k) {
       const DeqF16 deq(kzz & 0xFFu);
@@ -746,7 +772,7 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
       if (kquad == 0) {
         const bool held = (int)key_lane < left;
         const float vstep = hi_half(ksc);
-        sm.ks[buf][kkey] = held ? lo_half(ksc) * scale : 0.0f;
+        sm.ks[buf][kkey] = held ? lo_half(ksc) * step_scale : 0.0f;
         // (an overflowed step as a finite one too large for fp16, so that the
         // zero weight of a row that does not see the key stays zero)
         sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
@@ -779,8 +805,8 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     }
   };
 
-  // ---- queries, and the power of two that undoes their factor
-  float cs = 1.0f;
+  // ---- queries, and the power of two of their logits in the exponent
+  float cs = row_scale;
   const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
                        (int64_t)(h * p.group + row % p.group) * D + 8 * hh;
   u32x4 q[kSteps];
@@ -798,8 +824,9 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     const float f = half_range_factor(m);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) q[s] = bf16_to_half8(q[s], f);
-    cs = 1.0f / f;
+    cs *= 1.0f / f;
   }
+  cs = positive_scale(cs);
   const float slack_width = kSlack / cs;
   if (p.scale_log2 < 0.0f) {
 #pragma unroll
@@ -818,7 +845,8 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
 
   // The order of a tile's instructions is spelled out for the scheduler: left
   // to itself it keeps one operand register and waits out the LDS latency
-  // before every MFMA (915 us on 8192 tokens of 32 heads over 8, D = 128).
+  // before every MFMA (measured 915 us where this order took 834, on 8192 tokens of 32 heads over 8,
+  // D = 128).
   constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100;
   auto compute = [&](int buf, int t0) {
     const char *kl = sm.k[buf] + qc * Smem::kKeyRow + 16 * hh;

@@ -556,10 +556,10 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
  * Arithmetic: logits are exact integer-times-query products summed in fp32,
  * times the key's step and `scale`; softmax weights times the value's step are
  * rounded once to fp16 (2^-11 relative) and multiplied by the exact integers;
- * all sums, the maximum and the normalizer are fp32.  bfloat16 queries become
- * fp16 by a power-of-two factor per tile of rows, exactly (below 2^-31 of the
- * tile's largest value they are truncated).  Results do not change from call
- * to call.
+ * all sums, the maximum and the normalizer are fp32.  Queries may be scaled by a
+ * power of two per row (bfloat16 ones become fp16 so), exactly, except that
+ * values below 2^-24 of their row's largest lose their last bits.  Logits beyond
+ * fp32's range give infinities or NaN.  Results do not change from call to call.
  */
 awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, int64_t q_stride,
                             int32_t num_heads, const awq_kv_cache *cache, awq_config cfg,

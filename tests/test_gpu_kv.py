@@ -348,6 +348,17 @@ def test_bfloat16_queries_outside_fp16(n, gain):
 
 
 @pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("gain,scale", [(2.0 ** 120, 2.0 ** -123), (2.0 ** 120, 2.0 ** -80), (2.0 ** -110, 2.0 ** 108),
+                                        (2.0 ** -20, 2.0 ** 17), (1.0, 2.0 ** -126)])
+def test_queries_and_scales_at_the_ends_of_their_range(n, gain, scale):
+    a = Attend([n], [100], 4, 2, 64, 16, True, "bfloat16", seed=21)
+    a.Q = (a.Q.float() * gain).to(a.Q.dtype)
+    a.q64 = out_to_f64(a.Q)
+    a.check(scale=scale)
+    a.check(scale=-scale)
+
+
+@pytest.mark.parametrize("n", [1, 40])
 def test_nonfinite_keys_and_values_stay_with_those_who_see_them(n):
     """Tokens outside the window with infinite keys and values, and NaN queries
     of another request."""
