@@ -258,6 +258,24 @@ void kv_decode_kernel(KvAttn p) {
   const int row_last = row0 + 15 < rows ? row0 + 15 : rows - 1;
   const int row = row0 + c < rows ? row0 + c : rows - 1;
   const int qi = row / p.group;
+  const int32_t *table = p.table + (int64_t)b * p.max_blocks;
+  int page_base = 0;
+  int32_t page_ids = -1;                             // lane i: page page_base + i of the request
+  auto load_pages = [&](int first) {
+    page_base = first;
+    const int at = first + lane;
+    page_ids = at < p.max_blocks ? table[at] : -1;
+  };
+  // (the first pages and the queries do not wait for the request's length, which
+  // the rest depends on)
+  load_pages(0);
+  // queries: lane (c, kq) holds channels 32kq.. (D = 128) or 16kq.. (D = 64)
+  // of row c, the channels of the key words that it will load
+  const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
+                       (int64_t)(h * p.group + row % p.group) * D + kq * (8 * kWords);
+  u32x4 q[kWords];
+#pragma unroll
+  for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
   const int my_last = last_key(p, rq, qi), my_first = first_key(p, my_last);
   // keys that all rows see
   const int all_last = last_key(p, rq, row0 / p.group);
@@ -269,13 +287,6 @@ void kv_decode_kernel(KvAttn p) {
   const int nt = t_hi > t_lo ? (t_hi - t_lo + 31) / 32 : 0;
   const int i0 = nt * wave / NW, i1 = nt * (wave + 1) / NW;
 
-  // queries: lane (c, kq) holds channels 32kq.. (D = 128) or 16kq.. (D = 64)
-  // of row c, the channels of the key words that it will load
-  const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
-                       (int64_t)(h * p.group + row % p.group) * D + kq * (8 * kWords);
-  u32x4 q[kWords];
-#pragma unroll
-  for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
   // The key operand is the nibble pair as it lies in the word, a subnormal fp16:
   // code * 2^-24 for channels 0, 1, 4, 5 of a word, 16 times that for the others
   // (the MFMA takes subnormals exactly).  The queries make up for it: each row's
@@ -320,14 +331,6 @@ void kv_decode_kernel(KvAttn p) {
   }
 
   const int pmask = (1 << p.pshift) - 1;
-  const int32_t *table = p.table + (int64_t)b * p.max_blocks;
-  int page_base = 0;
-  int32_t page_ids = -1;                             // lane i: page page_base + i of the request
-  auto load_pages = [&](int first) {
-    page_base = first;
-    const int at = first + lane;
-    page_ids = at < p.max_blocks ? table[at] : -1;
-  };
   // A load's address is a uniform base (the tile's place) plus the lane's byte
   // offset within 16 tokens' key words, value words, and steps (zero points:
   // half of that).
@@ -568,7 +571,6 @@ void kv_decode_kernel(KvAttn p) {
   __syncthreads();
   if (i0 < i1) {
     int t = t_lo + 32 * i0;
-    load_pages(t >> p.pshift);
     DecodeAt at = place(t);
     load_keys(at);
     load_meta(at);
