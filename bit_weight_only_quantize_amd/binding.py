@@ -173,6 +173,7 @@ def _load():
 
 
 lib = _load()
+import torch as _TORCH  # noqa: E402  (after _load, which says why)
 
 
 def config(group_size: int = 128, w_bit: int = 4, zero_point: bool = True) -> awq_config:
@@ -195,8 +196,7 @@ def check(status: int, what: str) -> None:
 # dtype errors raise TypeError / ValueError even on machines without a GPU.
 
 def _torch():
-    import torch
-    return torch
+    return _TORCH
 
 
 def _tensor(t, name, dtype=None, shape=None):
@@ -264,8 +264,8 @@ def _one_gpu(*named):
 
 def _launch(fn, device, *args):
     """fn(*args, current stream) with `device` current, as the C calls want it; its status."""
-    torch = _torch()
-    if torch.cuda.current_device() == device:
+    torch = _torch()                                # (a tensor on the device has initialised it)
+    if torch._C._cuda_getDevice() == device:
         return fn(*args, torch._C._cuda_getCurrentRawStream(device))
     with torch.cuda.device(device):
         return fn(*args, torch._C._cuda_getCurrentRawStream(device))
@@ -284,7 +284,7 @@ def _scratch(workspace, need, like):
             raise ValueError("workspace must be a tensor, None or 'auto'")
         if need == 0:
             return None, 0
-        return torch.empty(need, dtype=torch.uint8, device=like.device), need
+        return like.new_empty(need, dtype=torch.uint8), need
     if workspace is None:
         return None, 0
     _tensor(workspace, "workspace")
@@ -513,7 +513,7 @@ def awq_linear_epilogue(X, qweight, scales, zeros, bias=None, residual=None,
                    None if residual is None else (residual, "residual"),
                    None if out is None else (out, "out"), None if ws is None else (ws, "workspace"))
     if out is None:
-        out = torch.empty((M, N), dtype=odt, device=X.device)
+        out = X.new_empty((M, N), dtype=odt)
     st = _launch(lib.awq_linear_epilogue, dev, _address(X), xd, _address(qweight), _address(scales),
                  _address(zeros), M, N, K, cfg, awq_epilogue(_address(bias), _address(residual), act),
                  _address(out), _dtype_code(odt), kernel, _address(ws), ws_bytes)
@@ -741,16 +741,22 @@ def _cache_arg(cache):
     if not isinstance(cache, (tuple, list)) or len(cache) != 3:
         raise TypeError("cache must be (codes, scales, zeros)")
     codes, scales, zeros = cache
-    _tensor(codes, "codes", torch.int32)
-    _tensor(scales, "scales", torch.float16)
-    if codes.dim() != 4 or codes.shape[1] != 2:
+    try:
+        fine = codes.dtype is torch.int32 and scales.dtype is torch.float16
+    except AttributeError:
+        fine = False
+    if not fine:
+        _tensor(codes, "codes", torch.int32)
+        _tensor(scales, "scales", torch.float16)
+    shape, meta = codes.shape, scales.shape
+    if len(shape) != 4 or shape[1] != 2:
         raise ValueError("codes must be [pages][2][heads][page_size * head_dim / 8]")
-    if scales.dim() != 4:
+    if len(meta) != 4:
         raise ValueError("scales must be [pages][heads][page_size][2]")
-    pages, _, heads, words = codes.shape
-    page = scales.shape[2]
-    meta = (pages, heads, page, 2)
-    _check(scales, "scales", torch.float16, meta)
+    pages, _, heads, words = shape
+    page = meta[2]
+    if meta != (pages, heads, page, 2):
+        _check(scales, "scales", torch.float16, (pages, heads, page, 2))
     if zeros is not None:
         _check(zeros, "zeros", torch.uint8, meta)
     if page < 1 or words * 8 % page:
@@ -822,7 +828,7 @@ def awq_kv_assign(old_lens, new_lens, block_table, free_pages, page_size: int, n
                    (free_pages, "free_pages"),
                    *(() if out is None else ((t, "out") for t in out)))
     if out is None:                                 # one allocation, in four parts
-        out = old_lens.new_empty(2 * B + num_slots + 2).split((B, B + 1, num_slots, 1))
+        out = old_lens.new_empty(2 * B + num_slots + 2).split_with_sizes((B, B + 1, num_slots, 1))
     seq_lens, query_start, slots, used = out
     st = _launch(lib.awq_kv_assign, dev, _address(old_lens), _address(new_lens), B, page_size,
                  _address(block_table), blocks, _address(free_pages), free_pages.shape[0],
@@ -881,8 +887,7 @@ def awq_kv_gather(cache, slots, out_dtype=None, out=None):
     dev = _one_gpu(*_cache_tensors(cache), (slots, "slots"),
                    *(() if out is None else ((out[0], "K"), (out[1], "V"))))
     if out is None:
-        out = (torch.empty(shape, dtype=odt, device=slots.device),
-               torch.empty(shape, dtype=odt, device=slots.device))
+        out = slots.new_empty(shape, dtype=odt), slots.new_empty(shape, dtype=odt)
     st = _launch(lib.awq_kv_gather, dev, c, cfg, _address(slots), T, _address(out[0]),
                  _address(out[1]), _dtype_code(odt))
     check(st, "awq_kv_gather")
@@ -948,8 +953,8 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
                    None if out is None else (out, "out"), None if ws is None else (ws, "workspace"))
     _same_gpu(dev, (Q, "Q"))
     if out is None:
-        out = torch.empty((T, heads, D), dtype=Q.dtype, device=Q.device)
-    lse = torch.empty((T, heads), dtype=torch.float32, device=Q.device) if return_lse else None
+        out = Q.new_empty((T, heads, D))
+    lse = Q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
     st = _launch(lib.awq_kv_attention, dev, _address(Q), _dtype_code(Q.dtype), T, stride, heads, c,
                  cfg, _address(block_table), blocks, _address(seq_lens), _address(query_start), B,
                  max_query_len, max_seq_len, D ** -0.5 if scale is None else scale, int(causal),
