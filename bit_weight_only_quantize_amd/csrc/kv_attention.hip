@@ -214,15 +214,16 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 //
 // Registers hold one tile: key codes are refilled with the next tile's as soon
 // as they are used, steps and zero points after the softmax, value codes after
-// their products, so a load has most of a tile's work to arrive in while three
-// waves share a SIMD.  (Two register sets, two waves per SIMD, measured 128 us
-// where this took 113 on 48 requests of up to 4096 tokens, 32 heads of 128.)
+// their products, so a load has most of a tile's work to arrive in while four
+// waves share a SIMD.  (48 requests of up to 4096 tokens, 32 heads of 128: two
+// register sets, two waves per SIMD, measured 128 us where one set and three
+// waves took 113; of the present code three waves take 94 and four 90.)
 //
-// Measured there (429.6 MB): 96 us from an idle card, 4.5 TB/s of the 5.0 that a
-// copy reaches, and 111 - 117 repeated back to back, when the card's power limit
+// Measured there (429.6 MB): 90 us from an idle card, 4.8 TB/s of the 5.0 that a
+// copy reaches, and 103 - 110 repeated back to back, when the card's power limit
 // lowers the clock: the VALU is active 69% of the time, the MFMA 14%, and memory
 // delivers 1.01 times the bytes.  Four requests of up to 65536 tokens, 64 heads
-// over 8 (158.3 MB, symmetric): 30.1 us, 5.3 TB/s, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 10.4 us, which is latency:
+// over 8 (158.3 MB, symmetric): 27 us, 5.9 TB/s, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.9 us, which is latency:
 // lengths, table, codes, and the waves' join, one after the other.
 template <int D>
 struct DecodeTile {
@@ -240,7 +241,7 @@ struct DecodeAt {
 };
 
 template <int D, bool SYM, bool BF16, int NW>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(3, 3)))
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void kv_decode_kernel(KvAttn p) {
   constexpr int kWords = D / 32, kTiles = D / 16;
   constexpr int kRow = D + 4;                        // floats per row in LDS
