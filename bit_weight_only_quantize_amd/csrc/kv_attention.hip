@@ -657,14 +657,18 @@ void kv_decode_kernel(KvAttn p) {
 // A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
 //
 // Measured: a prompt of 8192 tokens, 32 heads over 8, D = 128, bfloat16 (550
-// Gflop causal): 715 us from an idle card, 745 repeated, 740 - 770 Tflop/s; the
+// Gflop causal): 720 us from an idle card, 745 repeated, 740 - 765 Tflop/s; the
 // VALU is active 58% of the time, the MFMA 38%, the LDS 48% (a fifth of that
-// conflicts).  Six requests of up to 515 new tokens after up to 3000, 16 heads
-// over 4, D = 64: 40 us; there the longest request's 47 tiles, one after another,
-// are the time.  Slower on the long prompt: eight waves and 256 rows (993 us when
-// this took 834), a pipeline of half tiles (1376), the running maximum from a
-// bound in LDS (1115), 64 rows per wave at one wave per SIMD (the accumulators
-// travel between register files at every branch; D = 64: 1102 us for 630).
+// conflicts), at the 1.9 - 2.0 GHz that the power limit leaves.  With D = 64 three
+// waves fit a SIMD: 507 and 530 us (two waves 531 and 572).  Six requests of up to
+// 515 new tokens after up to 3000, 16 heads over 4, D = 64: 37 us; there the longest
+// request's 47 tiles, one after another, are the time.
+//
+// Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
+// a pipeline of half tiles (1376), the running maximum from a bound in LDS (1115),
+// 64 rows per wave at one wave per SIMD (the accumulators travel between register
+// files at every branch; D = 64: 1102 us for 616), the staging between the MFMAs
+// instead of after them (760 for 721).
 constexpr int kPtKeys = 64, kPtRows = 128, kPtThreads = 256;
 
 // LDS rows end in 16 spare bytes, which puts the 16 rows of an operand read on
@@ -680,7 +684,7 @@ struct PromptSmem {
 };
 
 template <int D, bool SYM, bool BF16>
-__global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
+__global__ __launch_bounds__(kPtThreads, D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttn p) {
   constexpr int kRows = kPtRows;
   using Smem = PromptSmem<D>;
   constexpr int kSteps = D / 16, kTiles = D / 32;
@@ -706,34 +710,30 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   if (split >= keys.parts) return;
   const int t_lo = keys.lo + split * keys.each;
   const int t_hi = split + 1 < keys.parts ? t_lo + keys.each : keys.end;
-  const int i0 = 0, i1 = t_hi > t_lo ? (t_hi - t_lo + kPtKeys - 1) / kPtKeys : 0;
+  const int nt = t_hi > t_lo ? (t_hi - t_lo + kPtKeys - 1) / kPtKeys : 0;
 
   // ---- staging: codes of one tile to registers, then as integers to LDS.  The
-  // pieces (16 bytes of a key's codes; one word of four tokens' value codes)
-  // are dealt out by groups of 16 tokens, which lie in one page: with D = 128
-  // a wave takes a group's 64 pieces of either kind, with
-  // D = 64 lanes below 32 of it the keys' 32, the others the values'.
-  const bool do_k = D == 128 || hh == 0, do_v = D == 128 || hh == 1;
-  const int piece = D == 128 ? lane : qc;
-  const int kkey = 16 * wave + piece / (D / 32), kquad = piece % (D / 32);
-  const int vblk = 4 * wave + piece / (D / 8), vword = piece % (D / 8);
+  // pieces are dealt out by groups of 16 tokens, which lie in one page, one group
+  // to a wave: a lane takes a quarter of a key's words, and one value word of four
+  // tokens (D = 128) or of two (D = 64).
+  constexpr int kKw = D / 32, kVt = D / 32;                  // key words; tokens of the value word
+  const int kkey = 16 * wave + (lane >> 2), kquad = lane & 3;
+  const int vblk = 4 * wave + (lane >> 4), vword = D == 128 ? lane & 15 : (lane & 15) >> 1;
+  const int vpair = D == 128 ? 0 : lane & 1;
   const int pmask = (1 << p.pshift) - 1;
   const int64_t P = (int64_t)pmask + 1;
   const int64_t code_stride = (int64_t)p.heads * P * D, meta_stride = (int64_t)p.heads * P * 2;
   const char *codes = reinterpret_cast<const char *>(p.codes) + h * P * (D / 2);
   const char *scales = reinterpret_cast<const char *>(p.scales) + h * P * 4;
   const char *zeros = reinterpret_cast<const char *>(p.zeros) + h * P * 2;
-  const uint32_t k_lane = (piece / (D / 32)) * (D / 2) + kquad * 16;
-  const uint32_t v_lane = (piece / (D / 8)) * (2 * D) + vword * 16;
-  const uint32_t key_lane = piece / (D / 32), blk_lane = (piece / (D / 8)) * 8;
   const int pages = p.pages < 0x7FFFFFFF ? (int)p.pages : 0x7FFFFFFF;
   const int32_t *table = p.table + (int64_t)b * p.max_blocks;
   int page_id = -1;                                          // of the tile to load next (uniform)
   int page_left = 0;                                         // its tokens of this wave's group
-  u32x4 kc = {}, vc = {};
-  uint32_t ksc = 0, kzz = 0x0808u;
-  u32x2 vzz = {0x08080808u, 0x08080808u};
+  uint32_t kc[kKw], vc[kVt];
+  uint32_t ksc = 0, kzz = 0x0808u, vzz[kVt / 2];
   int left = 0;                                              // tokens of the loaded group
+  // (past the last key there is no page: page 0 is read and counts for nothing)
   auto load_page = [&](int t0) {
     const int t = t0 + 16 * wave;
     page_id = t < rq.kv ? table[t >> p.pshift] : -1;
@@ -748,14 +748,22 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     const char *vp = kp + code_stride / 2;
     const char *sp = scales + (id * meta_stride + off * 2) * 2;
     const char *zp = zeros + (id * meta_stride + off * 2);
-    if (do_k) {
-      kc = *reinterpret_cast<const u32x4 *>(kp + k_lane);
-      ksc = *reinterpret_cast<const uint32_t *>(sp + key_lane * 4);
-      if constexpr (!SYM) kzz = *reinterpret_cast<const uint16_t *>(zp + key_lane * 2);
-    }
-    if (do_v) {
-      vc = *reinterpret_cast<const u32x4 *>(vp + v_lane);
-      if constexpr (!SYM) vzz = *reinterpret_cast<const u32x2 *>(zp + blk_lane);
+    using Piece = std::conditional_t<D == 128, u32x4, u32x2>;
+    const Piece kw = *reinterpret_cast<const Piece *>(kp + lane * (4 * kKw));
+    const Piece vw = *reinterpret_cast<const Piece *>(vp + lane * (4 * kVt));
+#pragma unroll
+    for (int j = 0; j < kKw; ++j) kc[j] = kw[j];
+#pragma unroll
+    for (int j = 0; j < kVt; ++j) vc[j] = vw[j];
+    ksc = *reinterpret_cast<const uint32_t *>(sp + (lane >> 2) * 4);
+    if constexpr (!SYM) {
+      kzz = *reinterpret_cast<const uint16_t *>(zp + (lane >> 2) * 2);
+#pragma unroll
+      for (int j = 0; j < kVt / 2; ++j)
+        vzz[j] = *reinterpret_cast<const uint32_t *>(zp + (lane >> 4) * 8 + vpair * 4 + 4 * j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVt / 2; ++j) vzz[j] = 0x08080808u;
     }
   };
   const DeqRegs dq;
@@ -764,48 +772,53 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   const uint32_t scale_bits = __builtin_bit_cast(uint32_t, __builtin_fabsf(p.scale_log2));
   const float step_scale = __builtin_bit_cast(float, (scale_bits & 0x007FFFFFu) | 0x3F800000u);
   const float row_scale = __builtin_bit_cast(float, scale_bits & 0x7F800000u);
-  auto stage = [&](int buf) {
-    if (do_k) {
-      const DeqF16 deq(kzz & 0xFFu);
+  auto stage_keys = [&](int buf) {
+    const DeqF16 deq(kzz & 0xFFu);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t w = kc[j];
-        *reinterpret_cast<u32x4 *>(sm.k[buf] + kkey * Smem::kKeyRow + kquad * 64 + 16 * j) = deq(w, dq);
-      }
-      if (kquad == 0) {
-        const bool held = (int)key_lane < left;
-        const float vstep = hi_half(ksc);
-        sm.ks[buf][kkey] = held ? lo_half(ksc) * step_scale : 0.0f;
-        // (an overflowed step as a finite one too large for fp16, so that the
-        // zero weight of a row that does not see the key stays zero)
-        sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
-      }
+    for (int j = 0; j < kKw; ++j)
+      *reinterpret_cast<u32x4 *>(sm.k[buf] + kkey * Smem::kKeyRow + (kquad * kKw + j) * 16) = deq(kc[j], dq);
+    // (the key's four lanes store the same)
+    const bool held = (lane >> 2) < left;
+    const float vstep = hi_half(ksc);
+    sm.ks[buf][kkey] = held ? lo_half(ksc) * step_scale : 0.0f;
+    // (an overflowed step as a finite one too large for fp16, so that the
+    // zero weight of a row that does not see the key stays zero)
+    sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
+  };
+  auto stage_values = [&](int buf) {
+    // word vword of kVt tokens: channel d's codes side by side
+    uint32_t a[kVt / 2], b[kVt / 2];
+#pragma unroll
+    for (int j = 0; j < kVt / 2; ++j) {
+      const uint32_t z = (vzz[j] >> 8) & 0x00FF00FFu;        // value zero points of two tokens
+      a[j] = z | 0xE400E400u;
+      b[j] = (z << 4) | 0xD400D400u;
     }
-    if (do_v) {
-      // word vword of four tokens: channel d's four codes side by side
-      uint32_t z0 = vzz[0], z1 = vzz[1];
-      z0 = (z0 >> 8) & 0x00FF00FFu;                          // value zero points of tokens 0, 1
-      z1 = (z1 >> 8) & 0x00FF00FFu;
-      const uint32_t a0 = z0 | 0xE400E400u, a1 = z1 | 0xE400E400u;
-      const uint32_t b0 = (z0 << 4) | 0xD400D400u, b1 = (z1 << 4) | 0xD400D400u;
-      const uint32_t w0 = vc[0], w1 = vc[1], w2 = vc[2], w3 = vc[3];
-      // tokens 16s + 8x + 4y + e sit at position 16s + 8y + 4x + e of the row
-      const int chunk = (vblk >> 2) * 2 + (vblk & 1), half = (vblk >> 1) & 1;
-      auto put = [&](int ch, uint32_t x0, uint32_t x1) {
-        *reinterpret_cast<u32x2 *>(sm.v[buf] + vword * Smem::kValueRow + chunk * 16 + 8 * half +
-                                   ch * (D / 8) * Smem::kValueRow) = u32x2{x0, x1};
-      };
-      auto bytes = [&](auto tag, int lo_ch, int hi_ch) {
-        constexpr int kB = decltype(tag)::value;
-        const uint32_t x0 = byte_pair<kB>(w0, w1), x1 = byte_pair<kB>(w2, w3);
-        put(lo_ch, add_half2((x0 & dq.lo) | dq.e1024, a0), add_half2((x1 & dq.lo) | dq.e1024, a1));
-        put(hi_ch, add_half2((x0 & dq.hi) | dq.e64, b0), add_half2((x1 & dq.hi) | dq.e64, b1));
-      };
-      bytes(std::integral_constant<int, 0>{}, 0, 2);
-      bytes(std::integral_constant<int, 1>{}, 4, 6);
-      bytes(std::integral_constant<int, 2>{}, 1, 3);
-      bytes(std::integral_constant<int, 3>{}, 5, 7);
-    }
+    // tokens 16s + 8x + 4y + e sit at position 16s + 8y + 4x + e of the row
+    const int chunk = (vblk >> 2) * 2 + (vblk & 1), half = (vblk >> 1) & 1;
+    char *row = sm.v[buf] + vword * Smem::kValueRow + chunk * 16 + 8 * half + 4 * vpair;
+    auto bytes = [&](auto tag, int lo_ch, int hi_ch) {
+      constexpr int kB = decltype(tag)::value;
+      uint32_t lo[kVt / 2], hi[kVt / 2];
+#pragma unroll
+      for (int j = 0; j < kVt / 2; ++j) {
+        const uint32_t x = byte_pair<kB>(vc[2 * j], vc[2 * j + 1]);
+        lo[j] = add_half2((x & dq.lo) | dq.e1024, a[j]);
+        hi[j] = add_half2((x & dq.hi) | dq.e64, b[j]);
+      }
+      char *lp = row + lo_ch * (D / 8) * Smem::kValueRow, *hp = row + hi_ch * (D / 8) * Smem::kValueRow;
+      if constexpr (D == 128) {
+        *reinterpret_cast<u32x2 *>(lp) = u32x2{lo[0], lo[1]};
+        *reinterpret_cast<u32x2 *>(hp) = u32x2{hi[0], hi[1]};
+      } else {
+        *reinterpret_cast<uint32_t *>(lp) = lo[0];
+        *reinterpret_cast<uint32_t *>(hp) = hi[0];
+      }
+    };
+    bytes(std::integral_constant<int, 0>{}, 0, 2);
+    bytes(std::integral_constant<int, 1>{}, 4, 6);
+    bytes(std::integral_constant<int, 2>{}, 1, 3);
+    bytes(std::integral_constant<int, 3>{}, 5, 7);
   };
 
   // ---- queries, and the power of two of their logits in the exponent
@@ -830,7 +843,6 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     cs *= 1.0f / f;
   }
   cs = positive_scale(cs);
-  const float slack_width = kSlack / cs;
   if (p.scale_log2 < 0.0f) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
@@ -843,14 +855,14 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
   for (int n = 0; n < kTiles; ++n)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
-  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f;
-  float vleast = 0.0f;                                       // the least vlim of the wave's rows
+  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, l = 0.0f;
+  float vleast = 0.0f;                                       // no row's vlim is less (uniform)
 
   // The order of a tile's instructions is spelled out for the scheduler: left
   // to itself it keeps one operand register and waits out the LDS latency
   // before every MFMA (measured 915 us where this order took 834, on 8192 tokens of 32 heads over 8,
   // D = 128).
-  constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100;
+  constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100, kLdsWrite = 0x200;
   auto compute = [&](int buf, int t0) {
     const char *kl = sm.k[buf] + qc * Smem::kKeyRow + 16 * hh;
     const char *vl = sm.v[buf] + qc * Smem::kValueRow + 16 * hh;
@@ -946,15 +958,16 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
         }
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         const float lim = vmax > 0.0f ? __builtin_ldexpf(1.0f, ex) : 0.0f;
-        vexp = lim > vlim ? (float)ex : vexp;
         vlim = fmaxf(vlim, lim);
-        if (!partial) vleast = fmaxf(vleast, lim);           // (every row has seen the tile)
+        if (!partial)                                        // (every row has seen the tile)
+          vleast = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, fmaxf(vleast, lim))));
       }
       // (top * cs is exact, so for logits past_fractions M is off by vexp at most,
       // and 2^(u cs - M) times a step stays an fp16 number)
+      const float vexp = vlim > 0.0f ? (float)((int)(__builtin_bit_cast(uint32_t, vlim) >> 23) - 127) : 0.0f;
       const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
-      slack = past_fractions(M) ? top : top + slack_width;
+      slack = past_fractions(M) ? top : top + kSlack / cs;
       l *= a;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
@@ -1005,21 +1018,25 @@ __global__ __launch_bounds__(kPtThreads, 2) void kv_prompt_kernel(KvAttn p) {
     }
   };
 
-  if (i0 < i1) {
-    load_page(t_lo + kPtKeys * i0);
-    load_codes(t_lo + kPtKeys * i0);
-    load_page(t_lo + kPtKeys * (i0 + 1));
-    stage(0);
+  if (nt > 0) {
+    load_page(t_lo);
+    load_codes(t_lo);
+    load_page(t_lo + kPtKeys);
+    stage_keys(0);
+    stage_values(0);
     __syncthreads();
-    for (int i = i0; i < i1; ++i) {
-      const int t0 = t_lo + kPtKeys * i, buf = (i - i0) & 1;
-      const bool more = i + 1 < i1;
+    for (int i = 0; i < nt; ++i) {
+      const int t0 = t_lo + kPtKeys * i, buf = i & 1;
+      const bool more = i + 1 < nt;
       if (more) {
         load_codes(t0 + kPtKeys);
         load_page(t0 + 2 * kPtKeys);
       }
       if (wave_live && t0 <= w_any_last && t0 + kPtKeys > w_any_first) compute(buf, t0);
-      if (more) stage(buf ^ 1);
+      if (more) {
+        stage_keys(buf ^ 1);
+        stage_values(buf ^ 1);
+      }
       __syncthreads();
     }
   }
