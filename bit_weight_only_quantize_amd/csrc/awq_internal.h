@@ -220,7 +220,7 @@ struct KvAttn {
   int tile_rows;              // rows that share their parts
   float *part_o, *part_lse;   // [splits][T * heads * group][D] and [splits][T * heads * group]
 };
-// Kernel, its tile of rows, waves (decode) and parts of the keys, and the
+// Kernel, its tile of rows, waves per workgroup and parts of the keys, and the
 // workspace of a call.
 struct KvAttnPlan {
   bool prompt;

@@ -660,9 +660,13 @@ void kv_decode_kernel(KvAttn p) {
 // Gflop causal): 720 us from an idle card, 745 repeated, 740 - 765 Tflop/s; the
 // VALU is active 58% of the time, the MFMA 38%, the LDS 48% (a fifth of that
 // conflicts), at the 1.9 - 2.0 GHz that the power limit leaves.  With D = 64 three
-// waves fit a SIMD: 507 and 530 us (two waves 531 and 572).  Six requests of up to
-// 515 new tokens after up to 3000, 16 heads over 4, D = 64: 37 us; there the longest
-// request's 47 tiles, one after another, are the time.
+// waves fit a SIMD: 507 and 530 us (two waves 531 and 572).
+//
+// With NG = 2 a workgroup has two groups of four waves that walk alternate tiles
+// of the same rows, each with buffers of its own, and the second group's sums join
+// the first's through LDS: half the steps for a request, at one workgroup per CU.
+// Six requests of up to 515 new tokens after up to 3000, 16 heads over 4, D = 64:
+// 25.8 us, where the longest request's 47 tiles, one after another, took 37.
 //
 // Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
 // a pipeline of half tiles (1376), the running maximum from a bound in LDS (1115),
@@ -683,14 +687,16 @@ struct PromptSmem {
   float vs[2][kPtKeys];          // value step; -1: no such token
 };
 
-template <int D, bool SYM, bool BF16>
-__global__ __launch_bounds__(kPtThreads, D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttn p) {
+template <int D, bool SYM, bool BF16, int NG>
+__global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv_prompt_kernel(KvAttn p) {
   constexpr int kRows = kPtRows;
   using Smem = PromptSmem<D>;
   constexpr int kSteps = D / 16, kTiles = D / 32;
-  __shared__ __attribute__((aligned(16))) Smem sm;
+  __shared__ __attribute__((aligned(16))) Smem sms[NG];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane((tid >> 6) & 3);
+  const int grp = NG == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
+  Smem &sm = sms[grp];
   const int qc = lane & 31, hh = lane >> 5;
   const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;     // longest rows first
   const int h = blockIdx.y % p.heads, split = blockIdx.y / p.heads, b = blockIdx.z;
@@ -1018,27 +1024,53 @@ __global__ __launch_bounds__(kPtThreads, D == 64 ? 3 : 2) void kv_prompt_kernel(
     }
   };
 
+  // group g of four waves walks the tiles g, g + NG, ...
+  constexpr int kStride = kPtKeys * NG;
   if (nt > 0) {
-    load_page(t_lo);
-    load_codes(t_lo);
-    load_page(t_lo + kPtKeys);
-    stage_keys(0);
-    stage_values(0);
+    const int t_first = t_lo + kPtKeys * grp;
+    if (grp < nt) {
+      load_page(t_first);
+      load_codes(t_first);
+      load_page(t_first + kStride);
+      stage_keys(0);
+      stage_values(0);
+    }
     __syncthreads();
-    for (int i = 0; i < nt; ++i) {
-      const int t0 = t_lo + kPtKeys * i, buf = i & 1;
-      const bool more = i + 1 < nt;
+    for (int s = 0; s * NG < nt; ++s) {
+      const int i = s * NG + grp, t0 = t_lo + kPtKeys * i, buf = s & 1;
+      const bool more = i + NG < nt;
       if (more) {
-        load_codes(t0 + kPtKeys);
-        load_page(t0 + 2 * kPtKeys);
+        load_codes(t0 + kStride);
+        load_page(t0 + 2 * kStride);
       }
-      if (wave_live && t0 <= w_any_last && t0 + kPtKeys > w_any_first) compute(buf, t0);
+      if (wave_live && i < nt && t0 <= w_any_last && t0 + kPtKeys > w_any_first) compute(buf, t0);
       if (more) {
         stage_keys(buf ^ 1);
         stage_values(buf ^ 1);
       }
       __syncthreads();
     }
+  }
+  if constexpr (NG == 2) {                                   // the second group's sums through LDS to the first's waves
+    float *po = reinterpret_cast<float *>(sms) + wave * (16 * kTiles + 2) * 64 + lane;
+    if (grp == 1) {
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) po[(16 * n + e) * 64] = o[n][e];
+      po[16 * kTiles * 64] = M;
+      po[(16 * kTiles + 1) * 64] = l;
+    }
+    __syncthreads();
+    if (grp == 1) return;
+    const float M1 = po[16 * kTiles * 64], m2 = fmaxf(M, M1);
+    const float a0 = __builtin_amdgcn_exp2f(M - m2), a1 = __builtin_amdgcn_exp2f(M1 - m2);
+    M = m2;
+    l = l * a0 + po[(16 * kTiles + 1) * 64] * a1;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) o[n][e] = o[n][e] * a0 + po[(16 * n + e) * 64] * a1;
   }
 
   // ---- store: lane (q, hh) holds LDS rows 32n + 8g + 4hh + e of row q, all
@@ -1170,9 +1202,18 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
   pl.waves = 4;
   int64_t splits;
   if (pl.prompt) {
-    // enough workgroups for every CU's two
-    pl.chunk = 256;
-    splits = wgs > 0 && wgs < 512 ? 512 / wgs : 1;
+    // Fewer workgroups than two per CU: eight waves each, two groups over
+    // alternate tiles, which halves the time of the longest request (six ragged
+    // requests, 408 workgroups of D = 64: 25.8 us against 39.8; seven, 476 of D =
+    // 128: 67 against 107; three of one length, 384, are slower, 87 against 78).
+    // From 512 on four waves serve better (2048 tokens, 32 heads over 8: 84 us
+    // against 93).  Keys are split while there is less than a workgroup per CU, into
+    // parts of 512 keys, or 256 for few rows: the parts' fp32 results are written
+    // and read again (512 tokens of 32 heads: 19.9 us in one part, 29.3 in two; 64
+    // tokens after 936: 19.8 us in four parts, 23.9 in two).
+    pl.chunk = wgs < 64 ? 256 : 512;
+    if (wgs < 512) pl.waves = 8;
+    splits = wgs > 0 && wgs < 256 ? 256 / wgs : 1;
   } else if (span <= 1024 && wgs < 512) {
     // short contexts of few requests: eight waves and no join
     pl.waves = 8;
@@ -1202,7 +1243,8 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   const int64_t rows = (int64_t)p.max_q * p.group;
   if (pl.prompt) {
     const dim3 grid((unsigned)((rows + kPtRows - 1) / kPtRows), (unsigned)(p.heads * p.splits), (unsigned)B);
-    kv_prompt_kernel<D, SYM, BF16><<<grid, kPtThreads, 0, st>>>(p);
+    if (pl.waves == 8) kv_prompt_kernel<D, SYM, BF16, 2><<<grid, 2 * kPtThreads, 0, st>>>(p);
+    else kv_prompt_kernel<D, SYM, BF16, 1><<<grid, kPtThreads, 0, st>>>(p);
   } else {
     const dim3 grid((unsigned)((rows + 15) / 16 * p.heads), (unsigned)p.splits, (unsigned)B);
     if (pl.waves == 8) kv_decode_kernel<D, SYM, BF16, 8><<<grid, 512, 0, st>>>(p);

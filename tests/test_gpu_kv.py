@@ -559,3 +559,23 @@ def test_decode_steps_end_to_end_captured():
         free, old = free[ru[0]:], rl
         s_old.copy_(lens)
         s_free[:len(free)] = _i32(free)
+
+
+@pytest.mark.parametrize("D,kv_lens", [(64, [1, 63, 64, 65, 128, 129, 200, 700]), (128, [64, 130, 190, 260])])
+@pytest.mark.parametrize("requests", [1, 40])
+def test_prompts_of_few_and_many_workgroups(D, kv_lens, requests):
+    """The same requests alone, where two groups of waves share the keys, and
+    among so many that one does; one to a dozen tiles of keys, odd and even."""
+    for n in kv_lens:
+        q = min(n, 150)
+        a = Attend([q] * requests, [n] * requests, 16, 16, D, 64, True, "float16", seed=n)
+        O, _ = a.run()
+        if requests == 1:
+            a.check()
+            a.check(window=70)
+            continue
+        one = Attend([q], [n], 16, 16, D, 64, True, "float16", seed=n)
+        one.Q, one.cache, one.table = a.Q[:q], a.cache, a.table[:1]
+        want, _ = one.run()
+        # the same weights in another order of sums, and of M: a rounding of either output
+        assert (O[:q].float() - want.float()).abs().max().item() <= 2.0 ** -9 * float(want.abs().max())
