@@ -220,10 +220,11 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 // waves took 113; of the present code three waves take 94 and four 90.)
 //
 // Measured there (429.6 MB): 90 us from an idle card, 4.8 TB/s of the 5.0 that a
-// copy reaches, and 103 - 110 repeated back to back, when the card's power limit
+// copy reaches, and 98 - 110 repeated back to back, when the card's power limit
 // lowers the clock: the VALU is active 69% of the time, the MFMA 14%, and memory
 // delivers 1.01 times the bytes.  Four requests of up to 65536 tokens, 64 heads
-// over 8 (158.3 MB, symmetric): 27 us, 5.9 TB/s, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.9 us, which is latency:
+// over 8 (158.3 MB, symmetric): 27 us repeated, when the last-level cache holds
+// part of it, about 35 from memory, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.9 us, which is latency:
 // lengths, table, codes, and the waves' join, one after the other.
 template <int D>
 struct DecodeTile {
@@ -657,16 +658,19 @@ void kv_decode_kernel(KvAttn p) {
 // A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
 //
 // Measured: a prompt of 8192 tokens, 32 heads over 8, D = 128, bfloat16 (550
-// Gflop causal): 720 us from an idle card, 745 repeated, 740 - 765 Tflop/s; the
+// Gflop causal): 700 us from an idle card, 740 repeated, 745 - 785 Tflop/s; the
 // VALU is active 58% of the time, the MFMA 38%, the LDS 48% (a fifth of that
-// conflicts), at the 1.9 - 2.0 GHz that the power limit leaves.  With D = 64 three
+// conflicts).  The two units do run side by side, but the card's power limit
+// then lowers the clock (32x32x16 MFMAs alone run at 1.9 GHz, with seven VALU
+// operations after each at 1.5), so what counts is the work, hardly its order.  With D = 64 three
 // waves fit a SIMD: 507 and 530 us (two waves 531 and 572).
 //
 // With NG = 2 a workgroup has two groups of four waves that walk alternate tiles
 // of the same rows, each with buffers of its own, and the second group's sums join
 // the first's through LDS: half the steps for a request, at one workgroup per CU.
-// Six requests of up to 515 new tokens after up to 3000, 16 heads over 4, D = 64:
-// 25.8 us, where the longest request's 47 tiles, one after another, took 37.
+// Six ragged requests of up to 515 new tokens after up to 3000, window 1000, 16
+// heads over 4, D = 64: 25.8 us where one group took 39.8, with other lengths 35
+// where it took 37.
 //
 // Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
 // a pipeline of half tiles (1376), the running maximum from a bound in LDS (1115),
