@@ -688,7 +688,7 @@ struct PromptSmem {
   char k[2][kPtKeys * kKeyRow];
   char v[2][D * kValueRow];      // row ch * D/8 + word: channel 8 word + ch
   float ks[2][kPtKeys];          // key step * step_scale
-  float vs[2][kPtKeys];          // value step; -1: no such token
+  float vs[2][kPtKeys];          // value step; 0 past the last token, -0 where a page is missing
 };
 
 template <int D, bool SYM, bool BF16, int NG>
@@ -743,6 +743,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   uint32_t kc[kKw], vc[kVt];
   uint32_t ksc = 0, kzz = 0x0808u, vzz[kVt / 2];
   int left = 0;                                              // tokens of the loaded group
+  bool hole = false;                                         // ... which should be there, but have no page
   // (past the last key there is no page: page 0 is read and counts for nothing)
   auto load_page = [&](int t0) {
     const int t = t0 + 16 * wave;
@@ -751,8 +752,10 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   };
   auto load_codes = [&](int t0) {
     int id = __builtin_amdgcn_readfirstlane(page_id);
-    left = (uint32_t)id < (uint32_t)pages ? page_left : 0;
-    if ((uint32_t)id >= (uint32_t)pages) id = 0;
+    const bool none = (uint32_t)id >= (uint32_t)pages;
+    left = none ? 0 : page_left;
+    hole = none && page_left > 0;
+    if (none) id = 0;
     const int off = (t0 + 16 * wave) & pmask;
     const char *kp = codes + (id * code_stride + off * (D / 2));
     const char *vp = kp + code_stride / 2;
@@ -791,9 +794,10 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
     const bool held = (lane >> 2) < left;
     const float vstep = hi_half(ksc);
     sm.ks[buf][kkey] = held ? lo_half(ksc) * step_scale : 0.0f;
-    // (an overflowed step as a finite one too large for fp16, so that the
-    // zero weight of a row that does not see the key stays zero)
-    sm.vs[buf][kkey] = !held ? -1.0f : vstep <= 65504.0f ? vstep : 0x1p127f;
+    // (an infinite or NaN step as a finite one too large for fp16, so that the
+    // zero weight of a row that does not see the key stays zero; steps of written
+    // slots are positive)
+    sm.vs[buf][kkey] = held ? fmaxf(fminf(vstep, 0x1p127f), 0.0f) : hole ? -0.0f : 0.0f;
   };
   auto stage_values = [&](int buf) {
     // word vword of kVt tokens: channel d's codes side by side
@@ -930,16 +934,26 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) vf[0][n] = value_frag(0, n);
     scaled(1);
-    const bool partial = t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last || __any(vstep < 0.0f);
+    const bool holes = __any(__builtin_bit_cast(uint32_t, vstep) == 0x80000000u);
+    const bool partial = t0 < w_all_first || t0 + kPtKeys - 1 > w_all_last || holes;
     if (partial) {
+      // key first <= at <= last, as one unsigned comparison of (at - first)
+      const bool any = my_first <= my_last;
+      const uint32_t first = any ? my_first - t0 - 4 * hh : 0x40000000, span = any ? my_last - my_first : 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int at = t0 + 8 * j + 4 * hh + e;
-          const bool seen = at >= my_first && at <= my_last && v[e] >= 0.0f;
-          u[4 * j + e] = seen ? u[4 * j + e] : -__builtin_inff();
+        for (int e = 0; e < 4; ++e)
+          u[4 * j + e] = 8 * j + e - first <= span ? u[4 * j + e] : -__builtin_inff();
+      if (holes) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float ve = v[e];
+            u[4 * j + e] = __builtin_bit_cast(uint32_t, ve) == 0x80000000u ? -__builtin_inff() : u[4 * j + e];
+          }
         }
       }
     }
@@ -950,22 +964,22 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
       top = fmaxf(top, umax);
       if (__any(vstep > vleast)) {
-        // the largest step of the keys that the row sees (one that overflowed counts for none)
-        float vmax = vstep <= 65504.0f ? vstep : 0.0f;
+        // the largest step of the keys that the row sees
+        float vmax = vstep;
         if (partial) {
           vmax = 0.0f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              vmax = fmaxf(vmax, (u[4 * j + e] > -__builtin_inff()) & (v[e] <= 65504.0f) ? v[e] : 0.0f);
+            for (int e = 0; e < 4; ++e) vmax = fmaxf(vmax, u[4 * j + e] > -__builtin_inff() ? v[e] : 0.0f);
           }
           vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
         } else {
 #pragma unroll
           for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
         }
+        vmax = fminf(vmax, 65504.0f);
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         const float lim = vmax > 0.0f ? __builtin_ldexpf(1.0f, ex) : 0.0f;
         vlim = fmaxf(vlim, lim);

@@ -579,3 +579,21 @@ def test_prompts_of_few_and_many_workgroups(D, kv_lens, requests):
         want, _ = one.run()
         # the same weights in another order of sums, and of M: a rounding of either output
         assert (O[:q].float() - want.float()).abs().max().item() <= 2.0 ** -9 * float(want.abs().max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_any_bits_in_hidden_steps(n, D):
+    """Slots behind a row, before its window, past the last token and in pages
+    that no row names: infinities and NaN of either sign, negative and tiny
+    steps, key and value, leave every row's result within its bound."""
+    bits = np.array([0x7C00, 0xFC00, 0x7E00, 0xFE00, 0xBC00, 0x8000, 0x0001, 0x8001, 0x7BFF, 0xFBFF], np.uint16)
+    a = Attend([n, n], [150 + n, 97 + n], 4, 2, D, 16, True, "float16", seed=22)
+    W = 30
+    for b in range(2):
+        kv_len = int(a.kv_lens[b])
+        first = kv_len - n - W + 1                       # of the first row's window
+        for pos in list(range(first)) + list(range(kv_len, -(-kv_len // 16) * 16)):
+            a.cache[1].view(np.uint16)[a.table[b, pos // 16], :, pos % 16] = \
+                bits[[(pos * 3) % len(bits), (pos * 7 + b) % len(bits)]]
+    a.check(window=W)
