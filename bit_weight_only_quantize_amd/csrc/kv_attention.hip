@@ -52,6 +52,13 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
   return __builtin_bit_cast(uint32_t, h);
 }
 
+// Two bfloat16 values, rounded to nearest even by one instruction.
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 h = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
 // a * (half h of w) with the half widened by the instruction (v_fma_mix_f32).
 __device__ __forceinline__ float mul_lo_half(float a, uint32_t w) { return __builtin_fmaf(a, lo_half(w), 0.0f); }
 __device__ __forceinline__ float mul_hi_half(float a, uint32_t w) { return __builtin_fmaf(a, hi_half(w), 0.0f); }
@@ -1125,8 +1132,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        w[i] = BF16 ? (uint32_t)float_to_bf16_bits(v[2 * i]) | ((uint32_t)float_to_bf16_bits(v[2 * i + 1]) << 16)
-                    : pack_half2(v[2 * i], v[2 * i + 1]);
+        w[i] = BF16 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : pack_half2(v[2 * i], v[2 * i + 1]);
       *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(p.O) + d) = w;
     }
   }
