@@ -228,7 +228,7 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 //
 // Measured there (429.6 MB): 90 us from an idle card, 4.8 TB/s of the 5.0 that a
 // copy reaches, and 98 - 110 repeated back to back, when the card's power limit
-// lowers the clock: the VALU is active 69% of the time, the MFMA 14%, and memory
+// lowers the clock: the VALU is active 76% of the time, the MFMA 15%, and memory
 // delivers 1.01 times the bytes.  Four requests of up to 65536 tokens, 64 heads
 // over 8 (158.3 MB, symmetric): 27 us repeated, when the last-level cache holds
 // part of it, about 35 from memory, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.9 us, which is latency:
@@ -665,7 +665,8 @@ void kv_decode_kernel(KvAttn p) {
 // A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
 //
 // Measured: a prompt of 8192 tokens, 32 heads over 8, D = 128, bfloat16 (550
-// Gflop causal): 700 us from an idle card, 740 repeated, 745 - 785 Tflop/s; the
+// Gflop causal): 700 - 735 us from an idle card, 725 - 770 repeated, by the card's
+// power, 715 - 785 Tflop/s; the
 // VALU is active 58% of the time, the MFMA 38%, the LDS 48% (a fifth of that
 // conflicts).  The two units do run side by side, but the card's power limit
 // then lowers the clock (32x32x16 MFMAs alone run at 1.9 GHz, with seven VALU
@@ -676,7 +677,7 @@ void kv_decode_kernel(KvAttn p) {
 // of the same rows, each with buffers of its own, and the second group's sums join
 // the first's through LDS: half the steps for a request, at one workgroup per CU.
 // Six ragged requests of up to 515 new tokens after up to 3000, window 1000, 16
-// heads over 4, D = 64: 25.8 us where one group took 39.8, with other lengths 35
+// heads over 4, D = 64: 25.8 us where one group took 39.8, with other lengths 33.6
 // where it took 37.
 //
 // Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
