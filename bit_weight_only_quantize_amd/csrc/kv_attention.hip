@@ -1239,10 +1239,13 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
     pl.chunk = wgs < 64 ? 256 : 512;
     if (wgs < 512) pl.waves = 8;
     splits = wgs > 0 && wgs < 256 ? 256 / wgs : 1;
-  } else if (span <= 1024 && wgs < 512) {
-    // short contexts of few requests: eight waves and no join
+  } else if (span <= 1536 && wgs < 512) {
+    // Short contexts of few requests: eight waves and no join, which costs a launch
+    // (1500 tokens, 32 heads over 8: one request 16.2 -> 13.0 us a call, in a graph
+    // 11.6 -> 12.5; sixteen 16.8 -> 13.7 and 14.8 -> 13.3).  Later the waves' own
+    // steps cost more (2048 tokens, one request: 11.4 us in a graph, 15.0 with eight).
     pl.waves = 8;
-    pl.chunk = 1024;
+    pl.chunk = 1536;
     splits = 1;
   } else {
     // four workgroups to a CU; with as many rows as that anyway, two parts for
