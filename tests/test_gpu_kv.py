@@ -597,3 +597,41 @@ def test_any_bits_in_hidden_steps(n, D):
             a.cache[1].view(np.uint16)[a.table[b, pos // 16], :, pos % 16] = \
                 bits[[(pos * 3) % len(bits), (pos * 7 + b) % len(bits)]]
     a.check(window=W)
+
+
+def test_two_graphs_and_two_streams_at_once():
+    """Two captured attention calls over one cache, each with splits and its own
+    scratch, replayed side by side on two streams and in turn: the eager results."""
+    import bit_weight_only_quantize_amd as awq
+    torch = torch_mod()
+    a = Attend([1, 1], [5000, 3300], 4, 2, 64, 16, True, "float16", seed=23)
+    b = Attend([64], [5000], 4, 2, 64, 16, True, "float16", seed=23)
+    cache = _to_cache(a.cache)
+    table, lens = _i32(a.table), _i32(a.kv_lens)
+    start = _i32([0, 64])
+    calls = (lambda: awq.awq_kv_attention(a.Q, cache, table, lens, max_seq_len=5000),
+             lambda: awq.awq_kv_attention(b.Q, cache, table[:1], lens[:1], query_start=start, max_query_len=64,
+                                          max_seq_len=5000))
+    want = [f() for f in calls]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for f in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(f())
+        graphs.append(g)
+    for i in range(6):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        if i % 2:
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        else:
+            for g in graphs:
+                g.replay()
+        eager = [f() for f in calls]
+        torch.cuda.synchronize()
+        for o, e, w in zip(outs, eager, want):
+            assert torch.equal(o, w) and torch.equal(e, w)
