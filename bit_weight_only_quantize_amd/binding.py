@@ -504,7 +504,9 @@ def awq_linear_epilogue(X, qweight, scales, zeros, bias=None, residual=None,
         _check(bias, "bias", odt, (N,))
     if residual is not None:
         _check(residual, "residual", odt, (M, N))
-    xd, cfg = _dtype_code(X.dtype), config(group_size, zero_point=zeros is not None)
+    xd = _dtype_code(X.dtype)
+    od = xd if odt is X.dtype else _dtype_code(odt)
+    cfg = _CONFIGS.get((group_size, zeros is not None)) or config(group_size, zero_point=zeros is not None)
     need = 0 if workspace is None else lib.awq_linear_workspace_size(M, N, K, cfg, xd, kernel)
     ws, ws_bytes = _scratch(workspace, need, X)
     dev = _one_gpu((X, "X"), (qweight, "qweight"), (scales, "scales"),
@@ -516,7 +518,7 @@ def awq_linear_epilogue(X, qweight, scales, zeros, bias=None, residual=None,
         out = X.new_empty((M, N), dtype=odt)
     st = _launch(lib.awq_linear_epilogue, dev, _address(X), xd, _address(qweight), _address(scales),
                  _address(zeros), M, N, K, cfg, awq_epilogue(_address(bias), _address(residual), act),
-                 _address(out), _dtype_code(odt), kernel, _address(ws), ws_bytes)
+                 _address(out), od, kernel, _address(ws), ws_bytes)
     check(st, "awq_linear_epilogue")
     return out
 

@@ -254,6 +254,8 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
   p.pshift = __builtin_ctz((unsigned)cache->page_size);
   p.heads = cache->num_kv_heads;
   p.group = group;
+  p.by_heads = make_divisor(cache->num_kv_heads);
+  p.by_group = make_divisor(group);
   p.table = block_table;
   p.max_blocks = max_blocks;
   p.seq_lens = seq_lens;

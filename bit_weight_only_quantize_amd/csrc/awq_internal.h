@@ -201,6 +201,19 @@ hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int64_t T, v
 
 // ---- kv_attention.hip -------------------------------------------------------------
 // Arguments of one attention call (from `splits` on the launcher's).
+// Division of x < 2^30 by d in [1, 1024] as one multiplication: with 2^L <= d < 2^(L+1)
+// and m = floor(2^(31+L) / d) + 1, floor(x m / 2^(31+L)) = floor(x / d), because
+// 0 < m d - 2^(31+L) <= d and so x (m d - 2^(31+L)) < 2^30 2^(L+1) = 2^(31+L).
+struct Divisor {
+  uint32_t m;
+  int shift;
+};
+inline Divisor make_divisor(int d) {
+  int L = 0;
+  while ((2 << L) <= d) ++L;
+  return Divisor{(uint32_t)(((uint64_t)1 << (31 + L)) / (uint32_t)d + 1), 31 + L};
+}
+
 struct KvAttn {
   const uint16_t *Q;
   int64_t q_stride;           // elements between query tokens
@@ -211,6 +224,7 @@ struct KvAttn {
   const uint8_t *zeros;
   int64_t pages, T;
   int pshift, heads, group;   // log2 of the page size; key/value heads; query heads per each
+  Divisor by_heads, by_group;
   const int32_t *table;
   int max_blocks;
   const int32_t *seq_lens, *query_start;

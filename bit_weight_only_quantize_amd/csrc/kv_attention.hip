@@ -171,6 +171,12 @@ __device__ __forceinline__ Request request_of(const KvAttn &p, int b) {
   r.kv = (int)(n < 0 ? 0 : n > cap ? cap : n);
   return r;
 }
+__device__ __forceinline__ int divide(int x, Divisor d) {
+  return (int)(((uint64_t)(uint32_t)x * d.m) >> d.shift);
+}
+// Query token of row r.
+__device__ __forceinline__ int token_of(const KvAttn &p, int r) { return divide(r, p.by_group); }
+
 // Last key that query token qi sees, and the first (the window's start).
 __device__ __forceinline__ int last_key(const KvAttn &p, const Request &r, int qi) {
   return p.causal ? r.kv - r.qn + qi : r.kv - 1;
@@ -188,9 +194,14 @@ struct Keys {
 };
 __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int row0, int row1, int align) {
   Keys k;
-  k.lo = first_key(p, last_key(p, r, row0 / p.group)) & -align;
-  k.end = last_key(p, r, row1 / p.group) + 1;
+  k.lo = first_key(p, last_key(p, r, token_of(p, row0))) & -align;
+  k.end = last_key(p, r, token_of(p, row1)) + 1;
   const int n = k.end > k.lo ? k.end - k.lo : 1;
+  if (p.splits == 1) {                               // (no divisions on the way to the first load)
+    k.each = (n + 63) & -64;
+    k.parts = 1;
+    return k;
+  }
   const int most = (n - 1) / p.chunk + 1;
   const int want = most < p.splits ? most : p.splits;
   k.each = ((n - 1) / want + 64) & -64;
@@ -231,7 +242,7 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 // lowers the clock: the VALU is active 76% of the time, the MFMA 15%, and memory
 // delivers 1.01 times the bytes.  Four requests of up to 65536 tokens, 64 heads
 // over 8 (158.3 MB, symmetric): 27 us repeated, when the last-level cache holds
-// part of it, about 35 from memory, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.9 us, which is latency:
+// part of it, about 35 from memory, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.5 us in a graph, which is latency:
 // lengths, table, codes, and the waves' join, one after the other.
 template <int D>
 struct DecodeTile {
@@ -259,14 +270,15 @@ void kv_decode_kernel(KvAttn p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, kq = lane >> 4;
-  const int h = blockIdx.x % p.heads, row0 = (int)(blockIdx.x / p.heads) * 16;
+  const int row_tile = divide(blockIdx.x, p.by_heads);
+  const int h = (int)blockIdx.x - row_tile * p.heads, row0 = row_tile * 16;
   const int split = blockIdx.y, b = blockIdx.z;
   const Request rq = request_of(p, b);
   const int rows = rq.ql * p.group;
   if (row0 >= rows) return;
   const int row_last = row0 + 15 < rows ? row0 + 15 : rows - 1;
   const int row = row0 + c < rows ? row0 + c : rows - 1;
-  const int qi = row / p.group;
+  const int qi = token_of(p, row);
   const int32_t *table = p.table + (int64_t)b * p.max_blocks;
   int page_base = 0;
   int32_t page_ids = -1;                             // lane i: page page_base + i of the request
@@ -281,14 +293,14 @@ void kv_decode_kernel(KvAttn p) {
   // queries: lane (c, kq) holds channels 32kq.. (D = 128) or 16kq.. (D = 64)
   // of row c, the channels of the key words that it will load
   const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
-                       (int64_t)(h * p.group + row % p.group) * D + kq * (8 * kWords);
+                       (int64_t)(h * p.group + row - qi * p.group) * D + kq * (8 * kWords);
   u32x4 q[kWords];
 #pragma unroll
   for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
   const int my_last = last_key(p, rq, qi), my_first = first_key(p, my_last);
   // keys that all rows see
-  const int all_last = last_key(p, rq, row0 / p.group);
-  const int all_first = first_key(p, last_key(p, rq, row_last / p.group));
+  const int all_last = last_key(p, rq, token_of(p, row0));
+  const int all_first = first_key(p, last_key(p, rq, token_of(p, row_last)));
   const Keys keys = keys_of(p, rq, row0, row_last, 32);
   if (split >= keys.parts) return;
   const int t_lo = keys.lo + split * keys.each;
@@ -630,8 +642,8 @@ void kv_decode_kernel(KvAttn p) {
   const float inv = none ? 0.0f : 1.0f / sum;
   const float lse2 = none ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
   const int rr = row0 + r;
-  const int64_t head_row = (rq.token0 + rr / p.group) * ((int64_t)p.heads * p.group) +
-                           h * p.group + rr % p.group;
+  const int rqi = token_of(p, rr);
+  const int64_t head_row = (rq.token0 + rqi) * ((int64_t)p.heads * p.group) + h * p.group + rr - rqi * p.group;
   if (keys.parts > 1) {
     const int64_t at = split * p.T * p.heads * p.group + head_row;
     float *po = p.part_o + at * D + d0;
@@ -677,7 +689,7 @@ void kv_decode_kernel(KvAttn p) {
 // of the same rows, each with buffers of its own, and the second group's sums join
 // the first's through LDS: half the steps for a request, at one workgroup per CU.
 // Six ragged requests of up to 515 new tokens after up to 3000, window 1000, 16
-// heads over 4, D = 64: 25.8 us where one group took 39.8, with other lengths 33.6
+// heads over 4, D = 64: 25.8 us where one group took 39.8, with other lengths 31.8
 // where it took 37.
 //
 // Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
@@ -711,7 +723,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   Smem &sm = sms[grp];
   const int qc = lane & 31, hh = lane >> 5;
   const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;     // longest rows first
-  const int h = blockIdx.y % p.heads, split = blockIdx.y / p.heads, b = blockIdx.z;
+  const int split = divide(blockIdx.y, p.by_heads), h = (int)blockIdx.y - split * p.heads, b = blockIdx.z;
   const Request rq = request_of(p, b);
   const int rows = rq.ql * p.group, row0 = tile * kRows;
   if (row0 >= rows) return;
@@ -719,10 +731,10 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   const int wrow0 = clamp_row(row0 + wave * 32), wrow1 = clamp_row(row0 + wave * 32 + 31);
   const int row = clamp_row(row0 + wave * 32 + qc);
   const bool wave_live = row0 + wave * 32 < rows;
-  const int qi = row / p.group;
+  const int qi = token_of(p, row);
   const int my_last = last_key(p, rq, qi), my_first = first_key(p, my_last);
-  const int w_any_last = last_key(p, rq, wrow1 / p.group);
-  const int w_all_last = last_key(p, rq, wrow0 / p.group);
+  const int w_any_last = last_key(p, rq, token_of(p, wrow1));
+  const int w_all_last = last_key(p, rq, token_of(p, wrow0));
   const int w_any_first = first_key(p, w_all_last), w_all_first = first_key(p, w_any_last);
   const Keys keys = keys_of(p, rq, row0, clamp_row(row0 + kRows - 1), kPtKeys);
   if (split >= keys.parts) return;
@@ -846,7 +858,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   // ---- queries, and the power of two of their logits in the exponent
   float cs = row_scale;
   const uint16_t *qp = p.Q + (rq.token0 + qi) * p.q_stride +
-                       (int64_t)(h * p.group + row % p.group) * D + 8 * hh;
+                       (int64_t)(h * p.group + row - qi * p.group) * D + 8 * hh;
   u32x4 q[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
@@ -1106,7 +1118,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   const bool none = l == 0.0f;
   const float inv = none ? 0.0f : 1.0f / l;
   const float lse2 = none ? -__builtin_inff() : M + __builtin_amdgcn_logf(l);
-  const int64_t head_row = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + row % p.group;
+  const int64_t head_row = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + row - qi * p.group;
   const int64_t at = keys.parts > 1 ? split * p.T * p.heads * p.group + head_row : head_row;
   if (keys.parts > 1) {
     if (hh == 0) p.part_lse[at] = lse2;
@@ -1166,7 +1178,8 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
   const int parts = keys_of(p, rq, row0, row1, p.tile_rows == 16 ? 32 : kPtKeys).parts;
   if (parts == 1) return;                            // stored by its one workgroup
   const int64_t n = p.T * p.heads * p.group;
-  const int64_t at = (rq.token0 + r / p.group) * ((int64_t)p.heads * p.group) + h * p.group + r % p.group;
+  const int qi = token_of(p, r);
+  const int64_t at = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + r - qi * p.group;
   const float x = lane < parts ? p.part_lse[lane * n + at] : -__builtin_inff();
   float m = x;
 #pragma unroll
