@@ -327,7 +327,11 @@ void kv_decode_kernel(KvAttn p) {
   const float f = half_range_factor(qmax);
   // (negated for a negative scale, so that larger sums are larger logits)
   const float fs = p.scale_log2 < 0.0f ? -f : f;
-  const float cs = positive_scale(__builtin_fabsf(p.scale_log2) * (1.0f / f) * 0x1p24f);
+  const float abs_scale = __builtin_fabsf(p.scale_log2);
+  // (bfloat16 queries near the end of their range, where this factor would pass
+  // fp32's: the sums then take 2^60 of it, in all rows alike)
+  const bool wide = __any(abs_scale * (1.0f / f) * 0x1p24f > __FLT_MAX__);
+  const float cs = positive_scale(wide ? abs_scale * 0x1p-36f * (1.0f / f) : abs_scale * (1.0f / f) * 0x1p24f);
   // sum of the row's queries, for the zero points: sum q (code - z) = sum q code - z sum q
   float qsum = 0.0f;
 #pragma unroll
@@ -466,16 +470,25 @@ void kv_decode_kernel(KvAttn p) {
         }
         u[4 * i + e] = mul_lo_half(x, w);
       }
-    if (at.bad || t < all_first || t + 31 > all_last) {
+    if (wide) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 8; ++i) u[i] *= 0x1p60f;
+    }
+    if (at.bad || t < all_first || t + 31 > all_last) {
+      // key first <= e <= last, as one unsigned comparison of (e - first).  (The three
+      // conditions joined by && became branches per lane for one element, and with
+      // them the compiler has lost that element's -inf.)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bool any = (my_first <= my_last) & (((at.bad >> i) & 1u) == 0u);
+        const uint32_t first = any ? my_first - t - 16 * i - 4 * kq : 0x40000000, span = any ? my_last - my_first : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int k = t + 16 * i + 4 * kq + e;
-          const bool seen = k >= my_first && k <= my_last && !((at.bad >> i) & 1u);
+          const bool seen = e - first <= span;
           u[4 * i + e] = seen ? u[4 * i + e] : -__builtin_inff();
           T.sc[i][e] = seen ? T.sc[i][e] : 0u;
         }
+      }
     }
     float umax = u[0];
     uint32_t smax = T.sc[0][0];
@@ -801,10 +814,14 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   };
   const DeqRegs dq;
   // scale * log2(e) = step_scale * row_scale: the mantissa goes into the key steps
-  // in LDS, the power of two (and the inverse of the row's factor) into the exponent
+  // in LDS, the power of two (and the inverse of the row's factor) into the exponent;
+  // of a scale above 1, up to 2^60 into the steps too, so that the rest times the
+  // inverse factor (at most 2^113) is a number
   const uint32_t scale_bits = __builtin_bit_cast(uint32_t, __builtin_fabsf(p.scale_log2));
-  const float step_scale = __builtin_bit_cast(float, (scale_bits & 0x007FFFFFu) | 0x3F800000u);
-  const float row_scale = __builtin_bit_cast(float, scale_bits & 0x7F800000u);
+  const int above = (int)(scale_bits >> 23) - 127;
+  const uint32_t kept = (uint32_t)(above < 0 ? 0 : above > 60 ? 60 : above) << 23;
+  const float step_scale = __builtin_bit_cast(float, (scale_bits & 0x007FFFFFu) | (0x3F800000u + kept));
+  const float row_scale = __builtin_bit_cast(float, (scale_bits & 0x7F800000u) - kept);
   auto stage_keys = [&](int buf) {
     const DeqF16 deq(kzz & 0xFFu);
 #pragma unroll

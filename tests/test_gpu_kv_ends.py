@@ -1,0 +1,117 @@
+"""GPU parity of the 4-bit key/value cache at its ends: keys just outside what a
+row sees, in every variant of the attention kernels; queries and logits near
+fp32's limits."""
+
+import numpy as np
+import pytest
+
+from gpu_common import out_to_f64, torch_mod
+from oracle import kv
+from test_gpu_kv import Attend, _i32, _rounded, _to_cache
+
+pytestmark = pytest.mark.gpu
+
+EPS = {"float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}
+
+
+class Request(Attend):
+    """A batch whose keys, values and queries a test sets itself."""
+
+    def put(self, b, pos, K, V):
+        """K, V fp32 [n][heads][D] as the tokens at positions `pos` of request b."""
+        pos = np.asarray(pos)
+        kv.append(self.cache, np.asarray(K, np.float32), np.asarray(V, np.float32),
+                  self.table[b, pos // self.page] * self.page + pos % self.page)
+
+    def ask(self, Q):
+        self.Q, q32 = _rounded(Q, self.dtype)
+        self.q64 = q32.astype(np.float64)
+
+    def tokens(self, b):
+        """kv.read of all of request b's tokens."""
+        pos = np.arange(int(self.kv_lens[b]))
+        return kv.read(self.cache, self.D, self.table[b, pos // self.page] * self.page + pos % self.page)
+
+    def answer(self, max_seq_len=None, **kw):
+        """The output in fp64, for one query token per request or several."""
+        import bit_weight_only_quantize_amd as awq
+        one = (self.q_lens == 1).all()
+        return awq.awq_kv_attention(self.Q, _to_cache(self.cache), _i32(self.table), _i32(self.kv_lens),
+                                    query_start=None if one else _i32(self.start),
+                                    max_query_len=int(self.q_lens.max()), return_lse=True,
+                                    max_seq_len=int(max(self.kv_lens)) if max_seq_len is None else max_seq_len, **kw)
+
+
+# ---- keys outside what a row sees --------------------------------------------------
+
+@pytest.mark.parametrize("n,most", [(1, None), (1, 100000), (3, None), (3, 100000), (20, None)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("zp", [True, False])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_hidden_keys_of_every_variant(n, most, D, zp, dtype):
+    """Every kernel variant (eight waves, four waves with parts, prompt), every
+    place in a tile where a row's keys may end or begin: keys that a row does not
+    see would take all of its weight."""
+    for first in (33, 41):
+        lens = [first + i * 17 for i in range(16)]
+        a = Request([n] * 16, lens, 4, 2, D, 16, zp, dtype, seed=37)
+        steps = a.cache[1].view(np.uint16)
+        for b, L in enumerate(lens):                        # past the last token
+            for pos in range(L, -(-L // 16) * 16):
+                steps[a.table[b, pos // 16], :, pos % 16] = 0x7800      # 32768
+        _check_hidden(a, most)
+        for b, L in enumerate(lens):                        # before every row's window
+            for pos in range(L - n - 9):
+                steps[a.table[b, pos // 16], :, pos % 16] = 0x7800
+        _check_hidden(a, most, 10)
+
+
+def _check_hidden(a, most, window=0):
+    O, lse = a.answer(max_seq_len=most, window=window)
+    want, wl, bound, lse_bound = kv.attention64(a.q64, a.cache, a.table, a.kv_lens, a.start, a.D ** -0.5, True, window,
+                                                EPS[a.dtype])
+    assert (np.abs(out_to_f64(O) - want) <= bound).all()
+    assert (np.abs(lse.cpu().numpy() - wl) <= lse_bound).all()
+
+
+# ---- near fp32's limits ------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gain,scale", [(2.0 ** 120, 0.125), (2.0 ** 121, 0.125), (2.0 ** 123, 0.125),
+                                        (2.0 ** 124, 2.0 ** -6), (2.0 ** 100, 2.0 ** 20)])
+def test_largest_bfloat16_queries(n, D, gain, scale):
+    """Finite logits up to 2^127 give finite results: those of the keys whose
+    logits fp32 cannot tell from the largest."""
+    a = Request([n], [100], 4, 2, D, 16, True, "bfloat16", seed=31)
+    a.Q = (a.Q.float() * gain).to(a.Q.dtype)
+    a.q64 = out_to_f64(a.Q)
+    for s in (scale, -scale):
+        _check_hull(a, s)
+
+
+def _check_hull(a, scale):
+    """O between the least and the largest value of the keys whose logits lie
+    within fp32's error of the row's largest.  A logit's error is at most dl (D
+    products, the zero term, the scaling: attention64), so a key more than 2 dl +
+    40 below the largest has a weight below e^-40 of it.  Beside that the weights'
+    rounding 2^-11 and the output's."""
+    O, lse = a.answer(scale=scale)
+    got = out_to_f64(O)
+    assert np.isfinite(got).all() and torch_mod().isfinite(lse).all()
+    heads, Hkv = a.Q.shape[1], a.cache[1].shape[1]
+    for b in range(len(a.kv_lens)):
+        c, z, s, val = a.tokens(b)
+        for i in range(int(a.q_lens[b])):
+            seen = int(a.kv_lens[b]) - int(a.q_lens[b]) + i + 1
+            for j in range(heads):
+                h, q = j * Hkv // heads, a.q64[a.start[b] + i, j]
+                logit = (val[0, :seen, h] @ q) * scale
+                mag = s[0, :seen, h] * ((c[0, :seen, h] + z[0, :seen, h][:, None] + 16) @ np.abs(q))
+                dl = (a.D + 8) * 2.0 ** -24 * abs(scale) * mag.max()
+                near = np.flatnonzero(logit >= logit.max() - 2 * dl - 40)
+                v = val[1, near, h]
+                tol = (EPS[a.dtype] + 2.0 ** -11) * np.abs(v).max(0) + 2.0 ** -11 * (
+                    s[1, near, h][:, None] * np.abs(c[1, near, h])).max(0) + 2.0 ** -24
+                o = got[a.start[b] + i, j]
+                assert (o >= v.min(0) - tol).all() and (o <= v.max(0) + tol).all(), (b, i, j)
