@@ -232,14 +232,16 @@ struct KvAttn {
   float scale_log2;           // softmax scale * log2(e)
   int splits, chunk;          // at most this many parts of a row's keys, of this length
   int tile_rows;              // rows that share their parts
-  float *part_o, *part_lse;   // [splits][T * heads * group][D] and [splits][T * heads * group]
+  float *part_o;              // [splits][T * heads * group][D], normalized
+  double *part_ref;           // [splits][T * heads * group]: weights are relative to 2^this
+  float *part_sum;            // likewise: their sum, 0 where a part holds no key of the row
 };
 // Kernel, its tile of rows, waves per workgroup and parts of the keys, and the
 // workspace of a call.
 struct KvAttnPlan {
   bool prompt;
   int tile_rows, waves, chunk, splits;
-  size_t lse_offset, workspace_bytes;   // 0 when splits == 1
+  size_t ref_offset, sum_offset, workspace_bytes;   // 0 when splits == 1
 };
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
                              int window);

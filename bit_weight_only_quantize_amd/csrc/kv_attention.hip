@@ -142,10 +142,26 @@ __device__ __forceinline__ float running_max(float top, float cs, float vexp) {
   return top == kNone ? kNone : __builtin_fmaf(top, cs, vexp);
 }
 
-// Logits so large that fp32 does not hold their fractions.  M is then not
-// top * cs + vexp to within a factor of two in 2^M, so weights are taken
-// relative to the largest logit itself, and no logit may exceed it.
-__device__ __forceinline__ bool past_fractions(float M) { return __builtin_fabsf(M) >= 0x1p24f && M != kNone; }
+// Logits so large that fp32 does not hold their fractions (top: the row's largest,
+// cs its factor).  Nothing can then be added to them: weights are taken relative
+// to the largest logit itself, and no logit may exceed it.
+__device__ __forceinline__ bool past_fractions(float top, float cs) {
+  return top != kNone && __builtin_fabsf(top * cs) >= 0x1p24f;
+}
+// What the decode kernel's weights are relative to, 2^reference: exact in fp64, so
+// that the rescaling and the joins of waves and parts shift sums by just the
+// difference of their references, whatever the logits' size.
+__device__ __forceinline__ double reference(float top, float cs, float M) {
+  return past_fractions(top, cs) ? (double)top * cs : (double)M;
+}
+__device__ __forceinline__ float exp2_difference(double a, double b) {
+  return __builtin_amdgcn_exp2f((float)(a - b));
+}
+
+// ln (2^reference * sum)
+__device__ __forceinline__ float natural_log(double reference, float sum) {
+  return ((float)reference + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+}
 
 // What a workgroup knows about its request.
 struct Request {
@@ -265,7 +281,8 @@ void kv_decode_kernel(KvAttn p) {
   constexpr int kWords = D / 32, kTiles = D / 16;
   constexpr int kRow = D + 4;                        // floats per row in LDS
   __shared__ __attribute__((aligned(16))) float red[NW][16][kRow];
-  __shared__ float red_m[NW][16], red_l[NW][16];
+  __shared__ double red_m[NW][16];
+  __shared__ float red_l[NW][16];
   __shared__ u32x4 sq[kWords][64];                   // the queries as MFMA operands, per lane
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -424,7 +441,8 @@ void kv_decode_kernel(KvAttn p) {
   f32x4 o[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // M = top * cs + vexp, top the largest sum so far (times the key's step), 2^vexp = vlim
+  // M = top * cs + vexp, top the largest sum so far (times the key's step), 2^vexp = vlim;
+  // for a row past_fractions, top * cs
   float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f, pz = 0.0f;
   const float slack_width = kSlack / cs;
   bool any_past = false;                             // a row of the wave is past_fractions (uniform)
@@ -510,15 +528,16 @@ void kv_decode_kernel(KvAttn p) {
       }
       vmax = fmaxf(vmax, __shfl_xor(vmax, 16, 64));
       vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
+      const double before = reference(top, cs, M);
       top = fmaxf(top, umax);
       if (vmax > vlim) {
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         vexp = (float)ex;
         vlim = __builtin_ldexpf(1.0f, ex);
       }
-      const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
-      M = m2;
-      const bool past = past_fractions(M);
+      const bool past = past_fractions(top, cs);
+      M = past ? top * cs : running_max(top, cs, vexp);
+      const float a = exp2_difference(before, reference(top, cs, M));
       slack = past ? top : top + slack_width;
       any_past = __any(past);
       l *= a;
@@ -530,10 +549,10 @@ void kv_decode_kernel(KvAttn p) {
     }
     float ref = M;
     if (any_past) {
-      const bool past = past_fractions(M);
+      const bool past = past_fractions(top, cs);
 #pragma unroll
       for (int i = 0; i < 8; ++i) u[i] -= past ? top : 0.0f;
-      ref = past ? vexp : M;
+      ref = past ? 0.0f : M;
     }
     u32x4 pb;
 #pragma unroll
@@ -633,27 +652,26 @@ void kv_decode_kernel(KvAttn p) {
       red[wave][c][d] = o[n][e] * (n & 1 ? 0x1p20f : 0x1p24f) - pz;
     }
   if (kq == 0) {
-    red_m[wave][c] = M;
+    red_m[wave][c] = reference(top, cs, M);
     red_l[wave][c] = l;
   }
   __syncthreads();
   constexpr int kPer = D / (4 * NW);                 // channels per thread
   const int r = tid / (4 * NW), d0 = (tid % (4 * NW)) * kPer;
   if (row0 + r >= rows) return;
-  float m = red_m[0][r];
+  double m = red_m[0][r];
 #pragma unroll
-  for (int w = 1; w < NW; ++w) m = fmaxf(m, red_m[w][r]);
+  for (int w = 1; w < NW; ++w) m = fmax(m, red_m[w][r]);
   float sum = 0.0f, acc[kPer] = {};
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const float a = __builtin_amdgcn_exp2f(red_m[w][r] - m);
+    const float a = exp2_difference(red_m[w][r], m);
     sum = __builtin_fmaf(red_l[w][r], a, sum);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = __builtin_fmaf(red[w][r][d0 + i], a, acc[i]);
   }
   const bool none = sum == 0.0f;                     // the row sees no key
   const float inv = none ? 0.0f : 1.0f / sum;
-  const float lse2 = none ? -__builtin_inff() : m + __builtin_amdgcn_logf(sum);
   const int rr = row0 + r;
   const int rqi = token_of(p, rr);
   const int64_t head_row = (rq.token0 + rqi) * ((int64_t)p.heads * p.group) + h * p.group + rr - rqi * p.group;
@@ -664,7 +682,10 @@ void kv_decode_kernel(KvAttn p) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) po[i] = acc[i] * inv;
     }
-    if (d0 == 0) p.part_lse[at] = lse2;
+    if (d0 == 0) {
+      p.part_ref[at] = m;
+      p.part_sum[at] = sum;
+    }
     return;
   }
 #pragma unroll
@@ -673,7 +694,7 @@ void kv_decode_kernel(KvAttn p) {
     if constexpr (BF16) reinterpret_cast<uint16_t *>(p.O)[head_row * D + d0 + i] = float_to_bf16_bits(v);
     else reinterpret_cast<uint16_t *>(p.O)[head_row * D + d0 + i] = float_to_half_bits(v);
   }
-  if (p.lse && d0 == 0) p.lse[head_row] = lse2 * 0.69314718055994531f;
+  if (p.lse && d0 == 0) p.lse[head_row] = none ? -__builtin_inff() : natural_log(m, sum);
 }
 
 // ---- many query rows: the prompt kernel --------------------------------------------------------
@@ -1028,7 +1049,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       const float vexp = vlim > 0.0f ? (float)((int)(__builtin_bit_cast(uint32_t, vlim) >> 23) - 127) : 0.0f;
       const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
       M = m2;
-      slack = past_fractions(M) ? top : top + kSlack / cs;
+      slack = past_fractions(top, cs) ? top : top + kSlack / cs;
       l *= a;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
@@ -1134,14 +1155,16 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   if (row0 + wave * 32 + qc >= rows) return;
   const bool none = l == 0.0f;
   const float inv = none ? 0.0f : 1.0f / l;
-  const float lse2 = none ? -__builtin_inff() : M + __builtin_amdgcn_logf(l);
   const int64_t head_row = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + row - qi * p.group;
   const int64_t at = keys.parts > 1 ? split * p.T * p.heads * p.group + head_row : head_row;
   if (keys.parts > 1) {
-    if (hh == 0) p.part_lse[at] = lse2;
+    if (hh == 0) {
+      p.part_ref[at] = M;
+      p.part_sum[at] = l;
+    }
     if (none) return;
   } else if (p.lse && hh == 0) {
-    p.lse[at] = lse2 * 0.69314718055994531f;
+    p.lse[at] = none ? -__builtin_inff() : natural_log(M, l);
   }
 #pragma unroll
   for (int x = 0; x < D / 16; ++x) {
@@ -1169,15 +1192,16 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
 }
 
 // ---- join the splits ---------------------------------------------------------------------------
-// Row (token, head): weights 2^(lse_s - max lse) over at most kMaxSplits splits,
-// WPR waves of a workgroup of four per row: lane s reads split s's lse, wave w of
-// the row sums the splits s = w mod WPR, their rows loaded eight at a time, and
-// the waves' sums meet in LDS.  (Many splits of few rows, a decode step's, want
-// the waves on one row: 32 splits of 256 rows took one wave per row 24 us, four
-// 4.  Few splits of many rows, a prompt's, want a wave each: 2 splits of 12360
-// rows of 64 took four waves per row 38 us.)  A split in which the row saw no
-// key has written -inf and no O.  Rows that no request serves were not written
-// and are not read.
+// Row (token, head): weights 2^(reference_s - the largest) sum_s over at most
+// kMaxSplits splits (kept apart: in one logarithm a large reference would swallow
+// the sum), WPR waves of a workgroup of four per row: lane s reads split s's
+// reference and sum, wave w of the row sums the splits s = w mod WPR, their rows
+// loaded eight at a time, and the waves' sums meet in LDS.  (Many splits of few
+// rows, a decode step's, want the waves on one row: 32 splits of 256 rows took one
+// wave per row 24 us, four 4.  Few splits of many rows, a prompt's, want a wave
+// each: 2 splits of 12360 rows of 64 took four waves per row 38 us.)  A split in
+// which the row saw no key has written a sum of 0 and no O.  Rows that no request
+// serves were not written and are not read.
 constexpr int kMaxSplits = 64;
 
 template <int D, bool BF16, int WPR>
@@ -1197,11 +1221,12 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
   const int64_t n = p.T * p.heads * p.group;
   const int qi = token_of(p, r);
   const int64_t at = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + r - qi * p.group;
-  const float x = lane < parts ? p.part_lse[lane * n + at] : -__builtin_inff();
-  float m = x;
+  const float l = lane < parts ? p.part_sum[lane * n + at] : 0.0f;
+  const double x = l != 0.0f ? p.part_ref[lane * n + at] : -__builtin_inf();
+  double m = x;
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-  const float w = x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x - m);
+  for (int d = 32; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d, 64));
+  const float w = l != 0.0f ? exp2_difference(x, m) * l : 0.0f;
   float sum = 0.0f, acc[kPer] = {};
   for (int s0 = w0; s0 < parts; s0 += WPR * kChunk) {
     float v[kChunk][kPer], ws[kChunk];
@@ -1239,7 +1264,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
     reinterpret_cast<uint16_t *>(p.O)[at * D + lane * kPer + i] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
   }
   if (p.lse && lane == 0 && w0 == 0)
-    p.lse[at] = sum == 0.0f ? -__builtin_inff() : (m + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+    p.lse[at] = sum == 0.0f ? -__builtin_inff() : natural_log(m, sum);
 }
 
 // ---- plan and launch ------------------------------------------------------------------------------
@@ -1289,8 +1314,9 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
   pl.splits = splits < 1 ? 1 : (int)splits;
   if (pl.splits > 1) {
     const int64_t n = T * heads * group;
-    pl.lse_offset = (size_t)pl.splits * n * D * 4;
-    pl.workspace_bytes = pl.lse_offset + (size_t)pl.splits * n * 4;
+    pl.ref_offset = (size_t)pl.splits * n * D * 4;
+    pl.sum_offset = pl.ref_offset + (size_t)pl.splits * n * 8;
+    pl.workspace_bytes = pl.sum_offset + (size_t)pl.splits * n * 4;
   }
   return pl;
 }
@@ -1325,7 +1351,8 @@ hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPla
   p.tile_rows = pl.tile_rows;
   if (pl.splits > 1) {
     p.part_o = reinterpret_cast<float *>(workspace);
-    p.part_lse = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + pl.lse_offset);
+    p.part_ref = reinterpret_cast<double *>(reinterpret_cast<char *>(workspace) + pl.ref_offset);
+    p.part_sum = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + pl.sum_offset);
   }
   const bool sym = p.zeros == nullptr, bf16 = xt == XType::BF16;
   if (D == 128) {

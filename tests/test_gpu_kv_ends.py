@@ -1,6 +1,6 @@
 """GPU parity of the 4-bit key/value cache at its ends: keys just outside what a
 row sees, in every variant of the attention kernels; queries and logits near
-fp32's limits."""
+fp32's limits; tied logits far past fp32's fractions."""
 
 import numpy as np
 import pytest
@@ -115,3 +115,53 @@ def _check_hull(a, scale):
                     s[1, near, h][:, None] * np.abs(c[1, near, h])).max(0) + 2.0 ** -24
                 o = got[a.start[b] + i, j]
                 assert (o >= v.min(0) - tol).all() and (o <= v.max(0) + tol).all(), (b, i, j)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("scale", [1e4, 1e6, 3e7, 2e8, 1e9, 1e12, 1e30])
+def test_logits_past_the_fractions_take_the_right_keys(n, dtype, scale):
+    for size in (1.0, 1e-3, 1e3):
+        _check_hull(Request([n, n], [150, 67], 4, 2, 64, 16, True, dtype, seed=20, size=size), scale)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [1e4, 1e6, 3e7, 2e8, 1e9, 1e12, 1e30, -1e9])
+def test_tied_logits_weigh_the_same(n, D, scale):
+    """Two kinds of keys only, one far above the other; the values' steps differ
+    by 2^17 from block to block.  The result is the mean of the winning kind's
+    values, however the keys are dealt over waves and parts: few of one kind in
+    some parts, many in others."""
+    rng = np.random.default_rng(32)
+    lens = [2100 + n, 700 + n]
+    a = Request([n, n], lens, 4, 2, D, 16, True, "float16", seed=32)
+    k0 = rng.normal(0, 1, (2, D))
+    kinds = []
+    for b, L in enumerate(lens):
+        pos = np.arange(L)
+        kind = np.where(pos < 600, pos % 97 != 5, pos % 3 == 0)
+        size = np.where((pos // 130) % 2 == 0, 2.0 ** -9, 2.0 ** 8)
+        a.put(b, pos, np.where(kind, -1.0, 1.0)[:, None, None] * k0,
+              rng.normal(0.5, 1, (L, 2, D)) * size[:, None, None])
+        kinds.append(kind)
+    sign = np.where(rng.random((2 * n, 4)) < 0.5, -1.0, 1.0)
+    a.ask(sign[..., None] * k0[[0, 0, 1, 1]] + rng.normal(0, 0.05, (2 * n, 4, D)))
+    for most in (max(lens), 700, 100, 50000):
+        O, _ = a.answer(max_seq_len=most, scale=scale)
+        got = out_to_f64(O)
+        for b, L in enumerate(lens):
+            c, z, s, val = a.tokens(b)
+            for i in range(n):
+                for j in range(4):
+                    h, r = j // 2, int(a.start[b]) + i
+                    seen = np.arange(L) <= L - n + i
+                    win = kinds[b] == (sign[r, j] * scale < 0)
+                    at = np.flatnonzero(seen & win)
+                    w = s[1, at, h]
+                    want = val[1, at, h].mean(0)
+                    cv = np.maximum(np.abs(c[1, at, h]), np.abs(c[1, at, h] - z[1, at, h][:, None]))
+                    bound = (EPS["float16"] * np.abs(want) + 2.0 ** -11 * (w[:, None] * cv).mean(0)
+                             + (len(at) + 64) * 2.0 ** -24 * (w[:, None] * (np.abs(c[1, at, h]) + 32)).mean(0) + 2.0 ** -25)
+                    err = np.abs(got[r, j] - want)
+                    assert (err <= bound).all(), (most, b, i, j, float((err / bound).max()))
