@@ -233,15 +233,16 @@ struct KvAttn {
   int splits, chunk;          // at most this many parts of a row's keys, of this length
   int tile_rows;              // rows that share their parts
   float *part_o;              // [splits][T * heads * group][D], normalized
-  double *part_ref;           // [splits][T * heads * group]: weights are relative to 2^this
-  float *part_sum;            // likewise: their sum, 0 where a part holds no key of the row
+  float2 *part_sum;           // [splits][T * heads * group]: weights are relative to 2^x; y, their
+                              // sum, is 0 where a part holds no key of the row
+  float *part_lo;             // likewise, where |x| >= 2^24 only: a part of the reference below x
 };
 // Kernel, its tile of rows, waves per workgroup and parts of the keys, and the
 // workspace of a call.
 struct KvAttnPlan {
   bool prompt;
   int tile_rows, waves, chunk, splits;
-  size_t ref_offset, sum_offset, workspace_bytes;   // 0 when splits == 1
+  size_t sum_offset, lo_offset, workspace_bytes;   // 0 when splits == 1
 };
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
                              int window);

@@ -148,19 +148,27 @@ __device__ __forceinline__ float running_max(float top, float cs, float vexp) {
 __device__ __forceinline__ bool past_fractions(float top, float cs) {
   return top != kNone && __builtin_fabsf(top * cs) >= 0x1p24f;
 }
-// What the decode kernel's weights are relative to, 2^reference: exact in fp64, so
-// that the rescaling and the joins of waves and parts shift sums by just the
-// difference of their references, whatever the logits' size.
-__device__ __forceinline__ double reference(float top, float cs, float M) {
-  return past_fractions(top, cs) ? (double)top * cs : (double)M;
+// What a row's weights are relative to, 2^(hi + lo), exactly: rescaling and the
+// joins of waves and parts shift sums by just the difference of their references,
+// whatever the logits' size.  lo is 0 but for rows past_fractions of the decode
+// kernel, whose top * cs is rounded.
+struct Reference {
+  float hi, lo;
+};
+__device__ __forceinline__ Reference reference(float top, float cs, float M) {
+  return Reference{M, past_fractions(top, cs) ? __builtin_fmaf(top, cs, -M) : 0.0f};
 }
-__device__ __forceinline__ float exp2_difference(double a, double b) {
-  return __builtin_amdgcn_exp2f((float)(a - b));
+// (lo is 0 below this)
+__device__ __forceinline__ bool may_have_low_part(float hi) {
+  return __builtin_fabsf(hi) >= 0x1p24f && hi != kNone;
+}
+__device__ __forceinline__ float exp2_difference(Reference a, Reference b) {
+  return __builtin_amdgcn_exp2f((a.hi - b.hi) + (a.lo - b.lo));
 }
 
 // ln (2^reference * sum)
-__device__ __forceinline__ float natural_log(double reference, float sum) {
-  return ((float)reference + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+__device__ __forceinline__ float natural_log(float reference, float sum) {
+  return (reference + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
 // What a workgroup knows about its request.
@@ -281,8 +289,7 @@ void kv_decode_kernel(KvAttn p) {
   constexpr int kWords = D / 32, kTiles = D / 16;
   constexpr int kRow = D + 4;                        // floats per row in LDS
   __shared__ __attribute__((aligned(16))) float red[NW][16][kRow];
-  __shared__ double red_m[NW][16];
-  __shared__ float red_l[NW][16];
+  __shared__ float red_m[NW][16], red_lo[NW][16], red_l[NW][16];
   __shared__ u32x4 sq[kWords][64];                   // the queries as MFMA operands, per lane
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -528,18 +535,24 @@ void kv_decode_kernel(KvAttn p) {
       }
       vmax = fmaxf(vmax, __shfl_xor(vmax, 16, 64));
       vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
-      const double before = reference(top, cs, M);
+      const float top_before = top;
       top = fmaxf(top, umax);
       if (vmax > vlim) {
         const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
         vexp = (float)ex;
         vlim = __builtin_ldexpf(1.0f, ex);
       }
-      const bool past = past_fractions(top, cs);
-      M = past ? top * cs : running_max(top, cs, vexp);
-      const float a = exp2_difference(before, reference(top, cs, M));
-      slack = past ? top : top + slack_width;
+      const float m_before = M;
+      M = running_max(top, cs, vexp);
+      float a = __builtin_amdgcn_exp2f(m_before - M);
+      slack = top + slack_width;
+      const bool past = past_fractions(top, cs), was = any_past;
       any_past = __any(past);
+      if (__builtin_expect(was | any_past, 0)) {
+        M = past ? top * cs : M;
+        slack = past ? top : slack;
+        a = exp2_difference(reference(top_before, cs, m_before), reference(top, cs, M));
+      }
       l *= a;
       pz *= a;
 #pragma unroll
@@ -652,20 +665,28 @@ void kv_decode_kernel(KvAttn p) {
       red[wave][c][d] = o[n][e] * (n & 1 ? 0x1p20f : 0x1p24f) - pz;
     }
   if (kq == 0) {
-    red_m[wave][c] = reference(top, cs, M);
+    red_m[wave][c] = M;
+    red_lo[wave][c] = any_past ? reference(top, cs, M).lo : 0.0f;
     red_l[wave][c] = l;
   }
   __syncthreads();
   constexpr int kPer = D / (4 * NW);                 // channels per thread
   const int r = tid / (4 * NW), d0 = (tid % (4 * NW)) * kPer;
   if (row0 + r >= rows) return;
-  double m = red_m[0][r];
+  Reference m = {red_m[0][r], 0.0f};
 #pragma unroll
-  for (int w = 1; w < NW; ++w) m = fmax(m, red_m[w][r]);
+  for (int w = 1; w < NW; ++w) m.hi = fmaxf(m.hi, red_m[w][r]);
+  const bool large = may_have_low_part(m.hi);
+  if (__builtin_expect(large, 0)) {
+    m.lo = kNone;
+    for (int w = 0; w < NW; ++w) m.lo = red_m[w][r] == m.hi ? fmaxf(m.lo, red_lo[w][r]) : m.lo;
+  }
   float sum = 0.0f, acc[kPer] = {};
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const float a = exp2_difference(red_m[w][r], m);
+    float e = red_m[w][r] - m.hi;
+    if (__builtin_expect(large, 0)) e += red_lo[w][r] - m.lo;
+    const float a = __builtin_amdgcn_exp2f(e);
     sum = __builtin_fmaf(red_l[w][r], a, sum);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = __builtin_fmaf(red[w][r][d0 + i], a, acc[i]);
@@ -683,8 +704,8 @@ void kv_decode_kernel(KvAttn p) {
       for (int i = 0; i < kPer; ++i) po[i] = acc[i] * inv;
     }
     if (d0 == 0) {
-      p.part_ref[at] = m;
-      p.part_sum[at] = sum;
+      p.part_sum[at] = float2{m.hi, sum};
+      if (__builtin_expect(large, 0)) p.part_lo[at] = m.lo;
     }
     return;
   }
@@ -694,7 +715,7 @@ void kv_decode_kernel(KvAttn p) {
     if constexpr (BF16) reinterpret_cast<uint16_t *>(p.O)[head_row * D + d0 + i] = float_to_bf16_bits(v);
     else reinterpret_cast<uint16_t *>(p.O)[head_row * D + d0 + i] = float_to_half_bits(v);
   }
-  if (p.lse && d0 == 0) p.lse[head_row] = none ? -__builtin_inff() : natural_log(m, sum);
+  if (p.lse && d0 == 0) p.lse[head_row] = none ? -__builtin_inff() : natural_log(m.hi, sum);
 }
 
 // ---- many query rows: the prompt kernel --------------------------------------------------------
@@ -1159,8 +1180,8 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   const int64_t at = keys.parts > 1 ? split * p.T * p.heads * p.group + head_row : head_row;
   if (keys.parts > 1) {
     if (hh == 0) {
-      p.part_ref[at] = M;
-      p.part_sum[at] = l;
+      p.part_sum[at] = float2{M, l};
+      if (__builtin_expect(may_have_low_part(M), 0)) p.part_lo[at] = 0.0f;
     }
     if (none) return;
   } else if (p.lse && hh == 0) {
@@ -1221,11 +1242,17 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
   const int64_t n = p.T * p.heads * p.group;
   const int qi = token_of(p, r);
   const int64_t at = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + r - qi * p.group;
-  const float l = lane < parts ? p.part_sum[lane * n + at] : 0.0f;
-  const double x = l != 0.0f ? p.part_ref[lane * n + at] : -__builtin_inf();
-  double m = x;
+  const float2 mine = lane < parts ? p.part_sum[lane * n + at] : float2{kNone, 0.0f};
+  const float l = mine.y;
+  Reference x = {l != 0.0f ? mine.x : kNone, 0.0f}, m = x;
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d, 64));
+  for (int d = 32; d > 0; d >>= 1) m.hi = fmaxf(m.hi, __shfl_xor(m.hi, d, 64));
+  if (__builtin_expect(__any(may_have_low_part(x.hi)), 0)) {
+    x.lo = may_have_low_part(x.hi) ? p.part_lo[lane * n + at] : 0.0f;
+    m.lo = x.hi == m.hi ? x.lo : kNone;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) m.lo = fmaxf(m.lo, __shfl_xor(m.lo, d, 64));
+  }
   const float w = l != 0.0f ? exp2_difference(x, m) * l : 0.0f;
   float sum = 0.0f, acc[kPer] = {};
   for (int s0 = w0; s0 < parts; s0 += WPR * kChunk) {
@@ -1264,7 +1291,7 @@ __global__ __launch_bounds__(256) void kv_join_kernel(KvAttn p) {
     reinterpret_cast<uint16_t *>(p.O)[at * D + lane * kPer + i] = BF16 ? float_to_bf16_bits(v) : float_to_half_bits(v);
   }
   if (p.lse && lane == 0 && w0 == 0)
-    p.lse[at] = sum == 0.0f ? -__builtin_inff() : natural_log(m, sum);
+    p.lse[at] = sum == 0.0f ? -__builtin_inff() : natural_log(m.hi, sum);
 }
 
 // ---- plan and launch ------------------------------------------------------------------------------
@@ -1314,9 +1341,9 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
   pl.splits = splits < 1 ? 1 : (int)splits;
   if (pl.splits > 1) {
     const int64_t n = T * heads * group;
-    pl.ref_offset = (size_t)pl.splits * n * D * 4;
-    pl.sum_offset = pl.ref_offset + (size_t)pl.splits * n * 8;
-    pl.workspace_bytes = pl.sum_offset + (size_t)pl.splits * n * 4;
+    pl.sum_offset = (size_t)pl.splits * n * D * 4;
+    pl.lo_offset = pl.sum_offset + (size_t)pl.splits * n * 8;
+    pl.workspace_bytes = pl.lo_offset + (size_t)pl.splits * n * 4;
   }
   return pl;
 }
@@ -1351,8 +1378,8 @@ hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPla
   p.tile_rows = pl.tile_rows;
   if (pl.splits > 1) {
     p.part_o = reinterpret_cast<float *>(workspace);
-    p.part_ref = reinterpret_cast<double *>(reinterpret_cast<char *>(workspace) + pl.ref_offset);
-    p.part_sum = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + pl.sum_offset);
+    p.part_sum = reinterpret_cast<float2 *>(reinterpret_cast<char *>(workspace) + pl.sum_offset);
+    p.part_lo = reinterpret_cast<float *>(reinterpret_cast<char *>(workspace) + pl.lo_offset);
   }
   const bool sym = p.zeros == nullptr, bf16 = xt == XType::BF16;
   if (D == 128) {
