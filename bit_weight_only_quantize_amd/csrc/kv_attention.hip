@@ -9,12 +9,15 @@
 // subnormals, below) and queries as fp16, after a power-of-two factor per row
 // where needed, so the only operand that is rounded is the weight
 // P'_t = 2^(u_t - M) vs_t, once, to fp16 (2^-11 relative); sums, the running
-// maximum and the normalizer are fp32.  M is the row's running maximum of u plus
-// the exponent of the largest value step that it has seen, so that P' <= 2^kSlack
-// whatever the steps: it neither overflows nor sinks into fp16's subnormals
-// because a layer's values are small.  M moves only when a logit exceeds it by
-// kSlack, which makes the rescaling of O (and the exchange between lanes that it
-// needs) rare: a wave tests one ballot.
+// maximum and the normalizer are fp32.  M follows the row's largest u_t + log2 vs_t,
+// the largest weight times its step (not the largest of each, which a large step
+// of no weight would drive apart), and is kept so that the largest P' lies between
+// 2^(kRaise - 3) and 2^kLimit: nothing overflows, and weights are rounded to less
+// than 11 bits (fp16's subnormals, steps of 2^-24) only below 2^-18 of the largest,
+// an error of 2^-29 of it at most.  M moves only when a tile might pass 2^kLimit,
+// which makes the rescaling of O (and the exchange between lanes that it needs)
+// rare: a wave tests one ballot, of the tile's largest u against `slack`, which
+// allows for the largest step that the tile may have, and of its steps against that.
 //
 // Rows of one key/value head are packed: row r of a request is query token
 // r / group, head r % group of the `group` query heads that share the
@@ -36,7 +39,9 @@ namespace awq {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr float kSlack = 8.0f;         // log2 of the largest P' between rescalings
+constexpr float kRaise = 7.0f;         // log2 of the largest P' where M is set, at most
+constexpr float kLimit = 15.0f;        // ... and before it is set again
+constexpr float kLeastStep = 0x1p-14f; // of what awq_kv_append writes; smaller ones count as this
 constexpr float kNone = -__FLT_MAX__;  // "no key yet": finite, so kNone - kNone is 0
 
 __device__ __forceinline__ f32x16 mfma32x16(u32x4 a, u32x4 b, f32x16 c) {
@@ -137,17 +142,18 @@ __device__ __forceinline__ uint32_t bf16_magnitude8(u32x4 raw) {
 // The logits' scale times log2(e) as the kernels use it: positive (a scale of 0
 // as one too small to matter), so that -inf times it stays -inf.
 __device__ __forceinline__ float positive_scale(float cs) { return cs > 0x1p-120f ? cs : 0x1p-120f; }
-// top * cs + vexp; kNone while no key was seen.
-__device__ __forceinline__ float running_max(float top, float cs, float vexp) {
-  return top == kNone ? kNone : __builtin_fmaf(top, cs, vexp);
-}
 
-// Logits so large that fp32 does not hold their fractions (top: the row's largest,
-// cs its factor).  Nothing can then be added to them: weights are taken relative
-// to the largest logit itself, and no logit may exceed it.
+__device__ __forceinline__ float power_of_two(int e) { return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23); }
+
+// Logits so large that fp32 hardly holds their fractions (top: the row's largest,
+// cs its factor).  Exponents of steps cannot then be added to them: weights are
+// taken relative to the largest logit itself, and no logit may exceed it.
 __device__ __forceinline__ bool past_fractions(float top, float cs) {
-  return top != kNone && __builtin_fabsf(top * cs) >= 0x1p24f;
+  return top != kNone && __builtin_fabsf(top * cs) >= 0x1p22f;
 }
+// (no row is past_fractions while this is false of its M, which is within 2^6 of
+// top * cs until then)
+__device__ __forceinline__ bool nearly_past(float M) { return M != kNone && __builtin_fabsf(M) >= 0x1p21f; }
 // What a row's weights are relative to, 2^(hi + lo), exactly: rescaling and the
 // joins of waves and parts shift sums by just the difference of their references,
 // whatever the logits' size.  lo is 0 but for rows past_fractions of the decode
@@ -160,7 +166,7 @@ __device__ __forceinline__ Reference reference(float top, float cs, float M) {
 }
 // (lo is 0 below this)
 __device__ __forceinline__ bool may_have_low_part(float hi) {
-  return __builtin_fabsf(hi) >= 0x1p24f && hi != kNone;
+  return __builtin_fabsf(hi) >= 0x1p22f && hi != kNone;
 }
 __device__ __forceinline__ float exp2_difference(Reference a, Reference b) {
   return __builtin_amdgcn_exp2f((a.hi - b.hi) + (a.lo - b.lo));
@@ -352,9 +358,9 @@ void kv_decode_kernel(KvAttn p) {
   // (negated for a negative scale, so that larger sums are larger logits)
   const float fs = p.scale_log2 < 0.0f ? -f : f;
   const float abs_scale = __builtin_fabsf(p.scale_log2);
-  // (bfloat16 queries near the end of their range, where this factor would pass
-  // fp32's: the sums then take 2^60 of it, in all rows alike)
-  const bool wide = __any(abs_scale * (1.0f / f) * 0x1p24f > __FLT_MAX__);
+  // (bfloat16 queries near the end of their range, where this factor or its inverse
+  // would pass fp32's: the sums then take 2^60 of it, in all rows alike)
+  const bool wide = __any(abs_scale * (1.0f / f) * 0x1p24f > 0x1p100f);
   const float cs = positive_scale(wide ? abs_scale * 0x1p-36f * (1.0f / f) : abs_scale * (1.0f / f) * 0x1p24f);
   // sum of the row's queries, for the zero points: sum q (code - z) = sum q code - z sum q
   float qsum = 0.0f;
@@ -448,10 +454,10 @@ void kv_decode_kernel(KvAttn p) {
   f32x4 o[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // M = top * cs + vexp, top the largest sum so far (times the key's step), 2^vexp = vlim;
-  // for a row past_fractions, top * cs
-  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, vexp = 0.0f, l = 0.0f, pz = 0.0f;
-  const float slack_width = kSlack / cs;
+  // top: the largest sum so far (times the key's step), the row's for a row
+  // past_fractions, whose M is top * cs; vlim: above the steps that slack allows for
+  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, l = 0.0f, pz = 0.0f;
+  const float inv_cs = 1.0f / cs;
   bool any_past = false;                             // a row of the wave is past_fractions (uniform)
   // The nibble pairs of word w (of shifted words, the next two): subnormal fp16
   constexpr uint32_t kLoNibbles = 0x000F000Fu, kHiNibbles = 0x00F000F0u;
@@ -524,34 +530,35 @@ void kv_decode_kernel(KvAttn p) {
       smax = max_half2(smax, w);
     }
     if (__any(umax > slack || hi_half(smax) > vlim)) {
-      umax = fmaxf(umax, __shfl_xor(umax, 16, 64));
-      umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
-      // (a step that overflowed counts for none)
-      float vmax = 0.0f;
+      // the row's largest weight times step, steps by their exponent field alone
+      // (hidden keys have u = -inf)
+      float best = kNone;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t w = T.sc[i >> 2][i & 3];
-        vmax = fmaxf(vmax, hi_half(w) <= 65504.0f ? hi_half(w) : 0.0f);
+        best = fmaxf(best, __builtin_fmaf(u[i], cs, (float)((w >> 26) & 31u)));
       }
-      vmax = fmaxf(vmax, __shfl_xor(vmax, 16, 64));
-      vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
-      const float top_before = top;
-      top = fmaxf(top, umax);
-      if (vmax > vlim) {
-        const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
-        vexp = (float)ex;
-        vlim = __builtin_ldexpf(1.0f, ex);
-      }
-      const float m_before = M;
-      M = running_max(top, cs, vexp);
+      best = fmaxf(best, __shfl_xor(best, 16, 64));
+      best = fmaxf(best, __shfl_xor(best, 32, 64));
+      // twice the largest step of this lane's keys, about that of the others too
+      const float m_before = M, vexp = (float)((smax >> 26) & 31u) - 13.0f;
+      M = fmaxf(M, best - (14.0f + kRaise));
+      vlim = power_of_two((int)vexp);
       float a = __builtin_amdgcn_exp2f(m_before - M);
-      slack = top + slack_width;
-      const bool past = past_fractions(top, cs), was = any_past;
-      any_past = __any(past);
-      if (__builtin_expect(was | any_past, 0)) {
+      slack = M == kNone ? kNone : (M + (kLimit - vexp)) * inv_cs;
+      float top_before = top;
+      top = fmaxf(top, umax);                        // (of this lane's keys, until it matters)
+      if (__builtin_expect(any_past | (bool)__any(nearly_past(M)), 0)) {
+#pragma unroll
+        for (int d = 16; d <= 32; d <<= 1) {
+          top_before = fmaxf(top_before, __shfl_xor(top_before, d, 64));
+          top = fmaxf(top, __shfl_xor(top, d, 64));
+        }
+        const bool past = past_fractions(top, cs);
         M = past ? top * cs : M;
         slack = past ? top : slack;
         a = exp2_difference(reference(top_before, cs, m_before), reference(top, cs, M));
+        any_past = __any(past);
       }
       l *= a;
       pz *= a;
@@ -948,8 +955,8 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   for (int n = 0; n < kTiles; ++n)
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[n][e] = 0.0f;
-  float M = kNone, top = kNone, slack = kNone, vlim = 0.0f, l = 0.0f;
-  float vleast = 0.0f;                                       // no row's vlim is less (uniform)
+  float M = kNone, top = kNone, slack = kNone, l = 0.0f;
+  float vlim = 0.0f;                                         // above the steps that slack allows for (uniform)
 
   // The order of a tile's instructions is spelled out for the scheduler: left
   // to itself it keeps one operand register and waits out the LDS latency
@@ -1039,38 +1046,39 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
     float umax = u[0];
 #pragma unroll
     for (int j = 1; j < 32; ++j) umax = fmaxf(umax, u[j]);
-    if (__any(umax > slack || vstep > vleast)) {
-      umax = fmaxf(umax, __shfl_xor(umax, 32, 64));
-      top = fmaxf(top, umax);
-      if (__any(vstep > vleast)) {
-        // the largest step of the keys that the row sees
-        float vmax = vstep;
-        if (partial) {
-          vmax = 0.0f;
+    if (__any(umax > slack || vstep > vlim)) {
+      // the least power of two (from kLeastStep on) that no step of the tile exceeds
+      int ve = -14;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
+      for (int bit = 16; bit > 0; bit >>= 1) ve += __any(vstep > power_of_two(ve + bit - 1)) ? bit : 0;
+      vlim = power_of_two(ve);
+      // each row's largest weight times step: over the keys where steps differ by
+      // more than 8 times (hidden ones among them), otherwise of the largest weight
+      float best = __builtin_fmaf(umax, cs, (float)ve);
+      if (__any(vstep > 0.0f && vstep < power_of_two(ve - 3))) {
+        best = kNone;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) vmax = fmaxf(vmax, u[4 * j + e] > -__builtin_inff() ? v[e] : 0.0f);
-          }
-          vmax = fmaxf(vmax, __shfl_xor(vmax, 32, 64));
-        } else {
+        for (int j = 0; j < 8; ++j) {
+          const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
 #pragma unroll
-          for (int d = 32; d > 0; d >>= 1) vmax = fmaxf(vmax, __shfl_xor(vmax, d, 64));
+          for (int e = 0; e < 4; ++e)
+            best = fmaxf(best, __builtin_fmaf(u[4 * j + e], cs, (float)__builtin_amdgcn_frexp_expf(fminf(fmaxf(v[e], kLeastStep), 65504.0f))));
+          __builtin_amdgcn_sched_barrier(0);                 // (bounds the registers in use)
         }
-        vmax = fminf(vmax, 65504.0f);
-        const int ex = ((int)(__builtin_bit_cast(uint32_t, vmax) >> 23) & 0xFF) - 126;
-        const float lim = vmax > 0.0f ? __builtin_ldexpf(1.0f, ex) : 0.0f;
-        vlim = fmaxf(vlim, lim);
-        if (!partial)                                        // (every row has seen the tile)
-          vleast = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, fmaxf(vleast, lim))));
       }
-      // (top * cs is exact, so for logits past_fractions M is off by vexp at most,
-      // and 2^(u cs - M) times a step stays an fp16 number)
-      const float vexp = vlim > 0.0f ? (float)((int)(__builtin_bit_cast(uint32_t, vlim) >> 23) - 127) : 0.0f;
-      const float m2 = running_max(top, cs, vexp), a = __builtin_amdgcn_exp2f(M - m2);
-      M = m2;
-      slack = past_fractions(top, cs) ? top : top + kSlack / cs;
+      best = fmaxf(best, __shfl_xor(best, 32, 64));
+      const float m_before = M;
+      M = fmaxf(M, best - kRaise);
+      slack = M == kNone ? kNone : __builtin_ldexpf(M + (kLimit - ve), 1 - __builtin_amdgcn_frexp_expf(cs));
+      top = fmaxf(top, umax);                                // (of this lane's keys, until it matters)
+      if (__builtin_expect(__any(nearly_past(M)), 0)) {
+        // (top * cs is exact, and so is every weight's exponent u cs - M)
+        top = fmaxf(top, __shfl_xor(top, 32, 64));
+        const bool past = past_fractions(top, cs);
+        M = past ? top * cs : M;
+        slack = past ? top : slack;
+      }
+      const float a = __builtin_amdgcn_exp2f(m_before - M);
       l *= a;
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)

@@ -551,15 +551,21 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
  * A row that sees no key gets O = 0 and lse = -inf.  Rows of no request (before
  * query_start[0], or behind query_start[num_seqs]) are left as they were.
  * Lengths beyond the table are cut to it; a table entry outside [0, num_pages)
- * holds no tokens.  max_blocks * P at most 2^30.  What lies in slots that a row does not see, infinities
- * and NaN included, does not reach it.
+ * holds no tokens.  max_blocks * P at most 2^30.  What lies in slots that a row
+ * does not see, infinities and NaN included, does not reach it.
  * Arithmetic: logits are exact integer-times-query products summed in fp32,
  * times the key's step and `scale`; softmax weights times the value's step are
- * rounded once to fp16 (2^-11 relative) and multiplied by the exact integers;
- * all sums, the maximum and the normalizer are fp32.  Queries may be scaled by a
- * power of two per row (bfloat16 ones become fp16 so), exactly, except that
- * values below 2^-24 of their row's largest lose their last bits.  Logits beyond
- * fp32's range give infinities or NaN.  Results do not change from call to call.
+ * rounded once to fp16 and multiplied by the exact integers: by 2^-11 relative,
+ * and below 2^-18 of the largest weight-times-step of the row's keys so far (of
+ * one part of them, where they are split) by up to 2^-29 of it instead.  Over n
+ * keys that leaves at most n 2^-29 of the largest product, so a tail of a million
+ * tiny weights beside one large one keeps 2^-9 of that.  Logits above 2^21 or so,
+ * whose fractions fp32 hardly holds, are weighed against the largest alone; tied
+ * ones weigh the same.  All sums, the maximum and the normalizer are fp32.
+ * Queries may be scaled by a power of two per row (bfloat16 ones become fp16 so),
+ * exactly, except that values below 2^-24 of their row's largest lose their last
+ * bits.  Logits beyond fp32's range give infinities or NaN.  Results do not
+ * change from call to call.
  */
 awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, int64_t q_stride,
                             int32_t num_heads, const awq_kv_cache *cache, awq_config cfg,

@@ -121,7 +121,8 @@ def assign(old, new, table, free, page, num_slots):
     return table, i32(lens), i32(start), slots, i32([used])
 
 
-def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_eps=2.0 ** -11):
+def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_eps=2.0 ** -11,
+                weighted=False):
     """(O, lse, bound, lse_bound) in fp64 for Q fp64 [T][num_heads][D]; rows of no
     request NaN.
 
@@ -136,6 +137,9 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
       fp32 logits of D products, the zero term    dl = (D + 8) 2^-24 a scale, a = ks sum |q|
       and the scaling                             (code + zero); moves p by 2 dl at most
       fp32 sums over n keys (and exp2)            (n + 64) 2^-24 sum p vs (code + zero)
+    With `weighted`, weights are taken as they are documented to be: multiplied by
+    code - zero, and small ones rounded to steps of 2^-24 where the row's (or its
+    part's) largest weight times step is at least 2^4, n 15 2^-29 max (p vs).
     """
     codes, scales, _ = cache
     pages, page = codes.shape[0], scales.shape[2]
@@ -178,8 +182,11 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
                 cv = np.maximum(np.abs(c[1, at, h]), np.abs(c[1, at, h] - z[1, at, h][:, None]))
                 n = len(at)
                 lse_bound[q0 + i, j] = dl + (n + 64) * 2.0 ** -24 + 2.0 ** -22 * abs(lse[q0 + i, j])
-                bound[q0 + i, j] = (out_eps * np.abs(o) + 2.0 ** -11 * ((p * vs) @ cv)
-                                    + n * 2.0 ** -21 * vs.max()
+                small = n * 2.0 ** -21 * vs.max()
+                if weighted:
+                    cv = np.abs(c[1, at, h] - z[1, at, h][:, None])
+                    small = n * 15 * 2.0 ** -29 * (p * vs).max()
+                bound[q0 + i, j] = (out_eps * np.abs(o) + 2.0 ** -11 * ((p * vs) @ cv) + small
                                     + 2 * dl * (p @ np.abs(val[1, at, h]))
                                     + (n + 64) * 2.0 ** -24 * ((p * vs) @ (c[1, at, h] + z[1, at, h][:, None] + 16)))
     return O, lse, bound, lse_bound

@@ -1,11 +1,13 @@
 """GPU parity of the 4-bit key/value cache at its ends: keys just outside what a
 row sees, in every variant of the attention kernels; queries and logits near
-fp32's limits; tied logits far past fp32's fractions."""
+fp32's limits; tied logits far past fp32's fractions;
+value steps many orders apart, long tails of small weights, contexts of many
+parts and pages."""
 
 import numpy as np
 import pytest
 
-from gpu_common import out_to_f64, torch_mod
+from gpu_common import out_to_f64, say, torch_mod
 from oracle import kv
 from test_gpu_kv import Attend, _i32, _rounded, _to_cache
 
@@ -165,3 +167,103 @@ def test_tied_logits_weigh_the_same(n, D, scale):
                              + (len(at) + 64) * 2.0 ** -24 * (w[:, None] * (np.abs(c[1, at, h]) + 32)).mean(0) + 2.0 ** -25)
                     err = np.abs(got[r, j] - want)
                     assert (err <= bound).all(), (most, b, i, j, float((err / bound).max()))
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_rows_on_both_sides_of_the_fractions(n, sign, dtype):
+    """Logits of one sign over a factor of 2^10, and rows 2^6 apart: from tile to
+    tile and row to row on either side of where weights change their reference."""
+    rng = np.random.default_rng(38)
+    L = 1000
+    a = Request([n], [L], 8, 2, 64, 16, True, dtype, seed=38)
+    base = rng.normal(0, 1, (2, 64))
+    a.put(0, np.arange(L), sign * base * 2.0 ** rng.uniform(-8, 2, (L, 1, 1)),
+          rng.normal(0, 1, (L, 2, 64)) * 2.0 ** rng.integers(-4, 4, (L, 1, 1)))
+    a.ask(base[[0] * 4 + [1] * 4] * 2.0 ** rng.integers(-3, 4, (n, 8, 1)))
+    for e in range(10, 24, 2):
+        _check_hull(a, 2.0 ** e)
+
+
+# ---- value steps many orders apart, and long tails ---------------------------------------
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ratio", [2.0 ** 14, 2.0 ** 20, 2.0 ** 24, 2.0 ** 28])
+@pytest.mark.parametrize("at", [0, 150])
+def test_large_steps_of_no_weight(n, D, ratio, at):
+    """A token whose values are orders of magnitude larger, with a weight near
+    2^-80: the others' weights keep their precision."""
+    rng = np.random.default_rng(33)
+    lens = [200 + n, 1700 + n]
+    a = Request([n, n], lens, 4, 2, D, 16, True, "float16", seed=33)
+    base = rng.normal(0, 1, (2, D))
+    for b, L in enumerate(lens):
+        V = rng.normal(0.3, 1, (L, 2, D)) * 2.0 ** -12
+        K = rng.normal(0, 1, (L, 2, D))
+        V[at] *= ratio
+        K[at] = -56 * D ** -0.5 * base
+        a.put(b, np.arange(L), K, V)
+    a.ask(base[[0, 0, 1, 1]] + rng.normal(0, 0.1, (2 * n, 4, D)))
+    _check_weighted(a)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_tails_of_small_weights(n, D):
+    """One key with nearly all of the weight and a value of zeros in half of the
+    channels, twenty thousand with 2^-25.5 of it each: the sum of the tail
+    arrives."""
+    rng = np.random.default_rng(34)
+    L = 20000
+    a = Request([n], [L], 2, 1, D, 64, True, "float16", seed=34)
+    base = rng.normal(0, 1, D)
+    K = rng.normal(0, 0.002, (L, 1, D))
+    K[0, 0] = base * (25.5 * np.log(2) * D ** 0.5 / (base @ base))
+    V = rng.uniform(0.5, 1, (L, 1, D))
+    V[0, 0, :D // 2], V[0, 0, D // 2:] = 0.0, 1.0
+    a.put(0, np.arange(L), K, V)
+    a.ask(base + rng.normal(0, 0.01, (n, 2, D)))
+    _check_weighted(a)
+    _check_weighted(a, max_seq_len=1000)
+
+
+def _check_weighted(a, relative=None, **kw):
+    O, lse = a.answer(**kw)
+    want, wl, bound, lse_bound = kv.attention64(a.q64, a.cache, a.table, a.kv_lens, a.start, a.D ** -0.5, True, 0,
+                                                EPS[a.dtype], weighted=True)
+    err = np.abs(out_to_f64(O) - want)
+    say("worst err / bound", float(np.max(err / np.maximum(bound, 1e-300))))
+    assert (err <= bound).all()
+    assert (np.abs(lse.cpu().numpy() - wl) <= lse_bound).all()
+    if relative is not None:
+        assert np.linalg.norm(err) <= relative * np.linalg.norm(want)
+
+
+# ---- contexts of many parts and pages ------------------------------------------------------
+
+@pytest.mark.parametrize("n,L,Hq,D,page,zp,dtype,most", [
+    (1, 20011, 2, 64, 16, True, "float16", 20011),          # 40 parts: the join's second turn
+    (1, 20011, 2, 128, 64, False, "bfloat16", 20011),
+    (1, 33000, 1, 64, 16, True, "float16", 60000),          # as many parts as there can be
+    (1, 20000, 2, 64, 16, True, "float16", 100),            # one workgroup: waves of 157 pages
+    (1, 9999, 2, 128, 16, True, "bfloat16", 1536),
+    (2, 9000, 8, 128, 16, False, "float16", 3000),          # few parts of many pages
+    (64, 5003, 1, 64, 16, True, "float16", 5003),           # the prompt kernel: 20 parts
+    (64, 20001, 1, 128, 64, True, "bfloat16", 20001),       # ... as many as there can be
+    (70, 9001, 1, 64, 32, False, "float16", 100),           # ... one part
+])
+def test_long_contexts(n, L, Hq, D, page, zp, dtype, most):
+    """Against the oracle, and (random values: the rounding errors of the many
+    weights cancel) within 1.25 times the output's rounding in the norm."""
+    a = Request([n], [L], Hq, 1, D, page, zp, dtype, seed=35)
+    _check_weighted(a, relative=1.25 * EPS[dtype], max_seq_len=most)
+
+
+def test_prompt_chunk_and_long_decoding_requests():
+    """One chunk of a prompt among requests of one token with long contexts."""
+    lens = [260, 5000, 33, 4100, 1, 700, 2048, 3000]
+    a = Request([200] + [1] * 7, lens, 4, 1, 64, 16, True, "float16", seed=36)
+    _check_weighted(a)
+    _check_weighted(a, max_seq_len=100)
