@@ -843,7 +843,10 @@ def awq_kv_assign(old_lens, new_lens, block_table, free_pages, page_size: int, n
 def awq_kv_append(K, V, cache, slots, nonfinite_count=None):
     """Quantize K and V (fp16 or bf16 [tokens][heads][D]; tokens may be strided,
     as slices of a fused projection's output are) into the cache's slots (int32
-    [tokens]; tokens with a negative slot are skipped).  Returns the cache."""
+    [tokens]; tokens with a negative slot are skipped).  ``nonfinite_count`` (int32)
+    grows by the values that are not finite and by the groups of finite values
+    (bfloat16 ones past fp16's range) whose step does not fit fp16.  Returns the
+    cache."""
     torch = _torch()
     c, cfg = _cache_arg(cache)
     _tensor(K, "K", (torch.float16, torch.bfloat16))

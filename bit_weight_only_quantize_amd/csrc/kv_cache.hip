@@ -231,6 +231,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(
     }
     const QuantWord qk = quantize_word<kLanes, SYM>(k, bad), qv = quantize_word<kLanes, SYM>(v, bad);
     if (!active) continue;
+    if (nonfinite != nullptr && word == 0) bad += (int)qk.overflow + (int)qv.overflow;
     const KvPlace p = kv_place<D>(slot, pshift, h, heads, word);
     codes[p.k_word] = qk.word;
     codes[p.v_word] = qv.word;

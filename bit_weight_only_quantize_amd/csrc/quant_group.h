@@ -43,18 +43,20 @@ __device__ __forceinline__ float group_max_nonneg(float v) {
 }
 
 // What a lane stores of its group: its word of eight codes, the step as fp16
-// and the zero point (0..15; 8 for the symmetric grid).
+// and the zero point (0..15; 8 for the symmetric grid).  `overflow`: the group holds
+// no infinity, but its step does not fit fp16.
 struct QuantWord {
   uint32_t word;
   _Float16 step;
   float zero;
+  bool overflow;
 };
 
 // Quantizes a group held by LANES consecutive lanes, eight values (v, in
 // channel order) per lane.  `bad` grows by the number of non-finite values.
 template <int LANES, bool SYM>
 __device__ __forceinline__ QuantWord quantize_word(const float (&v)[8], int &bad) {
-  float lo = 0.0f, hi = 0.0f, step;
+  float lo = 0.0f, hi = 0.0f, step, most;              // most: the group's largest magnitude
   if constexpr (SYM) {
     // the largest magnitude of the group on level +-7: one IEEE division
     // per lane and group
@@ -63,6 +65,7 @@ __device__ __forceinline__ QuantWord quantize_word(const float (&v)[8], int &bad
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, __builtin_fabsf(v[i]));
     amax = group_max_nonneg<LANES>(amax);
     step = amax / 7.0f;
+    most = amax;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -81,6 +84,7 @@ __device__ __forceinline__ QuantWord quantize_word(const float (&v)[8], int &bad
     const float q0 = d * 0x1.111112p-4f;
     const float q1 = __builtin_fmaf(__builtin_fmaf(-15.0f, q0, d), 0x1.111112p-4f, q0);
     step = d == __builtin_inff() ? d : q1;
+    most = fmaxf(hi, -lo);
   }
   const _Float16 sh = (_Float16)fmaxf(step, 0x1p-14f);
   const float sf = (float)sh;
@@ -129,7 +133,7 @@ __device__ __forceinline__ QuantWord quantize_word(const float (&v)[8], int &bad
                          : fminf(fmaxf(qv[i] + zf, qlo), qhi);
     word |= ((uint32_t)qf) << (4 * nibble_of_channel(i));
   }
-  return QuantWord{word, sh, zf};
+  return QuantWord{word, sh, zf, sf == __builtin_inff() && most < __builtin_inff()};
 }
 
 }  // namespace awq

@@ -449,8 +449,8 @@ awq_status awq_scale_search_ex(const void *X, const void *W, int64_t M, int64_t 
  *            zero_point = 0, whose zero is 8.
  * All three 16-byte aligned.  head_dim 64 or 128, page_size a power of two in
  * [AWQ_KV_MIN_PAGE, AWQ_KV_MAX_PAGE], num_pages * page_size at most 2^31.
- * Keys and values are expected within fp16's range (a larger group's step
- * would overflow). */
+ * Keys and values are expected within fp16's range (awq_kv_append reports groups
+ * whose step would overflow). */
 #define AWQ_KV_MIN_PAGE 16
 #define AWQ_KV_MAX_PAGE 1024
 #define AWQ_KV_MAX_HEADS 1024
@@ -504,7 +504,12 @@ awq_status awq_kv_assign(const int32_t *old_lens, const int32_t *new_lens, int32
  *   slots    device, int32 [num_tokens]; a token whose slot is negative or past
  *            the cache is skipped.  Slots must be distinct (a slot given twice
  *            ends with unspecified contents).  num_tokens at most 2^27.
- *   nonfinite_count  device int32 or NULL: as in awq_quantize_pack.
+ *   nonfinite_count  device int32 or NULL: as in awq_quantize_pack; besides, each
+ *            group (a token's key, or its value, of one head) without infinities
+ *            whose step does not fit fp16, as bfloat16 values from 7 * 65520 on can
+ *            make it (15 * 65520 for the range with zero_point = 1), adds 1.  Such
+ *            a step is stored as infinity, and rows that see the token get
+ *            infinities or NaN.
  * The formula is awq_quantize_pack's with s = 1, per token and head.
  */
 awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t num_tokens,

@@ -1,13 +1,13 @@
 """GPU parity of the 4-bit key/value cache at its ends: keys just outside what a
 row sees, in every variant of the attention kernels; queries and logits near
-fp32's limits; tied logits far past fp32's fractions;
-value steps many orders apart, long tails of small weights, contexts of many
-parts and pages."""
+fp32's limits; tied logits far past fp32's fractions; value steps many orders
+apart, long tails of small weights, contexts of many parts and pages; keys and
+values past fp16's range."""
 
 import numpy as np
 import pytest
 
-from gpu_common import out_to_f64, say, torch_mod
+from gpu_common import dev, out_to_f64, say, torch_mod
 from oracle import kv
 from test_gpu_kv import Attend, _i32, _rounded, _to_cache
 
@@ -267,3 +267,34 @@ def test_prompt_chunk_and_long_decoding_requests():
     a = Request([200] + [1] * 7, lens, 4, 1, 64, 16, True, "float16", seed=36)
     _check_weighted(a)
     _check_weighted(a, max_seq_len=100)
+
+
+# ---- append ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("zp", [True, False])
+def test_steps_beyond_fp16_are_counted(D, zp):
+    """bfloat16 keys and values can be so large that a group's step is not an fp16
+    number: each such group counts once; the largest that fit do not."""
+    import bit_weight_only_quantize_amd as awq
+    torch = torch_mod()
+    levels = 15 if zp else 7
+    fits, not_ = (978944.0, 983040.0) if zp else (456704.0, 458752.0)      # bfloat16; steps 65263 (65243), 65536
+    assert fits / levels < 65520 <= not_ / levels
+    K, V = torch.ones((6, 3, D)), torch.ones((6, 3, D))
+    K[0, 1, 7] = fits
+    V[1, 2, D - 1] = not_
+    K[2, 0, 0], K[2, 0, 1] = 3e38, -3e38                    # the range itself overflows
+    V[3, 1, 5] = -not_
+    K[4, 2, 9] = -fits
+    K[5, 0, 3] = 3e38                                       # this token is skipped
+    K, V = (x.to(torch.bfloat16).to(dev()) for x in (K, V))
+    cache = awq.empty_kv_cache(1, 3, D, 16, dev(), zero_point=zp)
+    count = torch.zeros(1, dtype=torch.int32, device=dev())
+    awq.awq_kv_append(K, V, cache, _i32([0, 3, 4, 9, 15, -1]), nonfinite_count=count)
+    assert count.item() == 3
+    inf = torch.isinf(cache[1][0][:, [0, 3, 4, 9, 15]]).nonzero().cpu().tolist()      # [head][token][k, v]
+    assert sorted(inf) == [[0, 2, 0], [1, 3, 1], [2, 1, 1]]
+    K[0, 0, 0] = float("inf")                               # an infinite value counts as itself only
+    awq.awq_kv_append(K[:1], V[:1], cache, _i32([0]), nonfinite_count=count)
+    assert count.item() == 4
