@@ -62,6 +62,30 @@ KvCache kv_cache(const awq_kv_cache *c, awq_config cfg) {
                  c->page_size, c->num_kv_heads, c->head_dim};
 }
 
+// Bytes that a call reads or writes.
+struct Span {
+  const void *p;
+  size_t n;
+};
+template <size_t A, size_t B>
+bool all_apart(const Span (&a)[A], const Span (&b)[B]) {
+  for (const Span &x : a)
+    for (const Span &y : b)
+      if (!apart(x.p, x.n, y.p, y.n)) return false;
+  return true;
+}
+// `tokens` rows of `width` elements of `size` bytes, `stride` elements apart.
+size_t strided_bytes(int64_t tokens, int64_t stride, int64_t width, size_t size) {
+  return ((size_t)(tokens - 1) * (size_t)stride + (size_t)width) * size;
+}
+struct CacheSpans {
+  Span codes, scales, zeros;
+};
+CacheSpans cache_spans(const KvCache &c) {
+  const size_t n = (size_t)c.pages * c.page_size * c.heads;      // (less than 2^41)
+  return CacheSpans{{c.codes, n * c.head_dim}, {c.scales, n * 4}, {c.zeros, c.zeros ? n * 2 : 0}};
+}
+
 // Sizes of an attention call that its workspace depends on.
 awq_status check_attention_sizes(const char *who, int64_t num_tokens, int32_t num_seqs,
                                  int32_t num_heads, const awq_kv_cache *cache, awq_config cfg,
@@ -155,9 +179,19 @@ awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t 
     return fail(AWQ_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", who);
   if (!aligned(slots, 4) || (nonfinite_count && !aligned(nonfinite_count, 4)))
     return fail(AWQ_ERR_INVALID_ARG, "%s: slots and nonfinite_count must be 4-byte aligned", who);
+  const KvCache kc = kv_cache(cache, cfg);
+  const CacheSpans cs = cache_spans(kc);
+  const Span in[] = {{K, strided_bytes(num_tokens, k_stride, width, 2)}, {V, strided_bytes(num_tokens, v_stride, width, 2)},
+                     {slots, (size_t)num_tokens * 4}},
+             arrays[] = {cs.codes, cs.scales, cs.zeros}, count[] = {{nonfinite_count, nonfinite_count ? 4u : 0u}};
+  if (!all_apart(in, arrays) || !all_apart(in, count) || !all_apart(count, arrays))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: K, V, slots, nonfinite_count and the cache may not overlap", who);
+  if (!apart(cs.codes.p, cs.codes.n, cs.scales.p, cs.scales.n) || !apart(cs.codes.p, cs.codes.n, cs.zeros.p, cs.zeros.n) ||
+      !apart(cs.scales.p, cs.scales.n, cs.zeros.p, cs.zeros.n))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: the cache arrays overlap each other", who);
   return hip_status(launch_kv_append(reinterpret_cast<const uint16_t *>(K), reinterpret_cast<const uint16_t *>(V),
                                      x_dtype == AWQ_BF16 ? XType::BF16 : XType::F16, num_tokens, k_stride,
-                                     v_stride, slots, kv_cache(cache, cfg), nonfinite_count,
+                                     v_stride, slots, kc, nonfinite_count,
                                      as_stream(stream)),
                     who);
 }
@@ -178,8 +212,13 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
     return fail(AWQ_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned, slots 4", who);
   const size_t bytes = (size_t)num_tokens * cache->num_kv_heads * cache->head_dim * (out_dtype == AWQ_F32 ? 4 : 2);
   if (!apart(K, bytes, V, bytes)) return fail(AWQ_ERR_INVALID_ARG, "%s: K and V overlap", who);
+  const KvCache kc = kv_cache(cache, cfg);
+  const CacheSpans cs = cache_spans(kc);
+  const Span out[] = {{K, bytes}, {V, bytes}},
+             in[] = {cs.codes, cs.scales, cs.zeros, {slots, (size_t)num_tokens * 4}};
+  if (!all_apart(out, in)) return fail(AWQ_ERR_INVALID_ARG, "%s: K or V overlaps the cache or the slots", who);
   const YType ot = out_dtype == AWQ_F16 ? YType::F16 : out_dtype == AWQ_BF16 ? YType::BF16 : YType::F32;
-  return hip_status(launch_kv_gather(kv_cache(cache, cfg), slots, num_tokens, K, V, ot, as_stream(stream)), who);
+  return hip_status(launch_kv_gather(kc, slots, num_tokens, K, V, ot, as_stream(stream)), who);
 }
 
 size_t awq_kv_attention_workspace_size(int64_t num_tokens, int32_t num_seqs, int32_t num_heads,
@@ -227,10 +266,7 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(lse, 4))
     return fail(AWQ_ERR_INVALID_ARG, "%s: block_table, seq_lens, query_start and lse must be 4-byte aligned", who);
   const size_t o_bytes = (size_t)num_tokens * num_heads * cache->head_dim * 2;
-  if (!apart(Q, ((size_t)(num_tokens - 1) * q_stride + (size_t)num_heads * cache->head_dim) * 2, O, o_bytes))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: O overlaps Q", who);
   const size_t lse_bytes = lse ? (size_t)num_tokens * num_heads * 4 : 0;
-  if (!apart(lse, lse_bytes, O, o_bytes)) return fail(AWQ_ERR_INVALID_ARG, "%s: lse overlaps O", who);
   // (no request has more query tokens than there are; the same in ..._workspace_size)
   if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
   const int group = num_heads / cache->num_kv_heads;
@@ -239,8 +275,16 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
   if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
     return fail(AWQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed (awq_kv_attention_workspace_size)", who,
                 workspace ? workspace_bytes : 0, plan.workspace_bytes);
-  if (!apart(workspace, plan.workspace_bytes, O, o_bytes) || !apart(workspace, plan.workspace_bytes, lse, lse_bytes))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: the workspace overlaps O or lse", who);
+  const CacheSpans cs = cache_spans(kv_cache(cache, cfg));
+  const Span out[] = {{O, o_bytes}, {lse, lse_bytes}, {workspace, plan.workspace_bytes}},
+             in[] = {{Q, strided_bytes(num_tokens, q_stride, (int64_t)num_heads * cache->head_dim, 2)},
+                     cs.codes, cs.scales, cs.zeros, {block_table, (size_t)num_seqs * max_blocks * 4},
+                     {seq_lens, (size_t)num_seqs * 4}, {query_start, query_start ? ((size_t)num_seqs + 1) * 4 : 0}};
+  if (!all_apart(out, in))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse or the workspace overlaps Q, the cache or the request arrays", who);
+  if (!apart(lse, lse_bytes, O, o_bytes) || !apart(workspace, plan.workspace_bytes, O, o_bytes) ||
+      !apart(workspace, plan.workspace_bytes, lse, lse_bytes))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse and the workspace may not overlap each other", who);
   KvAttn p{};
   p.Q = reinterpret_cast<const uint16_t *>(Q);
   p.q_stride = q_stride;

@@ -510,7 +510,9 @@ awq_status awq_kv_assign(const int32_t *old_lens, const int32_t *new_lens, int32
  *            make it (15 * 65520 for the range with zero_point = 1), adds 1.  Such
  *            a step is stored as infinity, and rows that see the token get
  *            infinities or NaN.
- * The formula is awq_quantize_pack's with s = 1, per token and head.
+ * The formula is awq_quantize_pack's with s = 1, per token and head.  K and V may
+ * be slices of one array; what is read, the cache's arrays and nonfinite_count may
+ * not overlap otherwise.
  */
 awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t num_tokens,
                          int64_t k_stride, int64_t v_stride, const awq_kv_cache *cache,
@@ -522,7 +524,7 @@ awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t 
  * weight's: K, V device [num_tokens][H][D] of out_dtype, dense, 16-byte
  * aligned; (code - zero) * step, exact for AWQ_F32, rounded once for AWQ_F16 and
  * AWQ_BF16.  A token whose slot is negative or past the cache gets zeros.  K
- * and V may not overlap; num_tokens at most 2^27.
+ * and V may overlap neither each other nor what is read; num_tokens at most 2^27.
  */
 awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_t *slots,
                          int64_t num_tokens, void *K, void *V, int32_t out_dtype,
@@ -547,12 +549,12 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
  *   causal   1: query token i of n sees keys 0 .. seq_len - n + i; 0: all keys.
  *   window   > 0 (causal only): of those, the last `window`; 0: all.
  *   O        device, [num_tokens][num_heads][D] of q_dtype, dense, 16-byte
- *            aligned, not overlapping Q.
+ *            aligned.
  *   lse      device, fp32 [num_tokens][num_heads], or NULL: ln sum e^logit.
  *   workspace  device, 256-byte aligned, awq_kv_attention_workspace_size()
  *            bytes (NULL when that is 0); scratch as for awq_linear_ex, not to
- *            be shared by calls that overlap in time.  (Outputs and workspace
- *            may not overlap each other.)
+ *            be shared by calls that overlap in time.
+ * O, lse and the workspace may not overlap each other, nor anything that is read.
  * A row that sees no key gets O = 0 and lse = -inf.  Rows of no request (before
  * query_start[0], or behind query_start[num_seqs]) are left as they were.
  * Lengths beyond the table are cut to it; a table entry outside [0, num_pages)
