@@ -19,6 +19,10 @@ constexpr int64_t kMaxTokens = (int64_t)1 << 27;
 // Tokens of a request that attention reads: key numbers stay within 32 bits, a
 // tile or two past the last key included.
 constexpr int64_t kMaxContext = (int64_t)1 << 30;
+// Elements from the first to the last token of a strided array, so that its bytes
+// count in 64 bits.
+constexpr int64_t kMaxExtent = (int64_t)1 << 60;
+bool too_far(int64_t tokens, int64_t stride) { return tokens > 0 && stride > kMaxExtent / tokens; }
 
 bool power_of_two(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 
@@ -173,6 +177,8 @@ awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t 
     return fail(AWQ_ERR_INVALID_ARG,
                 "%s: token strides %lld and %lld must be multiples of 8 of at least num_kv_heads * head_dim", who,
                 (long long)k_stride, (long long)v_stride);
+  if (too_far(num_tokens, k_stride) || too_far(num_tokens, v_stride))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: token strides reach beyond 2^60 elements", who);
   if (num_tokens == 0) return ok();
   if (!K || !V || !slots) return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
   if (!aligned(K, 16) || !aligned(V, 16))
@@ -250,6 +256,7 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
   if (q_stride < (int64_t)num_heads * cache->head_dim || q_stride % 8 != 0)
     return fail(AWQ_ERR_INVALID_ARG, "%s: q_stride=%lld must be a multiple of 8 of at least num_heads * head_dim",
                 who, (long long)q_stride);
+  if (too_far(num_tokens, q_stride)) return fail(AWQ_ERR_INVALID_ARG, "%s: q_stride reaches beyond 2^60 elements", who);
   if (causal != 0 && causal != 1) return fail(AWQ_ERR_INVALID_ARG, "%s: causal=%d: must be 0 or 1", who, causal);
   if (window > 0 && !causal) return fail(AWQ_ERR_INVALID_ARG, "%s: a window needs causal = 1", who);
   if (!std::isfinite(scale)) return fail(AWQ_ERR_INVALID_ARG, "%s: scale is not finite", who);
