@@ -12,9 +12,9 @@
 // maximum and the normalizer are fp32.  M follows the row's largest u_t + log2 vs_t,
 // the largest weight times its step (not the largest of each, which a large step
 // of no weight would drive apart), and is kept so that the largest P' lies between
-// 2^(kRaise - 3) and 2^kLimit: nothing overflows, and weights are rounded to less
-// than 11 bits (fp16's subnormals, steps of 2^-24) only below 2^-18 of the largest,
-// an error of 2^-29 of it at most.  M moves only when a tile might pass 2^kLimit,
+// 2^(kRaise - kSpread) and 2^kLimit: nothing overflows, and weights are rounded to
+// less than 11 bits (fp16's subnormals, steps of 2^-24) only below 2^-16 of the
+// largest, an error of 2^-27 of it at most.  M moves only when a tile might pass 2^kLimit,
 // which makes the rescaling of O (and the exchange between lanes that it needs)
 // rare: a wave tests one ballot, of the tile's largest u against `slack`, which
 // allows for the largest step that the tile may have, and of its steps against that.
@@ -41,6 +41,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kRaise = 7.0f;         // log2 of the largest P' where M is set, at most
 constexpr float kLimit = 15.0f;        // ... and before it is set again
+constexpr int kSpread = 5;             // log2 by which M may be above that for more slack
 constexpr float kLeastStep = 0x1p-14f; // of what awq_kv_append writes; smaller ones count as this
 constexpr float kNone = -__FLT_MAX__;  // "no key yet": finite, so kNone - kNone is 0
 
@@ -531,18 +532,21 @@ void kv_decode_kernel(KvAttn p) {
     }
     if (__any(umax > slack || hi_half(smax) > vlim)) {
       // the row's largest weight times step, steps by their exponent field alone
-      // (hidden keys have u = -inf)
-      float best = kNone;
+      // (hidden keys have u = -inf), and no less than it: the largest of each
+      float best = kNone, most = __builtin_fmaf(umax, cs, (float)((smax >> 26) & 31u));
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t w = T.sc[i >> 2][i & 3];
         best = fmaxf(best, __builtin_fmaf(u[i], cs, (float)((w >> 26) & 31u)));
       }
-      best = fmaxf(best, __shfl_xor(best, 16, 64));
-      best = fmaxf(best, __shfl_xor(best, 32, 64));
+#pragma unroll
+      for (int d = 16; d <= 32; d <<= 1) {
+        best = fmaxf(best, __shfl_xor(best, d, 64));
+        most = fmaxf(most, __shfl_xor(most, d, 64));
+      }
       // twice the largest step of this lane's keys, about that of the others too
       const float m_before = M, vexp = (float)((smax >> 26) & 31u) - 13.0f;
-      M = fmaxf(M, best - (14.0f + kRaise));
+      M = fmaxf(M, fminf(most, best + (kSpread - 1)) - (14.0f + kRaise));
       vlim = power_of_two((int)vexp);
       float a = __builtin_amdgcn_exp2f(m_before - M);
       slack = M == kNone ? kNone : (M + (kLimit - vexp)) * inv_cs;
@@ -962,7 +966,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   // to itself it keeps one operand register and waits out the LDS latency
   // before every MFMA (measured 915 us where this order took 834, on 8192 tokens of 32 heads over 8,
   // D = 128).
-  constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100, kLdsWrite = 0x200;
+  constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100;
   auto compute = [&](int buf, int t0) {
     const char *kl = sm.k[buf] + qc * Smem::kKeyRow + 16 * hh;
     const char *vl = sm.v[buf] + qc * Smem::kValueRow + 16 * hh;
@@ -1052,11 +1056,11 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
 #pragma unroll
       for (int bit = 16; bit > 0; bit >>= 1) ve += __any(vstep > power_of_two(ve + bit - 1)) ? bit : 0;
       vlim = power_of_two(ve);
-      // each row's largest weight times step: over the keys where steps differ by
-      // more than 8 times (hidden ones among them), otherwise of the largest weight
-      float best = __builtin_fmaf(umax, cs, (float)ve);
-      if (__any(vstep > 0.0f && vstep < power_of_two(ve - 3))) {
-        best = kNone;
+      // each row's largest weight times step is at most the largest of each, and by
+      // less than 2^kSpread so unless steps (hidden ones among them) differ by more
+      float most = __builtin_fmaf(umax, cs, (float)ve);
+      if (__any(vstep > 0.0f && vstep < power_of_two(ve - kSpread))) {
+        float best = kNone;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
@@ -1065,10 +1069,12 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
             best = fmaxf(best, __builtin_fmaf(u[4 * j + e], cs, (float)__builtin_amdgcn_frexp_expf(fminf(fmaxf(v[e], kLeastStep), 65504.0f))));
           __builtin_amdgcn_sched_barrier(0);                 // (bounds the registers in use)
         }
+        best = fmaxf(best, __shfl_xor(best, 32, 64));
+        most = fminf(fmaxf(most, __shfl_xor(most, 32, 64)), best + (kSpread - 1));
       }
-      best = fmaxf(best, __shfl_xor(best, 32, 64));
+      most = fmaxf(most, __shfl_xor(most, 32, 64));
       const float m_before = M;
-      M = fmaxf(M, best - kRaise);
+      M = fmaxf(M, most - kRaise);
       slack = M == kNone ? kNone : __builtin_ldexpf(M + (kLimit - ve), 1 - __builtin_amdgcn_frexp_expf(cs));
       top = fmaxf(top, umax);                                // (of this lane's keys, until it matters)
       if (__builtin_expect(__any(nearly_past(M)), 0)) {

@@ -563,10 +563,9 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
  * Arithmetic: logits are exact integer-times-query products summed in fp32,
  * times the key's step and `scale`; softmax weights times the value's step are
  * rounded once to fp16 and multiplied by the exact integers: by 2^-11 relative,
- * and below 2^-18 of the largest weight-times-step of the row's keys so far (of
- * one part of them, where they are split) by up to 2^-29 of it instead.  Over n
- * keys that leaves at most n 2^-29 of the largest product, so a tail of a million
- * tiny weights beside one large one keeps 2^-9 of that.  Logits above 2^21 or so,
+ * and below 2^-16 of the largest weight-times-step of the row's keys so far (of
+ * one part of them, where they are split) by up to 2^-27 of it instead: in a tail
+ * of n tiny weights beside one large one, n 2^-27 of that at most.  Logits above 2^21 or so,
  * whose fractions fp32 hardly holds, are weighed against the largest alone; tied
  * ones weigh the same.  All sums, the maximum and the normalizer are fp32.
  * Queries may be scaled by a power of two per row (bfloat16 ones become fp16 so),

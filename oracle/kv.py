@@ -139,7 +139,7 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
       fp32 sums over n keys (and exp2)            (n + 64) 2^-24 sum p vs (code + zero)
     With `weighted`, weights are taken as they are documented to be: multiplied by
     code - zero, and small ones rounded to steps of 2^-24 where the row's (or its
-    part's) largest weight times step is at least 2^4, n 15 2^-29 max (p vs).
+    part's) largest weight times step is at least 2^2, n 15 2^-27 max (p vs).
     """
     codes, scales, _ = cache
     pages, page = codes.shape[0], scales.shape[2]
@@ -185,7 +185,7 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
                 small = n * 2.0 ** -21 * vs.max()
                 if weighted:
                     cv = np.abs(c[1, at, h] - z[1, at, h][:, None])
-                    small = n * 15 * 2.0 ** -29 * (p * vs).max()
+                    small = n * 15 * 2.0 ** -27 * (p * vs).max()
                 bound[q0 + i, j] = (out_eps * np.abs(o) + 2.0 ** -11 * ((p * vs) @ cv) + small
                                     + 2 * dl * (p @ np.abs(val[1, at, h]))
                                     + (n + 64) * 2.0 ** -24 * ((p * vs) @ (c[1, at, h] + z[1, at, h][:, None] + 16)))
