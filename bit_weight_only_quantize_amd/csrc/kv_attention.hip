@@ -268,12 +268,12 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 // register sets, two waves per SIMD, measured 128 us where one set and three
 // waves took 113; of the present code three waves take 94 and four 90.)
 //
-// Measured there (429.6 MB): 90 us from an idle card, 4.8 TB/s of the 5.0 that a
-// copy reaches, and 98 - 110 repeated back to back, when the card's power limit
-// lowers the clock: the VALU is active 76% of the time, the MFMA 15%, and memory
-// delivers 1.01 times the bytes.  Four requests of up to 65536 tokens, 64 heads
-// over 8 (158.3 MB, symmetric): 27 us repeated, when the last-level cache holds
-// part of it, about 35 from memory, and 4 for the join.  One request of 777 tokens, 32 heads over 8: 9.5 us in a graph, which is latency:
+// Measured there (429.6 MB): 88 us from an idle card, 4.9 TB/s of the 5.1 that a
+// copy reaches, and 98 - 110 repeated back to back; the VALU is active 75% of the
+// time, the MFMA 15%, and memory delivers 1.01 times the bytes.  Four requests of up
+// to 65536 tokens, 64 heads over 8 (158.3 MB, symmetric): 28 us repeated, when the
+// last-level cache holds part of it, about 35 from memory, and 4 for the join.  One
+// request of 777 tokens, 32 heads over 8: 9.4 us in a graph, which is latency:
 // lengths, table, codes, and the waves' join, one after the other.
 template <int D>
 struct DecodeTile {
@@ -743,20 +743,19 @@ void kv_decode_kernel(KvAttn p) {
 // A workgroup's waves stage 16 tokens each, so a page lookup is one per wave.
 //
 // Measured: a prompt of 8192 tokens, 32 heads over 8, D = 128, bfloat16 (550
-// Gflop causal): 700 - 735 us from an idle card, 725 - 770 repeated, by the card's
-// power, 715 - 785 Tflop/s; the
-// VALU is active 58% of the time, the MFMA 38%, the LDS 48% (a fifth of that
-// conflicts).  The two units do run side by side, but the card's power limit
-// then lowers the clock (32x32x16 MFMAs alone run at 1.9 GHz, with seven VALU
-// operations after each at 1.5), so what counts is the work, hardly its order.  With D = 64 three
-// waves fit a SIMD: 507 and 530 us (two waves 531 and 572).
+// Gflop causal): 705 - 735 us, 750 - 780 Tflop/s, at 1.92 - 1.95 GHz.  The VALU is
+// active 58% of the time, the MFMA 38% and the LDS 49% (a fifth of that conflicts):
+// 96% of VALU and MFMA together, so on a SIMD the two take turns nearly all the
+// time although the units can run side by side (an MFMA with seven independent VALU
+// operations after it takes 20.4 ns where the two alone take 16.0 and 7.9).  With
+// D = 64 three waves fit a SIMD: 507 and 530 us (two waves 531 and 572).
 //
 // With NG = 2 a workgroup has two groups of four waves that walk alternate tiles
 // of the same rows, each with buffers of its own, and the second group's sums join
 // the first's through LDS: half the steps for a request, at one workgroup per CU.
 // Six ragged requests of up to 515 new tokens after up to 3000, window 1000, 16
-// heads over 4, D = 64: 25.8 us where one group took 39.8, with other lengths 31.8
-// where it took 37.
+// heads over 4, D = 64: 31.5 us, where one group took 37 (a set of shorter lengths:
+// 25.8 and 39.8).
 //
 // Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
 // a pipeline of half tiles (1376), the running maximum from a bound in LDS (1115),
@@ -1328,7 +1327,10 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
     // requests, 408 workgroups of D = 64: 25.8 us against 39.8; seven, 476 of D =
     // 128: 67 against 107; three of one length, 384, are slower, 87 against 78).
     // From 512 on four waves serve better (2048 tokens, 32 heads over 8: 84 us
-    // against 93).  Keys are split while there is less than a workgroup per CU, into
+    // against 93).  Every request is counted with max_q tokens, so these are more
+    // than the workgroups that have rows where lengths differ; counted by the tokens
+    // in all, some batches gain and some lose (a chunk of 200 among 11 single tokens
+    // after 20000: 361 -> 105 us; one of 512 among 15 after 4000: 422 -> 600).  Keys are split while there is less than a workgroup per CU, into
     // parts of 512 keys, or 256 for few rows: the parts' fp32 results are written
     // and read again (512 tokens of 32 heads: 19.9 us in one part, 29.3 in two; 64
     // tokens after 936: 19.8 us in four parts, 23.9 in two).

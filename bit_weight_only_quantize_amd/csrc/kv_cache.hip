@@ -32,7 +32,7 @@ namespace awq {
 // had before are only read, so no workgroup reads what another writes.
 //
 // Bound by latency: a launch, the lengths, two barriers, the table, the slots.
-// Measured 3.8 us for 24 requests of one token each, 5.2 us for 500 requests and
+// Measured 4.0 us for 24 requests of one token each, 5.3 us for 500 requests and
 // 16640 slots; there 256 slots to a workgroup took 5.1 us, 1024 took 8.0.
 constexpr int kAssignThreads = 256;
 constexpr int kAssignPer = 4;                               // requests per thread and chunk
@@ -176,9 +176,9 @@ hipError_t launch_kv_assign(const int32_t *old_lens, const int32_t *new_lens, in
 // so are its value words (four tokens to each 16 bytes).
 //
 // Bound by memory.  8192 tokens of 32 heads of 128, fp16: the append (reads
-// 134 MB, writes 36) takes 41 - 47 us, 3.6 - 4.2 TB/s; the gather into fp16, the
-// other way round, 28 - 34 us, 5.0 - 6.1 TB/s.  32 tokens of 8 heads: 3.6 and
-// 3.1 us, a launch's latency.
+// 134 MB, writes 36) takes 42 - 49 us, 3.5 - 4.0 TB/s; the gather into fp16, the
+// other way round, 29 - 35 us, 4.9 - 5.9 TB/s.  32 tokens of 8 heads: 3.8 and
+// 3.2 us, a launch's latency.
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t b) {
   return __builtin_bit_cast(float, b << 16);
 }
