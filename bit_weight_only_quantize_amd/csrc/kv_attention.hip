@@ -14,10 +14,11 @@
 // of no weight would drive apart), and is kept so that the largest P' lies between
 // 2^(kRaise - kSpread) and 2^kLimit: nothing overflows, and weights are rounded to
 // less than 11 bits (fp16's subnormals, steps of 2^-24) only below 2^-16 of the
-// largest, an error of 2^-27 of it at most.  M moves only when a tile might pass 2^kLimit,
-// which makes the rescaling of O (and the exchange between lanes that it needs)
-// rare: a wave tests one ballot, of the tile's largest u against `slack`, which
-// allows for the largest step that the tile may have, and of its steps against that.
+// largest, an error of 2^-27 of it at most.  M moves only when a tile might pass
+// 2^kLimit, which makes the rescaling of O (and the exchange between lanes that it
+// needs) rare: a wave tests one ballot, of the tile's largest u against `slack`,
+// which allows for the largest step that the tile may have, and of its steps
+// against that.
 //
 // Rows of one key/value head are packed: row r of a request is query token
 // r / group, head r % group of the `group` query heads that share the
@@ -266,7 +267,7 @@ __device__ __forceinline__ Keys keys_of(const KvAttn &p, const Request &r, int r
 // their products, so a load has most of a tile's work to arrive in while four
 // waves share a SIMD.  (48 requests of up to 4096 tokens, 32 heads of 128: two
 // register sets, two waves per SIMD, measured 128 us where one set and three
-// waves took 113; of the present code three waves take 94 and four 90.)
+// waves took 113; later three waves took 94 and four 90.)
 //
 // Measured there (429.6 MB): 88 us from an idle card, 4.9 TB/s of the 5.1 that a
 // copy reaches, and 98 - 110 repeated back to back; the VALU is active 75% of the

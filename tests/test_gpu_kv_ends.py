@@ -34,13 +34,13 @@ class Request(Attend):
         pos = np.arange(int(self.kv_lens[b]))
         return kv.read(self.cache, self.D, self.table[b, pos // self.page] * self.page + pos % self.page)
 
-    def answer(self, max_seq_len=None, **kw):
+    def answer(self, max_seq_len=None, max_query_len=None, **kw):
         """The output in fp64, for one query token per request or several."""
         import bit_weight_only_quantize_amd as awq
         one = (self.q_lens == 1).all()
         return awq.awq_kv_attention(self.Q, _to_cache(self.cache), _i32(self.table), _i32(self.kv_lens),
                                     query_start=None if one else _i32(self.start),
-                                    max_query_len=int(self.q_lens.max()), return_lse=True,
+                                    max_query_len=max_query_len or int(self.q_lens.max()), return_lse=True,
                                     max_seq_len=int(max(self.kv_lens)) if max_seq_len is None else max_seq_len, **kw)
 
 
@@ -68,8 +68,24 @@ def test_hidden_keys_of_every_variant(n, most, D, zp, dtype):
         _check_hidden(a, most, 10)
 
 
-def _check_hidden(a, most, window=0):
-    O, lse = a.answer(max_seq_len=most, window=window)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("zp", [True, False])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_hidden_keys_in_the_prompt_kernel_of_one_group(D, zp, dtype):
+    """Counted with the longest's tokens the requests here are 640 workgroups, which
+    take one group of waves each."""
+    n, B = 20, 32
+    lens = [33 + i * 7 for i in range(B)]
+    a = Request([n] * B, lens, 4, 2, D, 16, zp, dtype, seed=39)
+    steps = a.cache[1].view(np.uint16)
+    for b, L in enumerate(lens):
+        for pos in list(range(L, -(-L // 16) * 16)) + list(range(L - n - 9)):
+            steps[a.table[b, pos // 16], :, pos % 16] = 0x7800
+    _check_hidden(a, None, 10, max_query_len=n * B)
+
+
+def _check_hidden(a, most, window=0, **kw):
+    O, lse = a.answer(max_seq_len=most, window=window, **kw)
     want, wl, bound, lse_bound = kv.attention64(a.q64, a.cache, a.table, a.kv_lens, a.start, a.D ** -0.5, True, window,
                                                 EPS[a.dtype])
     assert (np.abs(out_to_f64(O) - want) <= bound).all()
