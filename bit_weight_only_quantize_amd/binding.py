@@ -35,6 +35,8 @@ AWQ_MAX_PARTS = 4
 AWQ_GEMV_MAX_M = 16
 AWQ_BATCHED_MAX_M = 64
 AWQ_KV_MIN_PAGE, AWQ_KV_MAX_PAGE, AWQ_KV_MAX_HEADS = 16, 1024, 1024
+AWQ_ROPE_MAX_DIM = 512
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 #: Every symbol include/awq355.h declares.
 EXPORTS = (
@@ -57,6 +59,9 @@ EXPORTS = (
     "awq_kv_gather",
     "awq_kv_attention",
     "awq_kv_attention_workspace_size",
+    "awq_rope_frequencies",
+    "awq_rope",
+    "awq_kv_append_rope",
     "awq_status_string",
     "awq_last_error",
     "awq_version",
@@ -87,6 +92,17 @@ class awq_kv_cache(ctypes.Structure):
                 ("zeros", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class awq_rope_args(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("attention_factor", ctypes.c_double), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("inverse", ctypes.c_int32)]
+
+
+class awq_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double)]
 
 
 class AwqError(RuntimeError):
@@ -163,6 +179,15 @@ def _load():
     lib.awq_kv_attention.restype = ctypes.c_int
     lib.awq_kv_attention_workspace_size.argtypes = [i64, i32, i32, pc, awq_config, i32, i64, i32]
     lib.awq_kv_attention_workspace_size.restype = ctypes.c_size_t
+    pr = ctypes.POINTER(awq_rope_args)
+    lib.awq_rope_frequencies.argtypes = [i32, ctypes.c_double, ctypes.POINTER(awq_rope_scaling),
+                                         ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]
+    lib.awq_rope_frequencies.restype = ctypes.c_int
+    lib.awq_rope.argtypes = [vp, vp, i32, i64, i64, vp, vp, i32, i64, i64, i32, i64, i32, pr, vp]
+    lib.awq_rope.restype = ctypes.c_int
+    lib.awq_kv_append_rope.argtypes = [vp, vp, i32, i64, i64, vp, vp, i32, i64, i64, i64, pc, awq_config, vp, pr, vp,
+                                       vp]
+    lib.awq_kv_append_rope.restype = ctypes.c_int
     lib.awq_status_string.argtypes = [ctypes.c_int]
     lib.awq_status_string.restype = ctypes.c_char_p
     lib.awq_last_error.argtypes = []
@@ -966,3 +991,126 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
                  window, _address(out), _address(lse), _address(ws), ws_bytes)
     check(st, "awq_kv_attention")
     return (out, lse) if return_lse else out
+
+
+# ---- rotary positions -------------------------------------------------------------
+
+def awq_rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                         original_len: float = 0.0, low: float = 0.0, high: float = 0.0, device="cuda"):
+    """(inv_freq, attention_factor): radians per position of each pair, a float64
+    tensor [rotary_dim / 2] on `device`, and the factor on cosines and sines.
+    ``scaling`` stretches them for contexts beyond the trained ones: 'linear',
+    'ntk', 'yarn' or 'bands', by `factor` from `original_len`; `low` and `high` are the
+    numbers of turns between which 'yarn' (default 1 and 32) and 'bands' (1 and 4) blend."""
+    torch = _torch()
+    kind = ROPE_SCALINGS.get(scaling)
+    if kind is None:
+        raise ValueError(f"scaling {scaling!r} is not one of {sorted(ROPE_SCALINGS)}")
+    inv = (ctypes.c_double * max(rotary_dim // 2, 1))()
+    scale = ctypes.c_double()
+    check(lib.awq_rope_frequencies(rotary_dim, base, awq_rope_scaling(kind, factor, original_len, low, high), inv,
+                                   ctypes.byref(scale)), "awq_rope_frequencies")
+    return torch.tensor(inv[:], dtype=torch.float64, device=device), scale.value
+
+
+def _rope_arg(positions, inv_freq, tokens, D, attention_factor, interleaved, inverse):
+    torch = _torch()
+    _check(positions, "positions", torch.int32, (tokens,))
+    _tensor(inv_freq, "inv_freq", torch.float64)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be 1-D [rotary_dim / 2]")
+    R = 2 * inv_freq.shape[0]
+    if R < 16 or R % 16 or R > D:
+        raise ValueError(f"inv_freq stands for rotary_dim={R}, which must be a multiple of 16 in [16, {D}]")
+    return awq_rope_args(_address(positions), inv_freq.data_ptr(), attention_factor, R, bool(interleaved),
+                         bool(inverse))
+
+
+def _rope_rows(x, name, tokens, D, out, dtype):
+    """Token strides of queries or keys to rotate and of their output (dense if `out` is
+    None)."""
+    if x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, expected [{tokens}][heads][{D}]")
+    heads = x.shape[1]
+    stride = _token_rows(x, name, heads, D)
+    if out is None:
+        return stride, heads * D
+    _tensor(out, f"{name}'s out", dtype, x.shape)
+    return stride, _token_rows(out, f"{name}'s out", heads, D)
+
+
+def awq_rope(Q, positions, inv_freq, K=None, attention_factor: float = 1.0, interleaved: bool = False,
+             inverse: bool = False, out=None):
+    """Q (fp16 or bf16 [tokens][heads][D], tokens may be strided) rotated by its
+    tokens' positions (int32 [tokens]): the first 2 * len(inv_freq) channels of each
+    head, halves paired, or neighbours with `interleaved`.  With K (the same for its own
+    number of heads) returns (Q', K').  ``inv_freq`` and ``attention_factor`` as
+    awq_rope_frequencies gives them.  ``inverse`` negates the angles: the gradient's
+    rotation.  ``out``: where to write (a tensor, or a pair with K); Q and K themselves
+    for a rotation in place."""
+    torch = _torch()
+    _tensor(Q, "Q", (torch.float16, torch.bfloat16))
+    if Q.dim() != 3:
+        raise ValueError("Q must be 3-D [tokens][heads][D]")
+    T, heads, D = Q.shape
+    if D % 16 or not 16 <= D <= AWQ_ROPE_MAX_DIM:
+        raise ValueError(f"heads of {D} channels: a multiple of 16 of at most {AWQ_ROPE_MAX_DIM} is needed")
+    q_out, k_out = (out, None) if K is None else (None, None) if out is None else out
+    q_stride, qo_stride = _rope_rows(Q, "Q", T, D, q_out, Q.dtype)
+    k_stride = ko_stride = kv_heads = 0
+    if K is not None:
+        _tensor(K, "K", Q.dtype)
+        k_stride, ko_stride = _rope_rows(K, "K", T, D, k_out, Q.dtype)
+        kv_heads = K.shape[1]
+    rope = _rope_arg(positions, inv_freq, T, D, attention_factor, interleaved, inverse)
+    dev = _one_gpu((inv_freq, "inv_freq"), (positions, "positions"))
+    _same_gpu(dev, (Q, "Q"), *(() if K is None else ((K, "K"),)), *(() if q_out is None else ((q_out, "out"),)),
+              *(() if k_out is None else ((k_out, "out"),)))
+    if q_out is None:
+        q_out = Q.new_empty((T, heads, D))
+    if K is not None and k_out is None:
+        k_out = K.new_empty((T, kv_heads, D))
+    st = _launch(lib.awq_rope, dev, _address(Q), _address(q_out), heads, q_stride, qo_stride, _address(K),
+                 _address(k_out), kv_heads, k_stride, ko_stride, _dtype_code(Q.dtype), T, D, rope)
+    check(st, "awq_rope")
+    return q_out if K is None else (q_out, k_out)
+
+
+def awq_kv_append_rope(K, V, cache, slots, positions, inv_freq, Q=None, attention_factor: float = 1.0,
+                       interleaved: bool = False, out=None, nonfinite_count=None):
+    """awq_kv_append of K rotated as awq_rope rotates it (quantized from fp32), and
+    of V as it is; with Q (the step's queries) also returns them rotated, in `out` if
+    given (Q itself for a rotation in place)."""
+    torch = _torch()
+    c, cfg = _cache_arg(cache)
+    D = c.head_dim
+    _tensor(K, "K", (torch.float16, torch.bfloat16))
+    _tensor(V, "V", K.dtype)
+    ks, vs = _token_rows(K, "K", c.num_kv_heads, D), _token_rows(V, "V", c.num_kv_heads, D)
+    T = K.shape[0]
+    if V.shape[0] != T:
+        raise ValueError("K and V must have the same number of tokens")
+    _check(slots, "slots", torch.int32, (T,))
+    if nonfinite_count is not None:
+        _tensor(nonfinite_count, "nonfinite_count", torch.int32)
+        if nonfinite_count.numel() < 1:
+            raise ValueError("nonfinite_count must hold one element")
+    q_stride = qo_stride = heads = 0
+    if Q is not None:
+        _tensor(Q, "Q", K.dtype)
+        q_stride, qo_stride = _rope_rows(Q, "Q", T, D, out, K.dtype)
+        heads = Q.shape[1]
+    elif out is not None:
+        raise ValueError("out is where Q goes: there is no Q")
+    rope = _rope_arg(positions, inv_freq, T, D, attention_factor, interleaved, False)
+    dev = _one_gpu(*_cache_tensors(cache), (slots, "slots"), (positions, "positions"), (inv_freq, "inv_freq"),
+                   None if nonfinite_count is None else (nonfinite_count, "nonfinite_count"))
+    _same_gpu(dev, (K, "K"), (V, "V"), *(() if Q is None else ((Q, "Q"),)),
+              *(() if out is None else ((out, "out"),)))
+    if Q is not None and out is None:
+        out = Q.new_empty((T, heads, D))
+    st = _launch(lib.awq_kv_append_rope, dev, _address(Q), _address(out), heads, q_stride, qo_stride, _address(K),
+                 _address(V), _dtype_code(K.dtype), T, ks, vs, c, cfg, _address(slots), rope,
+                 _address(nonfinite_count))
+    check(st, "awq_kv_append_rope")
+    return out

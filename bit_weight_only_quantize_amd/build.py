@@ -34,8 +34,10 @@ SOURCES = [
     "search.hip",
     "kv_cache.hip",
     "kv_attention.hip",
+    "rope.hip",
     "api.cpp",
     "api_kv.cpp",
+    "api_rope.cpp",
 ]
 
 ARCH = "gfx950"

@@ -5,90 +5,11 @@
 
 #include <cmath>
 
-#include "api_common.h"
-#include "awq_internal.h"
+#include "api_kv.h"
 
 using namespace awq;
 
 namespace {
-
-constexpr int64_t kMaxGrid = 65535;          // HIP's limit on grid y and z
-// Tokens of an append or gather: 16 or more to a workgroup of 256, and a grid
-// holds less than 2^32 threads.
-constexpr int64_t kMaxTokens = (int64_t)1 << 27;
-// Tokens of a request that attention reads: key numbers stay within 32 bits, a
-// tile or two past the last key included.
-constexpr int64_t kMaxContext = (int64_t)1 << 30;
-// Elements from the first to the last token of a strided array, so that its bytes
-// count in 64 bits.
-constexpr int64_t kMaxExtent = (int64_t)1 << 60;
-bool too_far(int64_t tokens, int64_t stride) { return tokens > 0 && stride > kMaxExtent / tokens; }
-
-bool power_of_two(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
-
-awq_status check_page(const char *who, int32_t page_size) {
-  if (!power_of_two(page_size) || page_size < AWQ_KV_MIN_PAGE || page_size > AWQ_KV_MAX_PAGE)
-    return fail(AWQ_ERR_UNSUPPORTED, "%s: page_size=%d: must be a power of two in [%d, %d]", who,
-                page_size, AWQ_KV_MIN_PAGE, AWQ_KV_MAX_PAGE);
-  return AWQ_OK;
-}
-
-awq_status check_cache(const char *who, const awq_kv_cache *c, awq_config cfg, bool need_ptrs) {
-  if (!c) return fail(AWQ_ERR_INVALID_ARG, "%s: cache is NULL", who);
-  if (cfg.w_bit != 4) return fail(AWQ_ERR_UNSUPPORTED, "%s: w_bit=%d: only 4 is supported", who, cfg.w_bit);
-  if (cfg.zero_point != 0 && cfg.zero_point != 1)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: zero_point=%d: must be 1 (asymmetric) or 0 (symmetric)", who,
-                cfg.zero_point);
-  if (c->head_dim != 64 && c->head_dim != 128)
-    return fail(AWQ_ERR_UNSUPPORTED, "%s: head_dim=%d: supported values are 64 and 128", who, c->head_dim);
-  if (cfg.group_size != c->head_dim)
-    return fail(AWQ_ERR_UNSUPPORTED, "%s: group_size=%d: a token's head is one group, so it must be head_dim=%d",
-                who, cfg.group_size, c->head_dim);
-  const awq_status st = check_page(who, c->page_size);
-  if (st != AWQ_OK) return st;
-  if (c->num_kv_heads < 1 || c->num_kv_heads > AWQ_KV_MAX_HEADS)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: num_kv_heads=%d: must be in [1, %d]", who, c->num_kv_heads,
-                AWQ_KV_MAX_HEADS);
-  if (c->num_pages < 1) return fail(AWQ_ERR_INVALID_ARG, "%s: num_pages=%lld: must be positive", who, (long long)c->num_pages);
-  if (c->num_pages > ((int64_t)1 << 31) / c->page_size)
-    return fail(AWQ_ERR_UNSUPPORTED, "%s: %lld pages of %d tokens exceed 2^31 slots", who,
-                (long long)c->num_pages, c->page_size);
-  if (!need_ptrs) return AWQ_OK;
-  if (!c->codes || !c->scales || (cfg.zero_point && !c->zeros))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: a cache array is NULL", who);
-  if (!aligned(c->codes, 16) || !aligned(c->scales, 16) || (cfg.zero_point && !aligned(c->zeros, 16)))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: the cache arrays must be 16-byte aligned", who);
-  return AWQ_OK;
-}
-
-KvCache kv_cache(const awq_kv_cache *c, awq_config cfg) {
-  return KvCache{c->codes, c->scales, cfg.zero_point ? c->zeros : nullptr, c->num_pages,
-                 c->page_size, c->num_kv_heads, c->head_dim};
-}
-
-// Bytes that a call reads or writes.
-struct Span {
-  const void *p;
-  size_t n;
-};
-template <size_t A, size_t B>
-bool all_apart(const Span (&a)[A], const Span (&b)[B]) {
-  for (const Span &x : a)
-    for (const Span &y : b)
-      if (!apart(x.p, x.n, y.p, y.n)) return false;
-  return true;
-}
-// `tokens` rows of `width` elements of `size` bytes, `stride` elements apart.
-size_t strided_bytes(int64_t tokens, int64_t stride, int64_t width, size_t size) {
-  return ((size_t)(tokens - 1) * (size_t)stride + (size_t)width) * size;
-}
-struct CacheSpans {
-  Span codes, scales, zeros;
-};
-CacheSpans cache_spans(const KvCache &c) {
-  const size_t n = (size_t)c.pages * c.page_size * c.heads;      // (less than 2^41)
-  return CacheSpans{{c.codes, n * c.head_dim}, {c.scales, n * 4}, {c.zeros, c.zeros ? n * 2 : 0}};
-}
 
 // Sizes of an attention call that its workspace depends on.
 awq_status check_attention_sizes(const char *who, int64_t num_tokens, int32_t num_seqs,
@@ -166,38 +87,12 @@ awq_status awq_kv_append(const void *K, const void *V, int32_t x_dtype, int64_t 
                          awq_config cfg, const int32_t *slots, int32_t *nonfinite_count,
                          awq_stream_t stream) {
   const char *who = "awq_kv_append";
-  const awq_status st = check_cache(who, cache, cfg, num_tokens > 0);
+  const awq_status st = check_append(who, K, V, x_dtype, num_tokens, k_stride, v_stride, cache, cfg, slots, nonfinite_count);
   if (st != AWQ_OK) return st;
-  if (x_dtype != AWQ_F16 && x_dtype != AWQ_BF16)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: x_dtype=%d: must be AWQ_F16 or AWQ_BF16", who, x_dtype);
-  if (num_tokens < 0) return fail(AWQ_ERR_INVALID_ARG, "%s: num_tokens=%lld is negative", who, (long long)num_tokens);
-  if (num_tokens > kMaxTokens) return fail(AWQ_ERR_INVALID_ARG, "%s: more than 2^27 tokens", who);
-  const int64_t width = (int64_t)cache->num_kv_heads * cache->head_dim;
-  if (k_stride < width || v_stride < width || k_stride % 8 != 0 || v_stride % 8 != 0)
-    return fail(AWQ_ERR_INVALID_ARG,
-                "%s: token strides %lld and %lld must be multiples of 8 of at least num_kv_heads * head_dim", who,
-                (long long)k_stride, (long long)v_stride);
-  if (too_far(num_tokens, k_stride) || too_far(num_tokens, v_stride))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: token strides reach beyond 2^60 elements", who);
   if (num_tokens == 0) return ok();
-  if (!K || !V || !slots) return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
-  if (!aligned(K, 16) || !aligned(V, 16))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: K and V must be 16-byte aligned", who);
-  if (!aligned(slots, 4) || (nonfinite_count && !aligned(nonfinite_count, 4)))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: slots and nonfinite_count must be 4-byte aligned", who);
-  const KvCache kc = kv_cache(cache, cfg);
-  const CacheSpans cs = cache_spans(kc);
-  const Span in[] = {{K, strided_bytes(num_tokens, k_stride, width, 2)}, {V, strided_bytes(num_tokens, v_stride, width, 2)},
-                     {slots, (size_t)num_tokens * 4}},
-             arrays[] = {cs.codes, cs.scales, cs.zeros}, count[] = {{nonfinite_count, nonfinite_count ? 4u : 0u}};
-  if (!all_apart(in, arrays) || !all_apart(in, count) || !all_apart(count, arrays))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: K, V, slots, nonfinite_count and the cache may not overlap", who);
-  if (!apart(cs.codes.p, cs.codes.n, cs.scales.p, cs.scales.n) || !apart(cs.codes.p, cs.codes.n, cs.zeros.p, cs.zeros.n) ||
-      !apart(cs.scales.p, cs.scales.n, cs.zeros.p, cs.zeros.n))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: the cache arrays overlap each other", who);
   return hip_status(launch_kv_append(reinterpret_cast<const uint16_t *>(K), reinterpret_cast<const uint16_t *>(V),
                                      x_dtype == AWQ_BF16 ? XType::BF16 : XType::F16, num_tokens, k_stride,
-                                     v_stride, slots, kc, nonfinite_count,
+                                     v_stride, slots, kv_cache(cache, cfg), nonfinite_count,
                                      as_stream(stream)),
                     who);
 }

@@ -199,6 +199,27 @@ hipError_t launch_kv_append(const uint16_t *K, const uint16_t *V, XType xt, int6
 hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int64_t T, void *K, void *V,
                             YType ot, hipStream_t st);
 
+// ---- rope.hip: rotary positions ---------------------------------------------------
+struct RopeArgs {
+  const int32_t *positions;   // [T]
+  const double *inv_freq;     // [rotary_dim / 2], radians per position
+  double factor;              // on cosines and sines
+  int rotary_dim;
+  bool pairs, inverse;        // neighbours paired rather than halves; angles negated
+};
+struct RopeArray {
+  const uint16_t *x;
+  uint16_t *y;                // may be x, with the same stride
+  int64_t x_stride, y_stride; // elements between tokens
+  int heads;                  // 0: there is none
+};
+constexpr int kRopeMaxDim = 512;   // a token's head fits a wave
+hipError_t launch_rope(const RopeArgs &p, const RopeArray &q, const RopeArray &k, XType xt, int64_t T, int D,
+                       hipStream_t st);
+hipError_t launch_kv_append_rope(const RopeArgs &p, const RopeArray &q, const uint16_t *K, const uint16_t *V, XType xt,
+                                 int64_t T, int64_t k_stride, int64_t v_stride, const int32_t *slots,
+                                 const KvCache &c, int32_t *nonfinite, hipStream_t st);
+
 // ---- kv_attention.hip -------------------------------------------------------------
 // Arguments of one attention call (from `splits` on the launcher's).
 // Division of x < 2^30 by d in [1, 1024] as one multiplication: with 2^L <= d < 2^(L+1)

@@ -14,6 +14,7 @@
 
 #include "awq_internal.h"
 #include "device_common.h"
+#include "kv_place.h"
 #include "quant_group.h"
 
 namespace awq {
@@ -179,37 +180,6 @@ hipError_t launch_kv_assign(const int32_t *old_lens, const int32_t *new_lens, in
 // 134 MB, writes 36) takes 42 - 49 us, 3.5 - 4.0 TB/s; the gather into fp16, the
 // other way round, 29 - 35 us, 4.9 - 5.9 TB/s.  32 tokens of 8 heads: 3.8 and
 // 3.2 us, a launch's latency.
-__device__ __forceinline__ float bf16_bits_to_float(uint32_t b) {
-  return __builtin_bit_cast(float, b << 16);
-}
-
-template <bool BF16>
-__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8]) {
-  const u32x4 raw = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t r = raw[i];
-    v[2 * i] = BF16 ? bf16_bits_to_float(r & 0xFFFFu) : half_bits_to_float((uint16_t)(r & 0xFFFFu));
-    v[2 * i + 1] = BF16 ? bf16_bits_to_float(r >> 16) : half_bits_to_float((uint16_t)(r >> 16));
-  }
-}
-
-// Where slot s of head h keeps its words, and its step and zero point.
-struct KvPlace {
-  int64_t k_word, v_word, meta;
-};
-template <int D>
-__device__ __forceinline__ KvPlace kv_place(int32_t slot, int pshift, int h, int heads, int word) {
-  const int64_t page = slot >> pshift;
-  const int64_t P = (int64_t)1 << pshift, off = slot & (P - 1);
-  KvPlace p;
-  const int64_t base = (page * 2 * heads + h) * P * (D / 8);
-  p.k_word = base + off * (D / 8) + word;
-  p.v_word = base + heads * P * (D / 8) + (off >> 2) * (D / 2) + word * 4 + (off & 3);
-  p.meta = ((page * heads + h) * P + off) * 2;
-  return p;
-}
-
 template <int D, bool SYM, bool BF16>
 __global__ __launch_bounds__(256) void kv_append_kernel(
     const uint16_t *__restrict__ K, const uint16_t *__restrict__ V, int64_t T, int heads,

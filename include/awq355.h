@@ -587,6 +587,95 @@ size_t awq_kv_attention_workspace_size(int64_t num_tokens, int32_t num_seqs, int
                                        const awq_kv_cache *cache, awq_config cfg,
                                        int32_t max_query_len, int64_t max_seq_len, int32_t window);
 
+/* ---- rotary positions ------------------------------------------------------
+ *
+ * Queries and keys are turned by angles that grow with their positions.  Of a
+ * head's first `rotary_dim` channels (a multiple of 16, at most head_dim), pair
+ * j < rotary_dim / 2 is (a, b) = channels (j, j + rotary_dim / 2), or with
+ * interleaved = 1 (2j, 2j + 1):
+ *   a' = a c - b s,  b' = b c + a s,
+ *   c, s = attention_factor * cos, sin(position * inv_freq[j]),
+ * the angle, its cosine and sine in 64 bits and then rounded to fp32; products and
+ * sums are fp32, each rounded once (no fused multiply-add), so results do not
+ * depend on sizes.  The channels behind the first rotary_dim are kept as they are.
+ *
+ *   positions  device, int32 [num_tokens], of either sign (distances between
+ *              queries and keys count, so any origin serves).
+ *   inv_freq   device, fp64 [rotary_dim / 2], radians per position, as from
+ *              awq_rope_frequencies; 8-byte aligned.
+ *   inverse    1: the angles negated, which is the gradient's rotation (and undoes
+ *              one whose factor is 1); 0: not. */
+typedef struct awq_rope_args {
+    const int32_t *positions;
+    const double *inv_freq;
+    double attention_factor;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    int32_t inverse;
+} awq_rope_args;
+/* Largest head_dim of awq_rope. */
+#define AWQ_ROPE_MAX_DIM 512
+
+/* How frequencies are stretched for contexts longer than the ones trained on
+ * (awq_rope_scaling.kind); L = original_len, s = factor, base-frequency f:
+ *  - LINEAR  f / s.
+ *  - NTK     base s^(R / (R - 2)) in place of base, R = rotary_dim.
+ *  - YARN    f / s for pairs that turn less than `low` times within L (default 1), f
+ *            for those that turn more than `high` times (32), a linear ramp over the
+ *            pairs' numbers between; attention_factor 0.1 ln s + 1 (s >= 1).
+ *  - BANDS   by wavelength w = 2 pi / f: f / s where L / w < low (default 1), f where
+ *            L / w > high (4), between them ((1 - m) / s + m) f, m = (L / w - low) /
+ *            (high - low). */
+enum { AWQ_ROPE_NONE = 0, AWQ_ROPE_LINEAR = 1, AWQ_ROPE_NTK = 2, AWQ_ROPE_YARN = 3, AWQ_ROPE_BANDS = 4 };
+typedef struct awq_rope_scaling {
+    int32_t kind;
+    double factor;       /* s > 0 */
+    double original_len; /* L > 0 (YARN and BANDS) */
+    double low, high;    /* 0: the default */
+} awq_rope_scaling;
+
+/*
+ * awq_rope_frequencies - inv_freq[j] = base^(-2j / rotary_dim), stretched by
+ * `scaling` (NULL: not), and the attention factor that goes with it.  Host
+ * arithmetic and host pointers: inv_freq fp64 [rotary_dim / 2], attention_factor
+ * fp64 [1].  base > 1.
+ */
+awq_status awq_rope_frequencies(int32_t rotary_dim, double base, const awq_rope_scaling *scaling,
+                                double *inv_freq, double *attention_factor);
+
+/*
+ * awq_rope - rotated queries and keys.
+ *   Q, K     device, [num_tokens][num_heads or num_kv_heads][head_dim] of x_dtype
+ *            (AWQ_F16 or AWQ_BF16), the heads of a token dense, tokens q_stride /
+ *            k_stride elements apart (a multiple of 8); 16-byte aligned.  K may be
+ *            NULL with num_kv_heads = 0.
+ *   Q_out, K_out  likewise, qo_stride / ko_stride apart, rounded once to x_dtype.
+ *            Q_out may be Q with the same stride, and K_out K (in place); otherwise
+ *            what is written overlaps neither what is read nor itself.
+ * head_dim a multiple of 16, at most AWQ_ROPE_MAX_DIM; num_tokens at most 2^27; at
+ * most AWQ_KV_MAX_HEADS heads each.
+ */
+awq_status awq_rope(const void *Q, void *Q_out, int32_t num_heads, int64_t q_stride,
+                    int64_t qo_stride, const void *K, void *K_out, int32_t num_kv_heads,
+                    int64_t k_stride, int64_t ko_stride, int32_t x_dtype, int64_t num_tokens,
+                    int32_t head_dim, const awq_rope_args *rope, awq_stream_t stream);
+
+/*
+ * awq_kv_append_rope - awq_kv_append of rotated keys, and rotated queries, in one
+ * launch.  The keys are quantized as rotated in fp32, without a rounding to
+ * x_dtype between; everything else is as in awq_kv_append and awq_rope.
+ *   Q, Q_out  the step's queries, [num_tokens][num_heads][D], and their place; NULL
+ *            with num_heads = 0.  Q_out may be Q with the same stride, and may
+ *            overlap nothing else that the call reads or writes.  Queries of tokens
+ *            without a slot are rotated too.
+ */
+awq_status awq_kv_append_rope(const void *Q, void *Q_out, int32_t num_heads, int64_t q_stride,
+                              int64_t qo_stride, const void *K, const void *V, int32_t x_dtype,
+                              int64_t num_tokens, int64_t k_stride, int64_t v_stride,
+                              const awq_kv_cache *cache, awq_config cfg, const int32_t *slots,
+                              const awq_rope_args *rope, int32_t *nonfinite_count,
+                              awq_stream_t stream);
+
 /* Static description of a status code. */
 const char *awq_status_string(awq_status status);
 
