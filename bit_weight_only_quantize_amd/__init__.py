@@ -18,6 +18,8 @@ _API = (
     "AWQ_KERNEL_GEMM", "AWQ_KERNEL_BATCHED", "AWQ_GEMV_MAX_M", "AWQ_BATCHED_MAX_M", "EXPORTS",
     "LIB_PATH", "empty_kv_cache", "awq_kv_assign", "awq_kv_append", "awq_kv_gather",
     "awq_kv_attention", "awq_kv_attention_workspace_size",
+    "awq_kv_copy_pages", "awq_kv_fork", "awq_kv_release", "awq_kv_release_workspace_size",
+    "awq_kv_compact", "awq_kv_compact_workspace_size",
     "awq_rope_frequencies", "awq_rope", "awq_kv_append_rope", "ROPE_SCALINGS", "AWQ_ROPE_MAX_DIM",
 )
 

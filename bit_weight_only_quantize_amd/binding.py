@@ -59,6 +59,12 @@ EXPORTS = (
     "awq_kv_gather",
     "awq_kv_attention",
     "awq_kv_attention_workspace_size",
+    "awq_kv_copy_pages",
+    "awq_kv_fork",
+    "awq_kv_release",
+    "awq_kv_release_workspace_size",
+    "awq_kv_compact",
+    "awq_kv_compact_workspace_size",
     "awq_rope_frequencies",
     "awq_rope",
     "awq_kv_append_rope",
@@ -179,6 +185,19 @@ def _load():
     lib.awq_kv_attention.restype = ctypes.c_int
     lib.awq_kv_attention_workspace_size.argtypes = [i64, i32, i32, pc, awq_config, i32, i64, i32]
     lib.awq_kv_attention_workspace_size.restype = ctypes.c_size_t
+    lib.awq_kv_copy_pages.argtypes = [pc, awq_config, vp, vp, i64, vp]
+    lib.awq_kv_copy_pages.restype = ctypes.c_int
+    lib.awq_kv_fork.argtypes = [pc, awq_config, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp]
+    lib.awq_kv_fork.restype = ctypes.c_int
+    lib.awq_kv_release.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, i64, vp, i32, vp, vp, i32, vp, vp,
+                                   ctypes.c_size_t, vp]
+    lib.awq_kv_release.restype = ctypes.c_int
+    lib.awq_kv_release_workspace_size.argtypes = [i64, i32]
+    lib.awq_kv_release_workspace_size.restype = ctypes.c_size_t
+    lib.awq_kv_compact.argtypes = [pc, awq_config, vp, i32, i32, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.awq_kv_compact.restype = ctypes.c_int
+    lib.awq_kv_compact_workspace_size.argtypes = [i64, i32]
+    lib.awq_kv_compact_workspace_size.restype = ctypes.c_size_t
     pr = ctypes.POINTER(awq_rope_args)
     lib.awq_rope_frequencies.argtypes = [i32, ctypes.c_double, ctypes.POINTER(awq_rope_scaling),
                                          ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]
@@ -991,6 +1010,149 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
                  window, _address(out), _address(lse), _address(ws), ws_bytes)
     check(st, "awq_kv_attention")
     return (out, lse) if return_lse else out
+
+
+# ---- pages of the cache -----------------------------------------------------------
+
+def _table_arg(block_table, seq_lens=None):
+    i32 = _torch().int32
+    _tensor(block_table, "block_table", i32)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be 2-D [B][max_blocks]")
+    if seq_lens is not None:
+        _check(seq_lens, "seq_lens", i32, (block_table.shape[0],))
+    return block_table.shape
+
+
+def _free_arg(free_pages, taken, name="taken"):
+    i32 = _torch().int32
+    _tensor(free_pages, "free_pages", i32)
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be 1-D")
+    if taken is not None:
+        _check(taken, name, i32, (1,))
+
+
+def _named(**tensors):
+    return ((t, name) for name, t in tensors.items() if t is not None)
+
+
+def awq_kv_copy_pages(cache, src, dst):
+    """Copy page src[i] of the cache to page dst[i] (int32 [n] each; pairs with an id
+    outside the cache are skipped).  Returns the cache."""
+    i32 = _torch().int32
+    c, cfg = _cache_arg(cache)
+    _tensor(src, "src", i32)
+    if src.dim() != 1:
+        raise ValueError("src must be 1-D")
+    _check(dst, "dst", i32, src.shape)
+    dev = _one_gpu(*_cache_tensors(cache), (src, "src"), (dst, "dst"))
+    check(_launch(lib.awq_kv_copy_pages, dev, c, cfg, _address(src), _address(dst), src.shape[0]), "awq_kv_copy_pages")
+    return cache
+
+
+def awq_kv_fork(cache, block_table, parents, children, lens, shared, free_pages, taken=None, out=None):
+    """Row children[i] of block_table becomes a branch of the first lens[i] tokens of
+    row parents[i] (int32 [n] each): full pages are shared, and counted in `shared`
+    (int32 [pages]: holders beyond the first), a last page that is not full is copied to
+    a page from the front of free_pages, behind the `taken` (int32 [1]) that awq_kv_assign
+    has used of it.  Returns pages_used (int32 [1]), those and its own."""
+    i32 = _torch().int32
+    c, cfg = _cache_arg(cache)
+    B, blocks = _table_arg(block_table)
+    _tensor(parents, "parents", i32)
+    if parents.dim() != 1:
+        raise ValueError("parents must be 1-D")
+    _check(children, "children", i32, parents.shape)
+    _check(lens, "lens", i32, parents.shape)
+    _check(shared, "shared", i32, (c.num_pages,))
+    _free_arg(free_pages, taken)
+    if out is not None:
+        _check(out, "out", i32, (1,))
+    dev = _one_gpu(*_cache_tensors(cache), *_named(block_table=block_table, parents=parents, children=children,
+                                                   lens=lens, shared=shared, free_pages=free_pages, taken=taken,
+                                                   out=out))
+    if out is None:
+        out = parents.new_empty(1)
+    st = _launch(lib.awq_kv_fork, dev, c, cfg, _address(parents), _address(children), _address(lens),
+                 parents.shape[0], _address(block_table), B, blocks, _address(shared), _address(free_pages),
+                 free_pages.shape[0], _address(taken), out.data_ptr())
+    check(st, "awq_kv_fork")
+    return out
+
+
+def awq_kv_release_workspace_size(num_pages: int, num_free: int) -> int:
+    return int(lib.awq_kv_release_workspace_size(num_pages, num_free))
+
+
+def awq_kv_release(block_table, seq_lens, shared, free_pages, page_size: int, start=None, end=None, pages_used=None,
+                   out=None, workspace="auto"):
+    """Give pages back: of each row, those whose tokens (below seq_lens) all lie between
+    `start` (0 if not given) and `end` (seq_lens), int32 [B] each; their entries of
+    block_table become -1.  Returns (free_pages, count): what is left of free_pages
+    behind the pages_used (int32 [1]) of the step, then the pages that no row holds any
+    more, then -1, as many entries as the pool has pages; and how many pages that is
+    (int32 [1]).  ``out`` gives both tensors; ``workspace`` as in awq_linear_ex."""
+    i32 = _torch().int32
+    B, blocks = _table_arg(block_table, seq_lens)
+    for t, name in ((start, "start"), (end, "end")):
+        if t is not None:
+            _check(t, name, i32, (B,))
+    _tensor(shared, "shared", i32)
+    if shared.dim() != 1 or shared.shape[0] < 1:
+        raise ValueError("shared must be 1-D [pages]")
+    pages = shared.shape[0]
+    _free_arg(free_pages, pages_used, "pages_used")
+    if out is not None:
+        if len(out) != 2:
+            raise ValueError("out must be (free_pages, count)")
+        _tensor(out[0], "out", i32)
+        if out[0].dim() != 1:
+            raise ValueError("out's free_pages must be 1-D")
+        _check(out[1], "count", i32, (1,))
+    need = 0 if workspace is None else lib.awq_kv_release_workspace_size(pages, free_pages.shape[0])
+    ws, ws_bytes = _scratch(workspace, need, shared)
+    dev = _one_gpu((block_table, "block_table"), *_named(
+        seq_lens=seq_lens, start=start, end=end, shared=shared, free_pages=free_pages, pages_used=pages_used,
+        out=None if out is None else out[0], count=None if out is None else out[1], workspace=ws))
+    if out is None:
+        out = shared.new_empty(pages + 1).split_with_sizes((pages, 1))
+    st = _launch(lib.awq_kv_release, dev, _address(block_table), B, blocks, page_size, _address(seq_lens),
+                 _address(start), _address(end), _address(shared), pages, _address(free_pages), free_pages.shape[0],
+                 _address(pages_used), _address(out[0]), out[0].shape[0], out[1].data_ptr(), _address(ws), ws_bytes)
+    check(st, "awq_kv_release")
+    return tuple(out)
+
+
+def awq_kv_compact_workspace_size(num_pages: int, page_size: int) -> int:
+    return int(lib.awq_kv_compact_workspace_size(num_pages, page_size))
+
+
+def awq_kv_compact(cache, block_table, seq_lens, shared, out=None, workspace="auto"):
+    """Move the n pages that the rows (of seq_lens tokens) use to the front of the pool;
+    block_table and `shared` are updated in place.  Returns (free_pages, num_used): the
+    pages from n on, then -1, int32 [pages]; n, int32 [1].  ``out`` gives both tensors;
+    ``workspace`` as in awq_linear_ex."""
+    i32 = _torch().int32
+    c, cfg = _cache_arg(cache)
+    B, blocks = _table_arg(block_table, seq_lens)
+    _check(shared, "shared", i32, (c.num_pages,))
+    if out is not None:
+        if len(out) != 2:
+            raise ValueError("out must be (free_pages, num_used)")
+        _check(out[0], "free_pages", i32, (c.num_pages,))
+        _check(out[1], "num_used", i32, (1,))
+    need = 0 if workspace is None else lib.awq_kv_compact_workspace_size(c.num_pages, c.page_size)
+    ws, ws_bytes = _scratch(workspace, need, shared)
+    dev = _one_gpu(*_cache_tensors(cache), *_named(
+        block_table=block_table, seq_lens=seq_lens, shared=shared, out=None if out is None else out[0],
+        num_used=None if out is None else out[1], workspace=ws))
+    if out is None:
+        out = shared.new_empty(c.num_pages + 1).split_with_sizes((c.num_pages, 1))
+    st = _launch(lib.awq_kv_compact, dev, c, cfg, _address(block_table), B, blocks, _address(seq_lens),
+                 _address(shared), out[0].data_ptr(), out[1].data_ptr(), _address(ws), ws_bytes)
+    check(st, "awq_kv_compact")
+    return tuple(out)
 
 
 # ---- rotary positions -------------------------------------------------------------

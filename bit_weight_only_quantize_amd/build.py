@@ -34,9 +34,11 @@ SOURCES = [
     "search.hip",
     "kv_cache.hip",
     "kv_attention.hip",
+    "kv_pages.hip",
     "rope.hip",
     "api.cpp",
     "api_kv.cpp",
+    "api_kv_pages.cpp",
     "api_rope.cpp",
 ]
 

@@ -199,6 +199,44 @@ hipError_t launch_kv_append(const uint16_t *K, const uint16_t *V, XType xt, int6
 hipError_t launch_kv_gather(const KvCache &c, const int32_t *slots, int64_t T, void *K, void *V,
                             YType ot, hipStream_t st);
 
+// ---- kv_pages.hip: pages copied, shared, given back, drawn together ---------------
+struct ForkArgs {
+  const int32_t *parents, *children, *lens;   // [n]
+  int n, num_seqs, max_blocks, pshift;
+  int32_t *table, *shared;
+  int64_t pages;
+  const int32_t *free_pages;
+  int64_t num_free;
+  const int32_t *taken;                       // [1] or null: 0
+  int32_t *pages_used;
+};
+struct ReleaseArgs {
+  int32_t *table;
+  int num_seqs, max_blocks, pshift;
+  const int32_t *seq_lens, *start, *end;      // start null: 0; end null: seq_lens
+  int32_t *shared;
+  int64_t pages;
+  const int32_t *free_pages;
+  int64_t num_free;
+  const int32_t *taken;                       // [1] or null: 0
+  int32_t *free_out;
+  int64_t num_out;
+  int32_t *count;
+};
+struct CompactArgs {
+  int32_t *table;
+  int num_seqs, max_blocks, pshift;
+  const int32_t *seq_lens;
+  int32_t *shared, *free_out, *num_used;
+  int32_t *moves, *holes, *movers, *place;    // the launcher's, in the workspace
+};
+hipError_t launch_kv_copy_pages(const KvCache &c, const int32_t *src, const int32_t *dst, int64_t n, hipStream_t st);
+hipError_t launch_kv_fork(const ForkArgs &a, const KvCache &c, hipStream_t st);
+size_t kv_release_workspace(int64_t pages, int64_t num_free);
+hipError_t launch_kv_release(const ReleaseArgs &a, void *workspace, hipStream_t st);
+size_t kv_compact_workspace(int64_t pages);
+hipError_t launch_kv_compact(CompactArgs a, const KvCache &c, void *workspace, hipStream_t st);
+
 // ---- rope.hip: rotary positions ---------------------------------------------------
 struct RopeArgs {
   const int32_t *positions;   // [T]

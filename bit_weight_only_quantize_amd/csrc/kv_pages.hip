@@ -1,0 +1,496 @@
+// Pages of the 4-bit key/value cache on gfx950: copied (awq_kv_copy_pages), shared by
+// branches of a request (awq_kv_fork), given back (awq_kv_release) and drawn together
+// at the front of the pool (awq_kv_compact).
+//
+// A page is three runs of memory, its codes, steps and zero points, each a multiple
+// of 16 bytes, so copies are of 16-byte units with no regard to what they hold.
+// `shared` counts, for each page, the block tables' entries that hold it beyond the
+// first: awq_kv_assign's fresh pages have none and it need not know of the counts.
+// Counts change by atomic additions, whose order does not matter, and lists are
+// written by rank, so every result is the same whatever the order of execution.
+
+#include "awq_internal.h"
+#include "device_common.h"
+
+namespace awq {
+
+constexpr int kPageThreads = 256;
+constexpr int kPieceUnits = 1024;          // 16-byte units that a workgroup copies at a time
+
+// The runs of a page, in 16-byte units.
+struct PageRuns {
+  int64_t codes, scales, zeros;
+};
+__host__ __device__ __forceinline__ PageRuns page_runs(const KvCache &c) {
+  const int64_t n = (int64_t)c.page_size * c.heads;
+  return PageRuns{n * c.head_dim / 16, n / 4, c.zeros ? n / 8 : 0};
+}
+__host__ __device__ __forceinline__ int64_t pieces_of(const PageRuns &r) {
+  return (r.codes + r.scales + r.zeros + kPieceUnits - 1) / kPieceUnits;
+}
+
+// Piece `piece` of page `from` to page `to`, by a workgroup: four loads in flight per lane.
+__device__ __forceinline__ void copy_piece(const KvCache &c, const PageRuns &r, int64_t from, int64_t to, int64_t piece) {
+  constexpr int kPer = kPieceUnits / kPageThreads;
+  u32x4 v[kPer];
+  int64_t src[kPer], dst[kPer];                      // addresses; 0: nothing
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t u = piece * kPieceUnits + i * kPageThreads + threadIdx.x;
+    const bool in_codes = u < r.codes, in_scales = u < r.codes + r.scales;
+    const void *base = in_codes ? (const void *)c.codes : in_scales ? (const void *)c.scales : (const void *)c.zeros;
+    const int64_t run = in_codes ? r.codes : in_scales ? r.scales : r.zeros;
+    const int64_t at = in_codes ? u : in_scales ? u - r.codes : u - r.codes - r.scales;
+    const bool in = u < r.codes + r.scales + r.zeros;
+    src[i] = in ? reinterpret_cast<int64_t>(base) + (from * run + at) * 16 : 0;
+    dst[i] = reinterpret_cast<int64_t>(base) + (to * run + at) * 16;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (src[i]) v[i] = *reinterpret_cast<const u32x4 *>(src[i]);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (src[i]) *reinterpret_cast<u32x4 *>(dst[i]) = v[i];
+}
+
+__device__ __forceinline__ bool is_page(int64_t id, int64_t pages) { return id >= 0 && id < pages; }
+
+// Blocks that `len` tokens take of a row of max_blocks.
+__device__ __forceinline__ int64_t blocks_of(int64_t len, int pshift, int max_blocks) {
+  const int64_t n = len > 0 ? (len + ((int64_t)1 << pshift) - 1) >> pshift : 0;
+  return n < max_blocks ? n : max_blocks;
+}
+
+// ---- copy ---------------------------------------------------------------------------
+// Bound by memory: a read and a write of every byte.
+__global__ __launch_bounds__(kPageThreads) void kv_copy_pages_kernel(KvCache c, const int32_t *__restrict__ src,
+                                                                     const int32_t *__restrict__ dst, int64_t units,
+                                                                     int64_t pieces) {
+  const PageRuns r = page_runs(c);
+  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int64_t i = u / pieces;
+    const int32_t from = src[i], to = dst[i];
+    if (is_page(from, c.pages) && is_page(to, c.pages) && from != to) copy_piece(c, r, from, to, u - i * pieces);
+  }
+}
+
+// ---- fork ---------------------------------------------------------------------------
+// Workgroup (i, part): fork i's share of the table entries, and of the page that is copied.
+// The free page that it takes is numbered by the forks before it that take one, which every
+// workgroup counts itself: a few hundred pairs of loads, where an exchange between
+// workgroups would cost another launch.  Bound by latency: lists, lengths, the parent's
+// entries, the page.
+struct ForkPage {
+  int64_t last;            // the parent's page that is copied, or -1
+  bool takes;
+};
+__device__ __forceinline__ ForkPage fork_page(const ForkArgs &a, int i) {
+  const int parent = a.parents[i], child = a.children[i];
+  ForkPage f = {-1, false};
+  if (!is_page(parent, a.num_seqs) || !is_page(child, a.num_seqs) || parent == child) return f;
+  const int64_t cap = (int64_t)a.max_blocks << a.pshift;
+  int64_t len = a.lens[i];
+  len = len < cap ? len : cap;
+  if (len <= 0 || (len & (((int64_t)1 << a.pshift) - 1)) == 0) return f;
+  f.last = a.table[(int64_t)parent * a.max_blocks + (len >> a.pshift)];
+  f.takes = is_page(f.last, a.pages);
+  return f;
+}
+
+__global__ __launch_bounds__(kPageThreads) void kv_fork_kernel(ForkArgs a, KvCache c) {
+  __shared__ int64_t s_count[kPageThreads / 64];
+  const int i = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
+  const int64_t taken = a.taken && *a.taken > 0 ? *a.taken : 0;
+  // forks before i that take a page (the last workgroup: all of them, for pages_used)
+  const bool reports = i == a.n - 1 && part == 0;
+  int64_t before = 0;
+  for (int64_t j = threadIdx.x; j < i; j += kPageThreads) before += fork_page(a, (int)j).takes;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) before += __shfl_xor(before, d, 64);
+  if ((threadIdx.x & 63) == 0) s_count[threadIdx.x >> 6] = before;
+  __syncthreads();
+  before = 0;
+#pragma unroll
+  for (int w = 0; w < kPageThreads / 64; ++w) before += s_count[w];
+  const ForkPage mine = fork_page(a, i);
+  if (reports && threadIdx.x == 0) {
+    const int64_t all = taken + before + mine.takes;
+    *a.pages_used = all > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)all;
+  }
+  const int parent = a.parents[i], child = a.children[i];
+  if (!is_page(parent, a.num_seqs) || !is_page(child, a.num_seqs) || parent == child) return;
+  const int64_t cap = (int64_t)a.max_blocks << a.pshift;
+  int64_t len = a.lens[i];
+  len = len < 0 ? 0 : len < cap ? len : cap;
+  const int64_t full = len >> a.pshift;
+  const int32_t *from = a.table + (int64_t)parent * a.max_blocks;
+  int32_t *to = a.table + (int64_t)child * a.max_blocks;
+  for (int64_t j = (int64_t)part * kPageThreads + threadIdx.x; j < full; j += (int64_t)parts * kPageThreads) {
+    const int32_t id = from[j];
+    to[j] = id;
+    if (is_page(id, a.pages)) atomicAdd(a.shared + id, 1);
+  }
+  if ((len & (((int64_t)1 << a.pshift) - 1)) == 0) return;
+  int64_t fresh = -1;
+  if (mine.takes && taken + before < a.num_free) fresh = a.free_pages[taken + before];
+  if (!is_page(fresh, a.pages)) fresh = -1;
+  if (part == 0 && threadIdx.x == 0) to[full] = (int32_t)fresh;
+  if (fresh < 0 || fresh == mine.last) return;
+  const PageRuns r = page_runs(c);
+  const int64_t pieces = pieces_of(r);
+  for (int64_t p = part; p < pieces; p += parts) copy_piece(c, r, mine.last, fresh, p);
+}
+
+__global__ void kv_fork_none_kernel(const int32_t *taken, int32_t *pages_used) {
+  *pages_used = taken && *taken > 0 ? *taken : 0;
+}
+
+// ---- ranks ---------------------------------------------------------------------------
+// A workgroup ranks the flagged ones of 32 items per thread, item r * THREADS + thread in
+// round r so that loads are coalesced: each wave's ballots are counted in LDS, and one
+// scan of the 32 * waves counts gives every ballot's first rank.
+constexpr int kRounds = 32;
+constexpr int kChunk = kRounds * kPageThreads;         // items of a workgroup of many
+constexpr int kAlone = 1024;                           // threads of a single workgroup
+constexpr int64_t kAloneItems = (int64_t)kRounds * kAlone;
+
+template <int THREADS>
+struct Ranks {
+  static constexpr int kWaves = THREADS / 64, kCounts = kRounds * kWaves;
+  struct Shared {
+    int32_t first[kCounts];
+    int32_t total;
+  };
+  Shared &s;
+  uint32_t mask = 0;                                   // bit r: the thread's item of round r
+  __device__ __forceinline__ explicit Ranks(Shared &sh) : s(sh) {}
+  // All threads call it; returns the number of flagged items.
+  template <class F>
+  __device__ __forceinline__ int32_t count(F flag) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll 8
+    for (int r = 0; r < kRounds; ++r) {
+      const bool f = flag(r * THREADS + (int)threadIdx.x);
+      mask |= (uint32_t)f << r;
+      const uint64_t b = __ballot(f);
+      if (lane == 0) s.first[r * kWaves + wave] = __popcll(b);
+    }
+    __syncthreads();
+    if (wave == 0) {                                   // exclusive scan, kCounts / 64 per lane
+      constexpr int kPer = kCounts / 64;
+      int32_t v[kPer], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        v[i] = sum;
+        sum += s.first[lane * kPer + i];
+      }
+      int32_t up = sum;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int32_t x = __shfl_up(up, d, 64);
+        if (lane >= d) up += x;
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) s.first[lane * kPer + i] = up - sum + v[i];
+      if (lane == 63) s.total = up;
+    }
+    __syncthreads();
+    return s.total;
+  }
+  // Flagged items before the thread's item of round r, and whether it is flagged itself.
+  __device__ __forceinline__ int32_t rank(int r, bool &f) const {
+    f = (mask >> r) & 1u;
+    const uint64_t below = __ballot(f) & (((uint64_t)1 << (threadIdx.x & 63)) - 1);
+    return s.first[r * kWaves + (threadIdx.x >> 6)] + __popcll(below);
+  }
+};
+
+// Sum of n counts and of the first `mine` of them, by a workgroup of kPageThreads.
+struct Sums {
+  int64_t before, all;
+};
+__device__ __forceinline__ Sums sum_counts(const int32_t *counts, int64_t n, int64_t mine) {
+  __shared__ int64_t s_sum[2][kPageThreads / 64];
+  Sums t = {0, 0};
+  for (int64_t i = threadIdx.x; i < n; i += kPageThreads) {
+    const int64_t x = counts[i];
+    t.all += x;
+    t.before += i < mine ? x : 0;
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) {
+    t.all += __shfl_xor(t.all, d, 64);
+    t.before += __shfl_xor(t.before, d, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    s_sum[0][threadIdx.x >> 6] = t.before;
+    s_sum[1][threadIdx.x >> 6] = t.all;
+  }
+  __syncthreads();
+  t = Sums{0, 0};
+#pragma unroll
+  for (int w = 0; w < kPageThreads / 64; ++w) {
+    t.before += s_sum[0][w];
+    t.all += s_sum[1][w];
+  }
+  return t;
+}
+
+// ---- release ---------------------------------------------------------------------------
+// First launch, a workgroup per row: released entries become -1 and their pages' counts
+// fall by one, below zero for a page without another holder.  Then the free list: what is
+// left of the old one, and the pages below zero by number, ranked by one workgroup where
+// they are few (one launch), else in chunks (two: counts, then places).  Few: a pool of
+// 7000 pages took ... in one workgroup.
+__global__ __launch_bounds__(kPageThreads) void kv_release_rows_kernel(ReleaseArgs a) {
+  const int64_t b = blockIdx.x;
+  const int64_t cap = (int64_t)a.max_blocks << a.pshift;
+  int64_t len = a.seq_lens[b];
+  len = len < 0 ? 0 : len < cap ? len : cap;
+  int64_t lo = a.start ? a.start[b] : 0, hi = a.end ? a.end[b] : len;
+  lo = lo < 0 ? 0 : lo;
+  // a page whose tokens below the length all lie in [lo, hi)
+  const int64_t first = (lo + ((int64_t)1 << a.pshift) - 1) >> a.pshift;
+  const int64_t stop = hi >= len ? blocks_of(len, a.pshift, a.max_blocks) : hi > 0 ? hi >> a.pshift : 0;
+  int32_t *row = a.table + b * a.max_blocks;
+  for (int64_t j = first + threadIdx.x; j < stop; j += kPageThreads) {
+    const int32_t id = row[j];
+    row[j] = -1;
+    if (is_page(id, a.pages)) atomicSub(a.shared + id, 1);
+  }
+}
+
+// Item i of the list: an entry of the old free list, then the pages.
+struct ReleaseItems {
+  const ReleaseArgs &a;
+  int64_t taken;
+  __device__ __forceinline__ bool flag(int64_t i) const {
+    if (i < a.num_free) return i >= taken && is_page(a.free_pages[i], a.pages);
+    return i < a.num_free + a.pages && a.shared[i - a.num_free] < 0;
+  }
+  __device__ __forceinline__ void place(int64_t i, int64_t at) const {
+    const int64_t id = i < a.num_free ? (int64_t)a.free_pages[i] : i - a.num_free;
+    if (at < a.num_out) a.free_out[at] = (int32_t)id;
+    if (i >= a.num_free) a.shared[id] = 0;
+  }
+};
+__device__ __forceinline__ int64_t taken_of(const ReleaseArgs &a) { return a.taken && *a.taken > 0 ? *a.taken : 0; }
+
+__global__ __launch_bounds__(kPageThreads) void kv_release_count_kernel(ReleaseArgs a, int32_t *counts) {
+  __shared__ Ranks<kPageThreads>::Shared s;
+  Ranks<kPageThreads> ranks(s);
+  const ReleaseItems items{a, taken_of(a)};
+  const int64_t base = (int64_t)blockIdx.x * kChunk;
+  const int32_t n = ranks.count([&](int i) { return items.flag(base + i); });
+  if (threadIdx.x == 0) counts[blockIdx.x] = n;
+}
+
+// THREADS = kAlone: one workgroup has all items.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_release_list_kernel(ReleaseArgs a, const int32_t *counts) {
+  __shared__ typename Ranks<THREADS>::Shared s;
+  Ranks<THREADS> ranks(s);
+  const ReleaseItems items{a, taken_of(a)};
+  const int64_t base = (int64_t)blockIdx.x * (kRounds * THREADS);
+  const int32_t n = ranks.count([&](int i) { return items.flag(base + i); });
+  Sums sums = {0, n};
+  if constexpr (THREADS != kAlone) sums = sum_counts(counts, gridDim.x, blockIdx.x);
+  for (int r = 0; r < kRounds; ++r) {
+    bool f;
+    const int64_t at = sums.before + ranks.rank(r, f);
+    if (f) items.place(base + r * THREADS + threadIdx.x, at);
+  }
+  for (int64_t i = sums.all + (int64_t)blockIdx.x * THREADS + threadIdx.x; i < a.num_out; i += (int64_t)gridDim.x * THREADS)
+    a.free_out[i] = -1;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.count = (int32_t)(sums.all > 0x7FFFFFFF ? 0x7FFFFFFF : sums.all);
+}
+
+// ---- compact ---------------------------------------------------------------------------
+// Of n pages in use, those numbered n or more move into the holes below n, the last into
+// the first: the k-th hole from the front, number p, has p - (used ones before it) = k, and
+// the k-th page from the back has n - 1 - (used ones before it) = k, so both lists are
+// written from one ranking of the used pages.  One workgroup marks and ranks a pool of up
+// to 32768 pages in LDS (one launch); a larger one takes four: clear, mark, count, list.
+// The last launch copies the pages, moves their counts and renumbers the tables.
+__global__ __launch_bounds__(kPageThreads) void kv_compact_clear_kernel(uint8_t *used, int64_t pages) {
+  for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < pages; i += (int64_t)gridDim.x * kPageThreads)
+    used[i] = 0;
+}
+
+__global__ __launch_bounds__(kPageThreads) void kv_compact_mark_kernel(CompactArgs a, int64_t pages, uint8_t *used) {
+  const int64_t b = blockIdx.x, n = blocks_of(a.seq_lens[b], a.pshift, a.max_blocks);
+  const int32_t *row = a.table + b * a.max_blocks;
+  for (int64_t j = threadIdx.x; j < n; j += kPageThreads) {
+    const int32_t id = row[j];
+    if (is_page(id, pages)) used[id] = 1;
+  }
+}
+
+__global__ __launch_bounds__(kPageThreads) void kv_compact_count_kernel(const uint8_t *used, int64_t pages, int32_t *counts) {
+  __shared__ Ranks<kPageThreads>::Shared s;
+  Ranks<kPageThreads> ranks(s);
+  const int64_t base = (int64_t)blockIdx.x * kChunk;
+  const int32_t n = ranks.count([&](int i) { return base + i < pages && used[base + i] != 0; });
+  if (threadIdx.x == 0) counts[blockIdx.x] = n;
+}
+
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void kv_compact_list_kernel(CompactArgs a, int64_t pages, const uint8_t *used,
+                                                                  const int32_t *counts) {
+  __shared__ typename Ranks<THREADS>::Shared s;
+  __shared__ uint32_t marks[THREADS == kAlone ? kAloneItems / 32 : 1];
+  Ranks<THREADS> ranks(s);
+  const int64_t base = (int64_t)blockIdx.x * (kRounds * THREADS);
+  int32_t in_chunk;
+  if constexpr (THREADS == kAlone) {
+    marks[threadIdx.x] = 0;
+    __syncthreads();
+    // a wave per row at a time
+    for (int64_t b = threadIdx.x >> 6; b < a.num_seqs; b += kAlone / 64) {
+      const int64_t n = blocks_of(a.seq_lens[b], a.pshift, a.max_blocks);
+      for (int64_t j = threadIdx.x & 63; j < n; j += 64) {
+        const int32_t id = a.table[b * a.max_blocks + j];
+        if (is_page(id, pages)) atomicOr(&marks[id >> 5], 1u << (id & 31));
+      }
+    }
+    __syncthreads();
+    in_chunk = ranks.count([&](int i) { return i < pages && ((marks[i >> 5] >> (i & 31)) & 1u); });
+  } else {
+    in_chunk = ranks.count([&](int i) { return base + i < pages && used[base + i] != 0; });
+  }
+  Sums sums = {0, in_chunk};
+  if constexpr (THREADS != kAlone) sums = sum_counts(counts, gridDim.x, blockIdx.x);
+  const int64_t n = sums.all;
+  for (int r = 0; r < kRounds; ++r) {
+    bool f;
+    const int64_t p = base + r * THREADS + threadIdx.x, before = sums.before + ranks.rank(r, f);
+    if (p >= pages) continue;
+    if (p < n && !f) a.holes[p - before] = (int32_t)p;
+    if (p >= n && f) {
+      a.movers[n - 1 - before] = (int32_t)p;
+      a.place[p] = (int32_t)(n - 1 - before);
+    }
+    if (p >= n && !f) a.shared[p] = 0;
+    if (p == n) *a.moves = (int32_t)(n - before);
+    a.free_out[p] = p + n < pages ? (int32_t)(p + n) : -1;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.num_used = (int32_t)n;
+    if (n == pages) *a.moves = 0;
+  }
+}
+
+// The first num_seqs workgroups renumber a row each, the others copy.
+__global__ __launch_bounds__(kPageThreads) void kv_compact_move_kernel(CompactArgs a, KvCache c) {
+  const int64_t b = blockIdx.x, n = *a.num_used, moves = *a.moves;
+  if (b < a.num_seqs) {
+    const int64_t blocks = blocks_of(a.seq_lens[b], a.pshift, a.max_blocks);
+    int32_t *row = a.table + b * a.max_blocks;
+    for (int64_t j = threadIdx.x; j < blocks; j += kPageThreads) {
+      const int32_t id = row[j];
+      if (id >= n && id < c.pages) row[j] = a.holes[a.place[id]];
+    }
+    return;
+  }
+  const PageRuns r = page_runs(c);
+  const int64_t pieces = pieces_of(r), units = moves * pieces;
+  for (int64_t u = b - a.num_seqs; u < units; u += gridDim.x - a.num_seqs) {
+    const int64_t k = u / pieces, piece = u - k * pieces;
+    const int32_t from = a.movers[k], to = a.holes[k];
+    if (piece == 0 && threadIdx.x == 0) {
+      a.shared[to] = a.shared[from];
+      a.shared[from] = 0;
+    }
+    copy_piece(c, r, from, to, piece);
+  }
+}
+
+// ---- launch -----------------------------------------------------------------------------
+namespace {
+constexpr int64_t kCopyWgs = 4096;         // 16 workgroups per CU
+int64_t chunks_of(int64_t items) { return (items + kChunk - 1) / kChunk; }
+size_t region(int64_t bytes) { return ((size_t)bytes + 255) & ~(size_t)255; }
+}  // namespace
+
+hipError_t launch_kv_copy_pages(const KvCache &c, const int32_t *src, const int32_t *dst, int64_t n, hipStream_t st) {
+  const int64_t pieces = pieces_of(page_runs(c)), units = n * pieces;
+  kv_copy_pages_kernel<<<(unsigned)(units < kCopyWgs ? units : kCopyWgs), kPageThreads, 0, st>>>(c, src, dst, units, pieces);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_fork(const ForkArgs &a, const KvCache &c, hipStream_t st) {
+  if (a.n == 0) {
+    kv_fork_none_kernel<<<1, 1, 0, st>>>(a.taken, a.pages_used);
+    return hipGetLastError();
+  }
+  // a part for each piece of the page, while that fills the card
+  int64_t parts = pieces_of(page_runs(c));
+  const int64_t most = (kCopyWgs + a.n - 1) / a.n;
+  parts = parts < most ? parts : most;
+  kv_fork_kernel<<<dim3((unsigned)a.n, (unsigned)parts), kPageThreads, 0, st>>>(a, c);
+  return hipGetLastError();
+}
+
+size_t kv_release_workspace(int64_t pages, int64_t num_free) {
+  const int64_t items = pages + num_free;
+  return items <= kAloneItems ? 0 : region(chunks_of(items) * 4);
+}
+
+hipError_t launch_kv_release(const ReleaseArgs &a, void *workspace, hipStream_t st) {
+  if (a.num_seqs > 0 && a.max_blocks > 0) {
+    kv_release_rows_kernel<<<(unsigned)a.num_seqs, kPageThreads, 0, st>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int64_t items = a.pages + a.num_free;
+  if (items <= kAloneItems) {
+    kv_release_list_kernel<kAlone><<<1, kAlone, 0, st>>>(a, nullptr);
+    return hipGetLastError();
+  }
+  int32_t *counts = reinterpret_cast<int32_t *>(workspace);
+  kv_release_count_kernel<<<(unsigned)chunks_of(items), kPageThreads, 0, st>>>(a, counts);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  kv_release_list_kernel<kPageThreads><<<(unsigned)chunks_of(items), kPageThreads, 0, st>>>(a, counts);
+  return hipGetLastError();
+}
+
+// Workspace: moves, holes, movers, places, and for a large pool the marks and the chunks' counts.
+size_t kv_compact_workspace(int64_t pages) {
+  const size_t lists = 256 + 3 * region(pages * 4);
+  return pages <= kAloneItems ? lists : lists + region(pages) + region(chunks_of(pages) * 4);
+}
+
+hipError_t launch_kv_compact(CompactArgs a, const KvCache &c, void *workspace, hipStream_t st) {
+  char *w = reinterpret_cast<char *>(workspace);
+  const size_t list = region(c.pages * 4);
+  a.moves = reinterpret_cast<int32_t *>(w);
+  a.holes = reinterpret_cast<int32_t *>(w + 256);
+  a.movers = reinterpret_cast<int32_t *>(w + 256 + list);
+  a.place = reinterpret_cast<int32_t *>(w + 256 + 2 * list);
+  hipError_t e;
+  if (c.pages <= kAloneItems) {
+    kv_compact_list_kernel<kAlone><<<1, kAlone, 0, st>>>(a, c.pages, nullptr, nullptr);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  } else {
+    uint8_t *used = reinterpret_cast<uint8_t *>(w + 256 + 3 * list);
+    int32_t *counts = reinterpret_cast<int32_t *>(w + 256 + 3 * list + region(c.pages));
+    const unsigned chunks = (unsigned)chunks_of(c.pages);
+    kv_compact_clear_kernel<<<chunks, kPageThreads, 0, st>>>(used, c.pages);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.num_seqs > 0) {
+      kv_compact_mark_kernel<<<(unsigned)a.num_seqs, kPageThreads, 0, st>>>(a, c.pages, used);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    kv_compact_count_kernel<<<chunks, kPageThreads, 0, st>>>(used, c.pages, counts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    kv_compact_list_kernel<kPageThreads><<<chunks, kPageThreads, 0, st>>>(a, c.pages, used, counts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  const int64_t units = c.pages / 2 * pieces_of(page_runs(c));       // (at most that many move)
+  const int64_t copies = units < 1 ? 1 : units < kCopyWgs ? units : kCopyWgs;
+  kv_compact_move_kernel<<<(unsigned)(a.num_seqs + copies), kPageThreads, 0, st>>>(a, c);
+  return hipGetLastError();
+}
+
+}  // namespace awq

@@ -587,6 +587,109 @@ size_t awq_kv_attention_workspace_size(int64_t num_tokens, int32_t num_seqs, int
                                        const awq_kv_cache *cache, awq_config cfg,
                                        int32_t max_query_len, int64_t max_seq_len, int32_t window);
 
+/* ---- pages: copied, shared, given back, drawn together ----------------------
+ *
+ * Rows of the block table may share pages: `shared`, device int32 [num_pages],
+ * counts for each page the table entries that hold it beyond the first.  All zeros
+ * at the start; awq_kv_fork adds, awq_kv_release subtracts, awq_kv_compact moves the
+ * counts along, and a page that awq_kv_assign hands out has none.  Nothing may be
+ * appended to a page that is shared (awq_kv_fork shares full pages only, so a
+ * request that appends behind its own last token never does).
+ *
+ * A free list is device int32 [num_free], ids to take from the front and entries
+ * outside [0, num_pages) for none.  `taken`, device int32 [1] or NULL, says how many of
+ * its first entries earlier calls of the step have used: the pages_used that
+ * awq_kv_assign or awq_kv_fork wrote.  Lists padded with -1 to num_pages entries
+ * serve a captured step: a release writes the next step's list.
+ *
+ * Results do not depend on any order of execution.  What these calls write may
+ * overlap neither what they read nor itself. */
+
+/*
+ * awq_kv_copy_pages - codes, steps and zero points of page src[i] to page dst[i].
+ *   src, dst  device, int32 [num_copies]; a pair with an id outside the cache is
+ *             skipped.  No id may be written twice, nor be read by one pair and
+ *             written by another (such pages end with unspecified contents).
+ * num_copies at most 2^27.
+ */
+awq_status awq_kv_copy_pages(const awq_kv_cache *cache, awq_config cfg, const int32_t *src,
+                             const int32_t *dst, int64_t num_copies, awq_stream_t stream);
+
+/*
+ * awq_kv_fork - branches of requests: row children[i] of the block table becomes a
+ * branch of the first lens[i] tokens of row parents[i].
+ *   parents, children, lens  device, int32 [num_forks].  Children are distinct rows,
+ *             and none is a parent in the same call (their entries and counts would be
+ *             unspecified); what they held before is not released.  A fork of a row
+ *             outside the table, or of a row to itself, does nothing.
+ *   block_table  device, int32 [num_seqs][max_blocks], updated in place: the child gets
+ *             the parent's entries of full pages, which are now shared (page j full:
+ *             (j + 1) P <= lens[i]), and for a last page that is not full a page of its
+ *             own, with a copy of the parent's whole page.  Entries behind are left alone.
+ *   free_pages, taken  where those come from, in the forks' order.  A fork that finds
+ *             none left, or whose parent has no such page, gets -1.
+ *   pages_used  device, int32 [1], written: taken and the pages that the forks need, also
+ *             beyond num_free.
+ * Lengths beyond the table are cut to it, negative ones count as 0.  num_forks at most
+ * 65535; max_blocks * P < 2^31.
+ */
+awq_status awq_kv_fork(const awq_kv_cache *cache, awq_config cfg, const int32_t *parents,
+                       const int32_t *children, const int32_t *lens, int32_t num_forks,
+                       int32_t *block_table, int32_t num_seqs, int32_t max_blocks, int32_t *shared,
+                       const int32_t *free_pages, int32_t num_free, const int32_t *taken,
+                       int32_t *pages_used, awq_stream_t stream);
+
+/*
+ * awq_kv_release - rows give pages back: all of them, those behind a length, or those
+ * that a window has left behind.
+ *   seq_lens  device, int32 [num_seqs]: tokens that each row holds.
+ *   start, end  device, int32 [num_seqs], or NULL for 0 and seq_lens: of row b, the pages
+ *             whose tokens below seq_lens[b] all lie in [start[b], end[b]).
+ *   block_table  device, int32 [num_seqs][max_blocks], updated in place: released entries
+ *             become -1.
+ *   shared    device, int32 [num_pages], updated in place.
+ *   free_pages, num_free, taken  the free list so far.
+ *   free_out  device, int32 [num_out], written: the old list's entries from `taken` on
+ *             that are pages, in order, then the pages that no row holds any more, by
+ *             number, then -1.  (num_pages entries always hold them.)
+ *   num_free_out  device, int32 [1], written: how many pages that are, also beyond num_out.
+ *   workspace  device, 256-byte aligned, awq_kv_release_workspace_size() bytes (NULL
+ *             when that is 0); scratch, not to be shared by calls that overlap in time.
+ * A page that the rows release more often than they hold it is freed once.  num_pages *
+ * P at most 2^31, max_blocks * P < 2^31, num_seqs at most 2^20.
+ */
+awq_status awq_kv_release(int32_t *block_table, int32_t num_seqs, int32_t max_blocks,
+                          int32_t page_size, const int32_t *seq_lens, const int32_t *start,
+                          const int32_t *end, int32_t *shared, int64_t num_pages,
+                          const int32_t *free_pages, int32_t num_free, const int32_t *taken,
+                          int32_t *free_out, int32_t num_out, int32_t *num_free_out,
+                          void *workspace, size_t workspace_bytes, awq_stream_t stream);
+
+/* Bytes of workspace that awq_kv_release needs; 0 when it needs none and on invalid arguments. */
+size_t awq_kv_release_workspace_size(int64_t num_pages, int32_t num_free);
+
+/*
+ * awq_kv_compact - the n pages in use become pages 0 .. n - 1: those numbered n or more
+ * move into the unused ones below n, the last into the first, and so on.
+ *   block_table  device, int32 [num_seqs][max_blocks], updated in place: the entries of
+ *             each row's first ceil(seq_lens / P) pages say which pages are in use, and
+ *             are renumbered; others, and ids outside the cache, are left alone.
+ *   shared    device, int32 [num_pages], updated in place: counts move along, and are 0
+ *             from n on.
+ *   free_out  device, int32 [num_pages], written: n, n + 1, ..., num_pages - 1, then -1.
+ *   num_used  device, int32 [1], written: n.
+ *   workspace  device, 256-byte aligned, awq_kv_compact_workspace_size() bytes; scratch,
+ *             not to be shared by calls that overlap in time.
+ * Free lists from before the call are void.  max_blocks * P < 2^31, num_seqs at most 2^20.
+ */
+awq_status awq_kv_compact(const awq_kv_cache *cache, awq_config cfg, int32_t *block_table,
+                          int32_t num_seqs, int32_t max_blocks, const int32_t *seq_lens,
+                          int32_t *shared, int32_t *free_out, int32_t *num_used, void *workspace,
+                          size_t workspace_bytes, awq_stream_t stream);
+
+/* Bytes of workspace that awq_kv_compact needs (0 on invalid arguments). */
+size_t awq_kv_compact_workspace_size(int64_t num_pages, int32_t page_size);
+
 /* ---- rotary positions ------------------------------------------------------
  *
  * Queries and keys are turned by angles that grow with their positions.  Of a
