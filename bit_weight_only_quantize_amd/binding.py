@@ -59,6 +59,8 @@ EXPORTS = (
     "awq_kv_gather",
     "awq_kv_attention",
     "awq_kv_attention_workspace_size",
+    "awq_kv_attention_ex",
+    "awq_kv_attention_ex_workspace_size",
     "awq_kv_copy_pages",
     "awq_kv_fork",
     "awq_kv_release",
@@ -98,6 +100,12 @@ class awq_kv_cache(ctypes.Structure):
                 ("zeros", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("page_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class awq_kv_attention_options(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("prefix_len", ctypes.c_int32), ("prefix_table", ctypes.c_void_p),
+                ("prefix_blocks", ctypes.c_int32)]
 
 
 class awq_rope_args(ctypes.Structure):
@@ -185,6 +193,12 @@ def _load():
     lib.awq_kv_attention.restype = ctypes.c_int
     lib.awq_kv_attention_workspace_size.argtypes = [i64, i32, i32, pc, awq_config, i32, i64, i32]
     lib.awq_kv_attention_workspace_size.restype = ctypes.c_size_t
+    pa = ctypes.POINTER(awq_kv_attention_options)
+    lib.awq_kv_attention_ex.argtypes = [vp, i32, i64, i64, i32, pc, awq_config, vp, i32, vp, vp, i32,
+                                        i32, i64, ctypes.c_float, pa, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.awq_kv_attention_ex.restype = ctypes.c_int
+    lib.awq_kv_attention_ex_workspace_size.argtypes = [i64, i32, i32, pc, awq_config, i32, i64, pa]
+    lib.awq_kv_attention_ex_workspace_size.restype = ctypes.c_size_t
     lib.awq_kv_copy_pages.argtypes = [pc, awq_config, vp, vp, i64, vp]
     lib.awq_kv_copy_pages.restype = ctypes.c_int
     lib.awq_kv_fork.argtypes = [pc, awq_config, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp]
@@ -944,16 +958,22 @@ def awq_kv_gather(cache, slots, out_dtype=None, out=None):
 
 
 def awq_kv_attention_workspace_size(num_tokens: int, num_seqs: int, num_heads: int, cache,
-                                    max_query_len: int, max_seq_len: int, window: int = 0) -> int:
+                                    max_query_len: int, max_seq_len: int, window: int = 0, sinks: int = 0,
+                                    prefix_len: int = 0) -> int:
     """Workspace bytes of awq_kv_attention for these sizes; cache as passed to it."""
     c, cfg = _cache_arg(cache)
+    if sinks != 0 or prefix_len != 0:
+        return int(lib.awq_kv_attention_ex_workspace_size(
+            num_tokens, num_seqs, num_heads, c, cfg, max_query_len, max_seq_len,
+            awq_kv_attention_options(1, window, sinks, prefix_len, None, -(-prefix_len // c.page_size))))
     return int(lib.awq_kv_attention_workspace_size(num_tokens, num_seqs, num_heads, c, cfg,
                                                    max_query_len, max_seq_len, window))
 
 
 def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_query_len=None,
                      max_seq_len=None, scale=None, causal: bool = True, window: int = 0, out=None,
-                     return_lse: bool = False, workspace="auto"):
+                     return_lse: bool = False, workspace="auto", sinks: int = 0, prefix_len: int = 0,
+                     prefix_table=None):
     """Attention of Q (fp16 or bf16 [tokens][num_heads][D], tokens may be strided)
     over the cached keys and values of each request: block_table int32
     [B][max_blocks] and seq_lens int32 [B] as awq_kv_assign gives them.
@@ -966,7 +986,12 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     `window` keys.  Returns O [tokens][num_heads][D], and with return_lse also
     the natural log of the softmax denominators, fp32 [tokens][num_heads]; rows
     of tokens of no request are not written (pass `out` to say what they hold).
-    ``workspace``: as in awq_linear_ex."""
+    ``workspace``: as in awq_linear_ex.
+
+    ``sinks``: beside a window's keys the first `sinks` stay visible.  ``prefix_len``:
+    the first prefix_len tokens of every request are the same, and are read once for all
+    of them, from prefix_table's pages (int32, at least ceil(prefix_len / page_size); the
+    first request's row, if not given)."""
     torch = _torch()
     c, cfg = _cache_arg(cache)
     D = c.head_dim
@@ -994,16 +1019,39 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     if out is not None:
         _check(out, "out", Q.dtype, (T, heads, D))
     stride = _token_rows(Q, "Q", heads, D)
-    need = 0 if workspace is None else lib.awq_kv_attention_workspace_size(
-        T, B, heads, c, cfg, max_query_len, max_seq_len, window)
+    more = sinks != 0 or prefix_len != 0
+    if more:
+        if prefix_table is not None:
+            _tensor(prefix_table, "prefix_table", torch.int32)
+            if prefix_table.dim() != 1:
+                raise ValueError("prefix_table must be 1-D")
+        elif prefix_len > 0 and B > 0:
+            prefix_table = block_table[0]
+        opts = awq_kv_attention_options(int(causal), window, sinks, prefix_len, _address(prefix_table),
+                                        blocks if prefix_table is None else prefix_table.shape[0])
+        need = 0 if workspace is None else lib.awq_kv_attention_ex_workspace_size(
+            T, B, heads, c, cfg, max_query_len, max_seq_len, opts)
+    else:
+        if prefix_table is not None:
+            raise ValueError("prefix_table needs prefix_len")
+        need = 0 if workspace is None else lib.awq_kv_attention_workspace_size(
+            T, B, heads, c, cfg, max_query_len, max_seq_len, window)
     ws, ws_bytes = _scratch(workspace, need, seq_lens)
     dev = _one_gpu(*_cache_tensors(cache), (block_table, "block_table"), (seq_lens, "seq_lens"),
                    None if query_start is None else (query_start, "query_start"),
-                   None if out is None else (out, "out"), None if ws is None else (ws, "workspace"))
+                   None if out is None else (out, "out"), None if ws is None else (ws, "workspace"),
+                   None if prefix_table is None else (prefix_table, "prefix_table"))
     _same_gpu(dev, (Q, "Q"))
     if out is None:
         out = Q.new_empty((T, heads, D))
     lse = Q.new_empty((T, heads), dtype=torch.float32) if return_lse else None
+    if more:
+        st = _launch(lib.awq_kv_attention_ex, dev, _address(Q), _dtype_code(Q.dtype), T, stride, heads, c, cfg,
+                     _address(block_table), blocks, _address(seq_lens), _address(query_start), B, max_query_len,
+                     max_seq_len, D ** -0.5 if scale is None else scale, opts, _address(out), _address(lse),
+                     _address(ws), ws_bytes)
+        check(st, "awq_kv_attention_ex")
+        return (out, lse) if return_lse else out
     st = _launch(lib.awq_kv_attention, dev, _address(Q), _dtype_code(Q.dtype), T, stride, heads, c,
                  cfg, _address(block_table), blocks, _address(seq_lens), _address(query_start), B,
                  max_query_len, max_seq_len, D ** -0.5 if scale is None else scale, int(causal),

@@ -34,6 +34,8 @@ SOURCES = [
     "search.hip",
     "kv_cache.hip",
     "kv_attention.hip",
+    "kv_attention_some.hip",
+    "kv_attention_shared.hip",
     "kv_pages.hip",
     "rope.hip",
     "api.cpp",

@@ -14,8 +14,8 @@ namespace {
 // Sizes of an attention call that its workspace depends on.
 awq_status check_attention_sizes(const char *who, int64_t num_tokens, int32_t num_seqs,
                                  int32_t num_heads, const awq_kv_cache *cache, awq_config cfg,
-                                 int32_t max_query_len, int64_t max_seq_len, int32_t window,
-                                 bool need_ptrs) {
+                                 int32_t max_query_len, int64_t max_seq_len,
+                                 const awq_kv_attention_options *opts, bool need_ptrs) {
   const awq_status st = check_cache(who, cache, cfg, need_ptrs);
   if (st != AWQ_OK) return st;
   if (num_tokens < 0 || num_seqs < 0)
@@ -34,8 +34,143 @@ awq_status check_attention_sizes(const char *who, int64_t num_tokens, int32_t nu
   if ((int64_t)max_query_len * (num_heads / cache->num_kv_heads) > ((int64_t)1 << 30))
     return fail(AWQ_ERR_UNSUPPORTED, "%s: max_query_len=%d times the query heads per key/value head exceeds 2^30",
                 who, max_query_len);
-  if (window < 0) return fail(AWQ_ERR_INVALID_ARG, "%s: window=%d is negative", who, window);
+  if (!opts) return fail(AWQ_ERR_INVALID_ARG, "%s: opts is NULL", who);
+  if (opts->window < 0) return fail(AWQ_ERR_INVALID_ARG, "%s: window=%d is negative", who, opts->window);
+  if (opts->sinks < 0 || opts->sinks > kMaxContext)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: sinks=%d: must be in [0, 2^30]", who, opts->sinks);
+  if (opts->prefix_len < 0 || opts->prefix_blocks < 0)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: negative prefix_len or prefix_blocks", who);
+  if (opts->prefix_len > 0) {
+    if (opts->window > 0) return fail(AWQ_ERR_UNSUPPORTED, "%s: a shared prefix takes no window", who);
+    if (opts->prefix_len > (int64_t)opts->prefix_blocks * cache->page_size)
+      return fail(AWQ_ERR_INVALID_ARG, "%s: prefix_len=%d is beyond the prefix_blocks=%d pages of %d tokens", who,
+                  opts->prefix_len, opts->prefix_blocks, cache->page_size);
+    if (opts->prefix_len > kMaxContext) return fail(AWQ_ERR_UNSUPPORTED, "%s: prefix_len=%d exceeds 2^30", who, opts->prefix_len);
+    // (the rows of all requests are counted as one's)
+    if (num_tokens * (num_heads / cache->num_kv_heads) > ((int64_t)1 << 30))
+      return fail(AWQ_ERR_UNSUPPORTED, "%s: a shared prefix takes at most 2^30 query tokens times the query heads per key/value head", who);
+  }
   return AWQ_OK;
+}
+
+// The plan of a call: of one over all keys, or of one over a shared prefix and the rest.
+struct AttentionPlan {
+  bool prefix;
+  KvAttnPlan whole;
+  KvPrefixPlan split;
+  size_t bytes() const { return prefix ? split.workspace_bytes : whole.workspace_bytes; }
+};
+AttentionPlan plan_of(int64_t num_tokens, int32_t num_seqs, int heads, int group, int D, int32_t max_query_len,
+                      int64_t max_seq_len, const awq_kv_attention_options &o) {
+  AttentionPlan p{};
+  p.prefix = o.prefix_len > 0;
+  if (p.prefix) p.split = kv_prefix_plan(num_tokens, num_seqs, heads, group, D, max_query_len, max_seq_len, o.prefix_len);
+  else p.whole = kv_attention_plan(num_tokens, num_seqs, heads, group, D, max_query_len, max_seq_len, o.window, o.sinks);
+  return p;
+}
+
+size_t attention_workspace(const char *who, int64_t num_tokens, int32_t num_seqs, int32_t num_heads,
+                           const awq_kv_cache *cache, awq_config cfg, int32_t max_query_len, int64_t max_seq_len,
+                           const awq_kv_attention_options *opts) {
+  if (check_attention_sizes(who, num_tokens, num_seqs, num_heads, cache, cfg, max_query_len, max_seq_len, opts, false) !=
+      AWQ_OK)
+    return 0;
+  if (num_tokens == 0 || num_seqs == 0 || max_query_len == 0) return 0;
+  if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
+  return plan_of(num_tokens, num_seqs, cache->num_kv_heads, num_heads / cache->num_kv_heads, cache->head_dim,
+                 max_query_len, max_seq_len, *opts)
+      .bytes();
+}
+
+awq_status attend(const char *who, const void *Q, int32_t q_dtype, int64_t num_tokens, int64_t q_stride,
+                  int32_t num_heads, const awq_kv_cache *cache, awq_config cfg, const int32_t *block_table,
+                  int32_t max_blocks, const int32_t *seq_lens, const int32_t *query_start, int32_t num_seqs,
+                  int32_t max_query_len, int64_t max_seq_len, float scale, const awq_kv_attention_options *opts,
+                  void *O, float *lse, void *workspace, size_t workspace_bytes, awq_stream_t stream) {
+  const bool work = num_tokens > 0 && num_seqs > 0 && max_query_len > 0;
+  awq_status st = check_attention_sizes(who, num_tokens, num_seqs, num_heads, cache, cfg, max_query_len,
+                                        max_seq_len, opts, work);
+  if (st != AWQ_OK) return st;
+  const awq_kv_attention_options &o = *opts;
+  if (q_dtype != AWQ_F16 && q_dtype != AWQ_BF16)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: q_dtype=%d: must be AWQ_F16 or AWQ_BF16", who, q_dtype);
+  if (q_stride < (int64_t)num_heads * cache->head_dim || q_stride % 8 != 0)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: q_stride=%lld must be a multiple of 8 of at least num_heads * head_dim",
+                who, (long long)q_stride);
+  if (too_far(num_tokens, q_stride)) return fail(AWQ_ERR_INVALID_ARG, "%s: q_stride reaches beyond 2^60 elements", who);
+  if (o.causal != 0 && o.causal != 1) return fail(AWQ_ERR_INVALID_ARG, "%s: causal=%d: must be 0 or 1", who, o.causal);
+  if (o.window > 0 && !o.causal) return fail(AWQ_ERR_INVALID_ARG, "%s: a window needs causal = 1", who);
+  if (!std::isfinite(scale)) return fail(AWQ_ERR_INVALID_ARG, "%s: scale is not finite", who);
+  if (max_blocks < 0 || (int64_t)max_blocks * cache->page_size > kMaxContext)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: max_blocks=%d: negative, or beyond 2^30 tokens", who, max_blocks);
+  if (!query_start && (num_tokens != num_seqs || max_query_len > 1))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: without query_start every request has one query token", who);
+  if (workspace && !aligned(workspace, kAlign))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", who);
+  if (!work) return ok();
+  if (!Q || !O || !seq_lens || (max_blocks > 0 && !block_table))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
+  if (o.prefix_len > 0 && !o.prefix_table)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
+  if (!aligned(Q, 16) || !aligned(O, 16)) return fail(AWQ_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", who);
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(lse, 4) ||
+      !aligned(o.prefix_table, 4))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: block_table, seq_lens, query_start, prefix_table and lse must be 4-byte aligned", who);
+  const size_t o_bytes = (size_t)num_tokens * num_heads * cache->head_dim * 2;
+  const size_t lse_bytes = lse ? (size_t)num_tokens * num_heads * 4 : 0;
+  // (no request has more query tokens than there are; the same in ..._workspace_size)
+  if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
+  const int group = num_heads / cache->num_kv_heads;
+  const AttentionPlan plan = plan_of(num_tokens, num_seqs, cache->num_kv_heads, group, cache->head_dim, max_query_len,
+                                     max_seq_len, o);
+  const size_t need = plan.bytes();
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(AWQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed (%s_workspace_size)", who,
+                workspace ? workspace_bytes : 0, need, who);
+  const CacheSpans cs = cache_spans(kv_cache(cache, cfg));
+  const Span out[] = {{O, o_bytes}, {lse, lse_bytes}, {workspace, need}},
+             in[] = {{Q, strided_bytes(num_tokens, q_stride, (int64_t)num_heads * cache->head_dim, 2)},
+                     cs.codes, cs.scales, cs.zeros, {block_table, (size_t)num_seqs * max_blocks * 4},
+                     {seq_lens, (size_t)num_seqs * 4}, {query_start, query_start ? ((size_t)num_seqs + 1) * 4 : 0},
+                     {o.prefix_table, o.prefix_len > 0 ? (size_t)o.prefix_blocks * 4 : 0}};
+  if (!all_apart(out, in))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse or the workspace overlaps Q, the cache or the request arrays", who);
+  if (!apart(lse, lse_bytes, O, o_bytes) || !apart(workspace, need, O, o_bytes) ||
+      !apart(workspace, need, lse, lse_bytes))
+    return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse and the workspace may not overlap each other", who);
+  KvAttn p{};
+  p.Q = reinterpret_cast<const uint16_t *>(Q);
+  p.q_stride = q_stride;
+  p.O = O;
+  p.lse = lse;
+  p.codes = cache->codes;
+  p.scales = cache->scales;
+  p.zeros = cfg.zero_point ? cache->zeros : nullptr;
+  p.pages = cache->num_pages;
+  p.T = num_tokens;
+  p.pshift = __builtin_ctz((unsigned)cache->page_size);
+  p.heads = cache->num_kv_heads;
+  p.group = group;
+  p.by_heads = make_divisor(cache->num_kv_heads);
+  p.by_group = make_divisor(group);
+  p.table = block_table;
+  p.max_blocks = max_blocks;
+  p.seq_lens = seq_lens;
+  p.query_start = query_start;
+  p.max_q = max_query_len;
+  p.causal = o.causal;
+  p.window = o.window;
+  p.num_seqs = num_seqs;
+  p.sinks = o.window > 0 ? o.sinks : 0;
+  p.after = o.prefix_len;
+  p.prefix_table = o.prefix_table;
+  p.prefix_blocks = o.prefix_blocks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const XType xt = q_dtype == AWQ_BF16 ? XType::BF16 : XType::F16;
+  return hip_status(o.prefix_len > 0
+                        ? launch_kv_attention_prefix(p, num_seqs, cache->head_dim, xt, plan.split, workspace, as_stream(stream))
+                        : launch_kv_attention(p, num_seqs, cache->head_dim, xt, plan.whole, workspace, as_stream(stream)),
+                    who);
 }
 
 }  // namespace
@@ -125,14 +260,9 @@ awq_status awq_kv_gather(const awq_kv_cache *cache, awq_config cfg, const int32_
 size_t awq_kv_attention_workspace_size(int64_t num_tokens, int32_t num_seqs, int32_t num_heads,
                                        const awq_kv_cache *cache, awq_config cfg,
                                        int32_t max_query_len, int64_t max_seq_len, int32_t window) {
-  if (check_attention_sizes("awq_kv_attention_workspace_size", num_tokens, num_seqs, num_heads, cache, cfg,
-                            max_query_len, max_seq_len, window, false) != AWQ_OK)
-    return 0;
-  if (num_tokens == 0 || num_seqs == 0 || max_query_len == 0) return 0;
-  if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
-  return kv_attention_plan(num_tokens, num_seqs, cache->num_kv_heads, num_heads / cache->num_kv_heads,
-                           cache->head_dim, max_query_len, max_seq_len, window)
-      .workspace_bytes;
+  const awq_kv_attention_options o{1, window, 0, 0, nullptr, 0};
+  return attention_workspace("awq_kv_attention_workspace_size", num_tokens, num_seqs, num_heads, cache, cfg,
+                             max_query_len, max_seq_len, &o);
 }
 
 awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, int64_t q_stride,
@@ -141,79 +271,28 @@ awq_status awq_kv_attention(const void *Q, int32_t q_dtype, int64_t num_tokens, 
                             const int32_t *query_start, int32_t num_seqs, int32_t max_query_len,
                             int64_t max_seq_len, float scale, int32_t causal, int32_t window, void *O,
                             float *lse, void *workspace, size_t workspace_bytes, awq_stream_t stream) {
-  const char *who = "awq_kv_attention";
-  const bool work = num_tokens > 0 && num_seqs > 0 && max_query_len > 0;
-  awq_status st = check_attention_sizes(who, num_tokens, num_seqs, num_heads, cache, cfg, max_query_len,
-                                        max_seq_len, window, work);
-  if (st != AWQ_OK) return st;
-  if (q_dtype != AWQ_F16 && q_dtype != AWQ_BF16)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: q_dtype=%d: must be AWQ_F16 or AWQ_BF16", who, q_dtype);
-  if (q_stride < (int64_t)num_heads * cache->head_dim || q_stride % 8 != 0)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: q_stride=%lld must be a multiple of 8 of at least num_heads * head_dim",
-                who, (long long)q_stride);
-  if (too_far(num_tokens, q_stride)) return fail(AWQ_ERR_INVALID_ARG, "%s: q_stride reaches beyond 2^60 elements", who);
-  if (causal != 0 && causal != 1) return fail(AWQ_ERR_INVALID_ARG, "%s: causal=%d: must be 0 or 1", who, causal);
-  if (window > 0 && !causal) return fail(AWQ_ERR_INVALID_ARG, "%s: a window needs causal = 1", who);
-  if (!std::isfinite(scale)) return fail(AWQ_ERR_INVALID_ARG, "%s: scale is not finite", who);
-  if (max_blocks < 0 || (int64_t)max_blocks * cache->page_size > kMaxContext)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: max_blocks=%d: negative, or beyond 2^30 tokens", who, max_blocks);
-  if (!query_start && (num_tokens != num_seqs || max_query_len > 1))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: without query_start every request has one query token", who);
-  if (workspace && !aligned(workspace, kAlign))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", who);
-  if (!work) return ok();
-  if (!Q || !O || !seq_lens || (max_blocks > 0 && !block_table))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
-  if (!aligned(Q, 16) || !aligned(O, 16)) return fail(AWQ_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", who);
-  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(lse, 4))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: block_table, seq_lens, query_start and lse must be 4-byte aligned", who);
-  const size_t o_bytes = (size_t)num_tokens * num_heads * cache->head_dim * 2;
-  const size_t lse_bytes = lse ? (size_t)num_tokens * num_heads * 4 : 0;
-  // (no request has more query tokens than there are; the same in ..._workspace_size)
-  if (max_query_len > num_tokens) max_query_len = (int32_t)num_tokens;
-  const int group = num_heads / cache->num_kv_heads;
-  const KvAttnPlan plan = kv_attention_plan(num_tokens, num_seqs, cache->num_kv_heads, group, cache->head_dim,
-                                            max_query_len, max_seq_len, window);
-  if (plan.workspace_bytes > 0 && (!workspace || workspace_bytes < plan.workspace_bytes))
-    return fail(AWQ_ERR_WORKSPACE, "%s: workspace of %zu bytes, %zu needed (awq_kv_attention_workspace_size)", who,
-                workspace ? workspace_bytes : 0, plan.workspace_bytes);
-  const CacheSpans cs = cache_spans(kv_cache(cache, cfg));
-  const Span out[] = {{O, o_bytes}, {lse, lse_bytes}, {workspace, plan.workspace_bytes}},
-             in[] = {{Q, strided_bytes(num_tokens, q_stride, (int64_t)num_heads * cache->head_dim, 2)},
-                     cs.codes, cs.scales, cs.zeros, {block_table, (size_t)num_seqs * max_blocks * 4},
-                     {seq_lens, (size_t)num_seqs * 4}, {query_start, query_start ? ((size_t)num_seqs + 1) * 4 : 0}};
-  if (!all_apart(out, in))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse or the workspace overlaps Q, the cache or the request arrays", who);
-  if (!apart(lse, lse_bytes, O, o_bytes) || !apart(workspace, plan.workspace_bytes, O, o_bytes) ||
-      !apart(workspace, plan.workspace_bytes, lse, lse_bytes))
-    return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse and the workspace may not overlap each other", who);
-  KvAttn p{};
-  p.Q = reinterpret_cast<const uint16_t *>(Q);
-  p.q_stride = q_stride;
-  p.O = O;
-  p.lse = lse;
-  p.codes = cache->codes;
-  p.scales = cache->scales;
-  p.zeros = cfg.zero_point ? cache->zeros : nullptr;
-  p.pages = cache->num_pages;
-  p.T = num_tokens;
-  p.pshift = __builtin_ctz((unsigned)cache->page_size);
-  p.heads = cache->num_kv_heads;
-  p.group = group;
-  p.by_heads = make_divisor(cache->num_kv_heads);
-  p.by_group = make_divisor(group);
-  p.table = block_table;
-  p.max_blocks = max_blocks;
-  p.seq_lens = seq_lens;
-  p.query_start = query_start;
-  p.max_q = max_query_len;
-  p.causal = causal;
-  p.window = window;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  return hip_status(launch_kv_attention(p, num_seqs, cache->head_dim,
-                                        q_dtype == AWQ_BF16 ? XType::BF16 : XType::F16, plan, workspace,
-                                        as_stream(stream)),
-                    who);
+  const awq_kv_attention_options o{causal, window, 0, 0, nullptr, 0};
+  return attend("awq_kv_attention", Q, q_dtype, num_tokens, q_stride, num_heads, cache, cfg, block_table, max_blocks,
+                seq_lens, query_start, num_seqs, max_query_len, max_seq_len, scale, &o, O, lse, workspace,
+                workspace_bytes, stream);
+}
+
+size_t awq_kv_attention_ex_workspace_size(int64_t num_tokens, int32_t num_seqs, int32_t num_heads,
+                                          const awq_kv_cache *cache, awq_config cfg, int32_t max_query_len,
+                                          int64_t max_seq_len, const awq_kv_attention_options *opts) {
+  return attention_workspace("awq_kv_attention_ex_workspace_size", num_tokens, num_seqs, num_heads, cache, cfg,
+                             max_query_len, max_seq_len, opts);
+}
+
+awq_status awq_kv_attention_ex(const void *Q, int32_t q_dtype, int64_t num_tokens, int64_t q_stride, int32_t num_heads,
+                               const awq_kv_cache *cache, awq_config cfg, const int32_t *block_table,
+                               int32_t max_blocks, const int32_t *seq_lens, const int32_t *query_start,
+                               int32_t num_seqs, int32_t max_query_len, int64_t max_seq_len, float scale,
+                               const awq_kv_attention_options *opts, void *O, float *lse, void *workspace,
+                               size_t workspace_bytes, awq_stream_t stream) {
+  return attend("awq_kv_attention_ex", Q, q_dtype, num_tokens, q_stride, num_heads, cache, cfg, block_table, max_blocks,
+                seq_lens, query_start, num_seqs, max_query_len, max_seq_len, scale, opts, O, lse, workspace,
+                workspace_bytes, stream);
 }
 
 }  // extern "C"

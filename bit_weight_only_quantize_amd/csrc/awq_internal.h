@@ -295,6 +295,12 @@ struct KvAttn {
   float2 *part_sum;           // [splits][T * heads * group]: weights are relative to 2^x; y, their
                               // sum, is 0 where a part holds no key of the row
   float *part_lo;             // likewise, where |x| >= 2^24 only: a part of the reference below x
+  // calls with sinks, or a shared prefix
+  int num_seqs, sinks;        // the first `sinks` keys are seen beside the window's
+  int after;                  // tokens of the prefix, or 0
+  const int32_t *prefix_table;
+  int prefix_blocks;
+  int prefix_parts;           // parts that the prefix takes, before the others
 };
 // Kernel, its tile of rows, waves per workgroup and parts of the keys, and the
 // workspace of a call.
@@ -304,8 +310,21 @@ struct KvAttnPlan {
   size_t sum_offset, lo_offset, workspace_bytes;   // 0 when splits == 1
 };
 KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv,
-                             int window);
+                             int window, int sinks);
+// The same for a shared prefix' keys and for the rest; parts: of the prefix.
+struct KvPrefixPlan {
+  KvAttnPlan shared, rest;
+  int parts;
+  size_t sum_offset, lo_offset, workspace_bytes;
+};
+KvPrefixPlan kv_prefix_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv, int prefix_len);
 hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPlan &plan,
                                void *workspace, hipStream_t st);
+hipError_t launch_kv_attention_prefix(KvAttn p, int B, int D, XType xt, const KvPrefixPlan &plan, void *workspace,
+                                      hipStream_t st);
+// kv_attention_some.hip, kv_attention_shared.hip: the kernels over some keys (and the join),
+// over a shared prefix'.
+hipError_t attn_launch_some(const KvAttn &p, int B, int D, XType xt, const KvAttnPlan &pl, hipStream_t st);
+hipError_t attn_launch_shared(const KvAttn &p, int D, XType xt, const KvAttnPlan &pl, hipStream_t st);
 
 }  // namespace awq

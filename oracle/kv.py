@@ -122,9 +122,9 @@ def assign(old, new, table, free, page, num_slots):
 
 
 def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_eps=2.0 ** -11,
-                weighted=False):
+                weighted=False, sinks=0):
     """(O, lse, bound, lse_bound) in fp64 for Q fp64 [T][num_heads][D]; rows of no
-    request NaN.
+    request NaN.  With `sinks` a row sees the first ones beside its window.
 
     `bound` (and lse_bound likewise) says how far a result of the documented arithmetic may be from O:
       the output's rounding                       out_eps |o|
@@ -161,7 +161,7 @@ def attention64(Q, cache, table, lens, start, scale, causal=True, window=0, out_
             last = kv - (q1 - q0) + i if causal else kv - 1
             seen = held & (pos <= last)
             if window:
-                seen &= pos > last - window
+                seen &= (pos > last - window) | (pos < sinks)
             at = np.flatnonzero(seen)
             for j in range(heads):
                 h = j // group
