@@ -854,6 +854,10 @@ void kv_decode_kernel(KvAttn p) {
 // heads over 4, D = 64: 31.5 us, where one group took 37 (a set of shorter lengths:
 // 25.8 and 39.8).
 //
+// With KH = 1 (a shared prefix, up to 64 rows) a workgroup has 64 rows, two waves of it half of
+// each tile's keys and two the other, joined likewise: in a tile of 128 rows half the waves would have
+// none, and the others all the softmax (32768 tokens, 64 rows of 32 heads: 116 us a call, 109 so).
+//
 // Slower on the long prompt: eight waves and 256 rows (993 us when this took 834),
 // a pipeline of half tiles (1376), the running maximum from a bound in LDS (1115),
 // 64 rows per wave at one wave per SIMD (the accumulators travel between register
@@ -873,9 +877,10 @@ struct PromptSmem {
   float vs[2][kPtKeys];          // value step; 0 past the last token, -0 where a page is missing
 };
 
-template <int D, bool SYM, bool BF16, int NG, int KEYS>
+template <int D, bool SYM, bool BF16, int NG, int KEYS, int KH = 2>
 __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv_prompt_kernel(KvAttn p) {
-  constexpr int kRows = kPtRows;
+  constexpr int kRows = 64 * KH;
+  static_assert(KH == 2 || NG == 1);
   using Smem = PromptSmem<D>;
   constexpr int kSteps = D / 16, kTiles = D / 32;
   __shared__ __attribute__((aligned(16))) Smem sms[NG];
@@ -884,32 +889,22 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   const int grp = NG == 1 ? 0 : __builtin_amdgcn_readfirstlane(tid >> 8);
   Smem &sm = sms[grp];
   const int qc = lane & 31, hh = lane >> 5;
+  const int rw = KH == 2 ? wave : wave & 1, half = KH == 2 ? 0 : wave >> 1;   // the wave's rows, and half of the keys
   const int tile = (int)gridDim.x - 1 - (int)blockIdx.x;     // longest rows first
   const int split = divide(blockIdx.y, p.by_heads), h = (int)blockIdx.y - split * p.heads, b = blockIdx.z;
   const Request rq = rows_of<KEYS>(p, b);
   const int rows = rq.ql * p.group, row0 = tile * kRows;
   if (row0 >= rows) return;
   auto clamp_row = [&](int r) { return r < rows ? r : rows - 1; };
-  const int wrow0 = clamp_row(row0 + wave * 32), wrow1 = clamp_row(row0 + wave * 32 + 31);
-  const int row = clamp_row(row0 + wave * 32 + qc);
-  const bool wave_live = row0 + wave * 32 < rows;
+  const int wrow0 = clamp_row(row0 + rw * 32), wrow1 = clamp_row(row0 + rw * 32 + 31);
+  const int row = clamp_row(row0 + rw * 32 + qc);
+  const bool wave_live = row0 + rw * 32 < rows;
   const int qi = token_of(p, row);
-  const int my_last = row_last<KEYS>(p, rq, qi), my_first = row_first<KEYS>(p, my_last);
-  int w_any_last, w_all_last;
-  if constexpr (KEYS == kShared) {
-    w_any_last = w_all_last = my_last;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int x = __shfl_xor(w_any_last, d, 64), y = __shfl_xor(w_all_last, d, 64);
-      w_any_last = x > w_any_last ? x : w_any_last;
-      w_all_last = y < w_all_last ? y : w_all_last;
-    }
-    w_any_last = __builtin_amdgcn_readfirstlane(w_any_last);
-    w_all_last = __builtin_amdgcn_readfirstlane(w_all_last);
-  } else {
-    w_any_last = last_key(p, rq, token_of(p, wrow1));
-    w_all_last = last_key(p, rq, token_of(p, wrow0));
-  }
+  // (kShared: looked up once the first tile's loads are under way)
+  int my_last = KEYS == kShared ? 0 : row_last<KEYS>(p, rq, qi);
+  const int my_first = row_first<KEYS>(p, my_last);
+  int w_any_last = KEYS == kShared ? 0 : last_key(p, rq, token_of(p, wrow1));
+  int w_all_last = KEYS == kShared ? 0 : last_key(p, rq, token_of(p, wrow0));
   const int w_any_first = row_first<KEYS>(p, w_all_last), w_all_first = row_first<KEYS>(p, w_any_last);
   const int my_sinks = KEYS != kSome ? 0 : p.sinks < my_last + 1 ? p.sinks : my_last + 1;
   const Keys keys = keys_of<KEYS>(p, rq, row0, clamp_row(row0 + kRows - 1), kPtKeys);
@@ -1078,11 +1073,11 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   // D = 128).
   constexpr int kMfma = 0x008, kValu = 0x002, kLdsRead = 0x100;
   auto compute = [&](int buf, int t0) {
-    const char *kl = sm.k[buf] + qc * Smem::kKeyRow + 16 * hh;
-    const char *vl = sm.v[buf] + qc * Smem::kValueRow + 16 * hh;
+    const char *kl = sm.k[buf] + (32 * half + qc) * Smem::kKeyRow + 16 * hh;
+    const char *vl = sm.v[buf] + qc * Smem::kValueRow + 64 * half + 16 * hh;
     // the four keys 32i + 8g + 4hh + e of result group g
     auto per_key = [&](const float *x, int i, int g) {
-      return *reinterpret_cast<const f32x4 *>(x + 32 * i + 8 * g + 4 * hh);
+      return *reinterpret_cast<const f32x4 *>(x + 32 * half + 32 * i + 8 * g + 4 * hh);
     };
     auto key_frag = [&](int i, int st) {
       return *reinterpret_cast<const u32x4 *>(kl + 32 * i * Smem::kKeyRow + 32 * st);
@@ -1091,27 +1086,16 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       return *reinterpret_cast<const u32x4 *>(vl + 32 * n * Smem::kValueRow + 32 * s);
     };
     const float vstep = sm.vs[buf][lane];                    // (of the tile's key `lane`)
-    f32x16 s[2];
+    f32x16 s[KH];
     u32x4 kf[kSteps];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < KH; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[i][e] = 0.0f;
 #pragma unroll
     for (int st = 0; st < kSteps; ++st) kf[st] = key_frag(0, st);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      s[0] = mfma32x16(kf[st], q[st], s[0]);
-      kf[st] = key_frag(1, st);
-    }
-#pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    float u[32];
+    float u[16 * KH];
     auto scaled = [&](int i) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -1120,20 +1104,35 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
         for (int e = 0; e < 4; ++e) u[16 * i + 4 * g + e] = s[i][4 * g + e] * a[e];
       }
     };
+    if constexpr (KH == 2) {
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st) s[1] = mfma32x16(kf[st], q[st], s[1]);
-    scaled(0);
-    __builtin_amdgcn_sched_group_barrier(kLdsRead, 4, 0);
+      for (int st = 0; st < kSteps; ++st) {
+        s[0] = mfma32x16(kf[st], q[st], s[0]);
+        kf[st] = key_frag(1, st);
+      }
 #pragma unroll
-    for (int st = 0; st < kSteps; ++st) {
-      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(kValu, 16 / kSteps, 0);
+      for (int st = 0; st < kSteps; ++st) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int st = 0; st < kSteps; ++st) s[KH - 1] = mfma32x16(kf[st], q[st], s[KH - 1]);
+    if constexpr (KH == 2) {
+      scaled(0);
+      __builtin_amdgcn_sched_group_barrier(kLdsRead, 4, 0);
+#pragma unroll
+      for (int st = 0; st < kSteps; ++st) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kValu, 16 / kSteps, 0);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
     u32x4 vf[2][kTiles];
 #pragma unroll
     for (int n = 0; n < kTiles; ++n) vf[0][n] = value_frag(0, n);
-    scaled(1);
+    scaled(KH - 1);
     const bool holes = __any(__builtin_bit_cast(uint32_t, vstep) == 0x80000000u);
     // (all rows see the sinks)
     const bool early = KEYS == kSome ? t0 < w_all_first && t0 + kPtKeys > p.sinks : t0 < w_all_first;
@@ -1141,18 +1140,18 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
     if (partial) {
       // key first <= at <= last, as one unsigned comparison of (at - first)
       const bool any = my_first <= my_last;
-      const uint32_t first = any ? my_first - t0 - 4 * hh : 0x40000000, span = any ? my_last - my_first : 0;
+      const uint32_t first = any ? my_first - t0 - 32 * half - 4 * hh : 0x40000000, span = any ? my_last - my_first : 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < 4 * KH; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           bool seen = 8 * j + e - first <= span;
-          if constexpr (KEYS == kSome) seen |= 8 * j + e < my_sinks - t0 - 4 * hh;
+          if constexpr (KEYS == kSome) seen |= 8 * j + e < my_sinks - t0 - 32 * half - 4 * hh;
           u[4 * j + e] = seen ? u[4 * j + e] : -__builtin_inff();
         }
       if (holes) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4 * KH; ++j) {
           const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -1164,7 +1163,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
     }
     float umax = u[0];
 #pragma unroll
-    for (int j = 1; j < 32; ++j) umax = fmaxf(umax, u[j]);
+    for (int j = 1; j < 16 * KH; ++j) umax = fmaxf(umax, u[j]);
     if (__any(umax > slack || vstep > vlim)) {
       // the least power of two (from kLeastStep on) that no step of the tile exceeds
       int ve = -14;
@@ -1177,7 +1176,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       if (__any(vstep > 0.0f && vstep < power_of_two(ve - kSpread))) {
         float best = kNone;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4 * KH; ++j) {
           const f32x4 v = per_key(sm.vs[buf], j >> 2, j & 3);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -1228,16 +1227,16 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
     u32x4 pb = weights(0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int st = 0; st < 4; ++st) {
+    for (int st = 0; st < 2 * KH; ++st) {
       u32x4 next = pb;
-      if (st < 3) {
+      if (st < 2 * KH - 1) {
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) vf[(st + 1) & 1][n] = value_frag(st + 1, n);
         next = weights(st + 1);
       }
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) o[n] = mfma32x16(vf[st & 1][n], pb, o[n]);
-      if (st < 3) {
+      if (st < 2 * KH - 1) {
         __builtin_amdgcn_sched_group_barrier(kLdsRead, kTiles + 2, 0);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
@@ -1259,6 +1258,20 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       load_page(real(t_first));
       load_codes(real(t_first));
       load_page(real(t_first + kStride));
+    }
+    if constexpr (KEYS == kShared) {
+      my_last = row_last<KEYS>(p, rq, qi);
+      w_any_last = w_all_last = my_last;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_xor(w_any_last, d, 64), y = __shfl_xor(w_all_last, d, 64);
+        w_any_last = x > w_any_last ? x : w_any_last;
+        w_all_last = y < w_all_last ? y : w_all_last;
+      }
+      w_any_last = __builtin_amdgcn_readfirstlane(w_any_last);
+      w_all_last = __builtin_amdgcn_readfirstlane(w_all_last);
+    }
+    if (grp < nt) {
       stage_keys(0);
       stage_values(0);
     }
@@ -1280,9 +1293,10 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       __syncthreads();
     }
   }
-  if constexpr (NG == 2) {                                   // the second group's sums through LDS to the first's waves
-    float *po = reinterpret_cast<float *>(sms) + wave * (16 * kTiles + 2) * 64 + lane;
-    if (grp == 1) {
+  if constexpr (NG == 2 || KH == 1) {                        // the second half's sums through LDS to the first's waves
+    const int other = KH == 1 ? half : grp;
+    float *po = reinterpret_cast<float *>(sms) + rw * (16 * kTiles + 2) * 64 + lane;
+    if (other == 1) {
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
 #pragma unroll
@@ -1291,7 +1305,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
       po[(16 * kTiles + 1) * 64] = l;
     }
     __syncthreads();
-    if (grp == 1) return;
+    if (other == 1) return;
     const float M1 = po[16 * kTiles * 64], m2 = fmaxf(M, M1);
     const float a0 = __builtin_amdgcn_exp2f(M - m2), a1 = __builtin_amdgcn_exp2f(M1 - m2);
     M = m2;
@@ -1305,7 +1319,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   // ---- store: lane (q, hh) holds LDS rows 32n + 8g + 4hh + e of row q, all
   // eight channels of D/16 of its words
   l += __shfl_xor(l, 32, 64);
-  if (row0 + wave * 32 + qc >= rows) return;
+  if (row0 + rw * 32 + qc >= rows) return;
   const bool none = l == 0.0f;
   const float inv = none ? 0.0f : 1.0f / l;
   const int64_t head_row = (rq.token0 + qi) * ((int64_t)p.heads * p.group) + h * p.group + row - qi * p.group;
@@ -1434,15 +1448,22 @@ template <int KEYS, int D, bool SYM, bool BF16>
 hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st) {
   const int64_t rows = KEYS == kShared ? p.T * p.group : (int64_t)p.max_q * p.group;
   if (pl.prompt) {
-    const dim3 grid((unsigned)((rows + kPtRows - 1) / kPtRows), (unsigned)(p.heads * p.splits), (unsigned)B);
-    if (pl.waves == 8) kv_prompt_kernel<D, SYM, BF16, 2, KEYS><<<grid, 2 * kPtThreads, 0, st>>>(p);
-    else kv_prompt_kernel<D, SYM, BF16, 1, KEYS><<<grid, kPtThreads, 0, st>>>(p);
+    const dim3 grid((unsigned)((rows + pl.tile_rows - 1) / pl.tile_rows), (unsigned)(p.heads * p.splits), (unsigned)B);
+    if constexpr (KEYS == kShared) {
+      if (pl.tile_rows == kPtRows) kv_prompt_kernel<D, SYM, BF16, 1, KEYS><<<grid, kPtThreads, 0, st>>>(p);
+      else kv_prompt_kernel<D, SYM, BF16, 1, KEYS, 1><<<grid, kPtThreads, 0, st>>>(p);
+    } else {
+      if (pl.waves == 8) kv_prompt_kernel<D, SYM, BF16, 2, KEYS><<<grid, 2 * kPtThreads, 0, st>>>(p);
+      else kv_prompt_kernel<D, SYM, BF16, 1, KEYS><<<grid, kPtThreads, 0, st>>>(p);
+    }
   } else {
     const dim3 grid((unsigned)((rows + 15) / 16 * p.heads), (unsigned)p.splits, (unsigned)B);
-    if constexpr (KEYS != kShared) {
+    if constexpr (KEYS == kShared) {
+      kv_decode_kernel<D, SYM, BF16, 4, KEYS><<<grid, 256, 0, st>>>(p);
+    } else {
       if (pl.waves == 8) kv_decode_kernel<D, SYM, BF16, 8, KEYS><<<grid, 512, 0, st>>>(p);
+      else kv_decode_kernel<D, SYM, BF16, 4, KEYS><<<grid, 256, 0, st>>>(p);
     }
-    if (KEYS == kShared || pl.waves != 8) kv_decode_kernel<D, SYM, BF16, 4, KEYS><<<grid, 256, 0, st>>>(p);
   }
   const hipError_t e = hipGetLastError();
   if constexpr (KEYS != kShared) {

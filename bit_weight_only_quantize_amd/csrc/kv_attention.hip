@@ -61,34 +61,40 @@ KvAttnPlan kv_attention_plan(int64_t T, int B, int heads, int group, int D, int 
   return pl;
 }
 
-// The prefix' keys for the T * group rows of all requests.
+// The prefix' keys for the T * group rows of all requests, and the requests' own.
 KvPrefixPlan kv_prefix_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv, int prefix_len) {
   KvPrefixPlan pl{};
   pl.rest = kv_attention_plan(T, B, heads, group, D, max_q, max_kv > prefix_len ? max_kv - prefix_len : 1, 0, 0);
-  const int64_t rows = T * group;
-  KvAttnPlan &sh = pl.shared;
-  sh.prompt = rows > 32;
-  sh.tile_rows = sh.prompt ? kPtRows : 16;
-  const int64_t wgs = heads * ((rows + sh.tile_rows - 1) / sh.tile_rows);
-  sh.waves = 4;
-  sh.chunk = 512;
-  int64_t splits = sh.prompt ? 512 / wgs : 1024 / wgs;
-  const int64_t most = ((int64_t)prefix_len + sh.chunk - 1) / sh.chunk;
-  splits = splits < most ? splits : most;
-  splits = splits < kMaxSplits / 2 ? splits : kMaxSplits / 2;
-  sh.splits = splits < 1 ? 1 : (int)splits;
   if (pl.rest.splits > kMaxSplits / 2) pl.rest.splits = kMaxSplits / 2;
+  const int64_t rows = T * group, n = prefix_len;
+  KvAttnPlan &sh = pl.shared;
+  // Up to 32 rows take the decode kernel (32768 tokens, 32 rows of 8 heads: 31.9 us a call, 39.2 as a
+  // prompt's), up to 64 the prompt kernel's tiles of 64 (64 rows of 32 heads: 109 us, 116 in a tile of
+  // 128; of 8 heads 42.6, 47.7).
+  sh.prompt = rows > 32;
+  sh.tile_rows = !sh.prompt ? 16 : rows <= kPtRows / 2 ? kPtRows / 2 : kPtRows;
+  sh.waves = 4;
+  const int64_t wgs = heads * ((rows + sh.tile_rows - 1) / sh.tile_rows);
+  // Two workgroups to a CU: with one, or four, 384 rows of 8 heads over 32768 tokens took 117 and 116 us a
+  // call for 102 (32 rows, by the decode kernel: four to a CU 34.3 us, two 31.9).  Parts of 256 keys, since every part's results are
+  // written and read again (4096 tokens, 256 rows of 8 heads of 64: 28.1 us, 31.7 with parts of 128), and
+  // of 128 where that leaves half the CUs without one (2000 tokens, 128 rows of 8 heads: 24.8 us, 26.7).
+  sh.chunk = wgs * ((n + 255) / 256) < 128 ? 128 : 256;
+  int64_t splits = 512 / wgs;
+  const int64_t most = (n + sh.chunk - 1) / sh.chunk;
+  splits = splits < most ? splits : most;
+  splits = splits < kMaxSplits - pl.rest.splits ? splits : kMaxSplits - pl.rest.splits;
+  sh.splits = splits < 1 ? 1 : (int)splits;
   pl.parts = 1;                                       // (as keys_of counts them)
   if (sh.splits > 1) {
-    const int n = prefix_len, by_chunk = (n - 1) / sh.chunk + 1;
-    const int want = by_chunk < sh.splits ? by_chunk : sh.splits;
-    const int each = ((n - 1) / want + 64) & -64;
-    pl.parts = (n - 1) / each + 1;
+    const int64_t want = most < sh.splits ? most : sh.splits;
+    const int64_t each = ((n - 1) / want + 64) & -64;
+    pl.parts = (int)((n - 1) / each + 1);
   }
-  const int64_t n = T * heads * group, all = pl.parts + pl.rest.splits;
-  pl.sum_offset = (size_t)(all * n) * D * 4;
-  pl.lo_offset = pl.sum_offset + (size_t)(all * n) * 8;
-  pl.workspace_bytes = pl.lo_offset + (size_t)(all * n) * 4;
+  const int64_t results = (pl.parts + pl.rest.splits) * T * heads * group;
+  pl.sum_offset = (size_t)results * D * 4;
+  pl.lo_offset = pl.sum_offset + (size_t)results * 8;
+  pl.workspace_bytes = pl.lo_offset + (size_t)results * 4;
   return pl;
 }
 
