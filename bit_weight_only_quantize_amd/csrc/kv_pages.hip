@@ -25,32 +25,49 @@ __host__ __device__ __forceinline__ PageRuns page_runs(const KvCache &c) {
   const int64_t n = (int64_t)c.page_size * c.heads;
   return PageRuns{n * c.head_dim / 16, n / 4, c.zeros ? n / 8 : 0};
 }
+// Pieces of a page: of its codes, and of its steps and zero points together.
 __host__ __device__ __forceinline__ int64_t pieces_of(const PageRuns &r) {
-  return (r.codes + r.scales + r.zeros + kPieceUnits - 1) / kPieceUnits;
+  return (r.codes + kPieceUnits - 1) / kPieceUnits + (r.scales + r.zeros + kPieceUnits - 1) / kPieceUnits;
 }
 
 // Piece `piece` of page `from` to page `to`, by a workgroup: four loads in flight per lane.
+// (Codes have a path of their own, whose addresses are the same for all lanes but for the
+// lane's place: with one path for all three runs, each lane telling which, 2000 pages of 69 KB
+// took 63 us.)
 __device__ __forceinline__ void copy_piece(const KvCache &c, const PageRuns &r, int64_t from, int64_t to, int64_t piece) {
   constexpr int kPer = kPieceUnits / kPageThreads;
   u32x4 v[kPer];
-  int64_t src[kPer], dst[kPer];                      // addresses; 0: nothing
+  const int64_t code_pieces = (r.codes + kPieceUnits - 1) / kPieceUnits;
+  if (piece < code_pieces) {
+    const u32x4 *src = reinterpret_cast<const u32x4 *>(c.codes) + from * r.codes + piece * kPieceUnits;
+    u32x4 *dst = reinterpret_cast<u32x4 *>(c.codes) + to * r.codes + piece * kPieceUnits;
+    const int64_t left = r.codes - piece * kPieceUnits;
+    const int n = (int)(left < kPieceUnits ? left : kPieceUnits);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i * kPageThreads + (int)threadIdx.x < n) v[i] = src[i * kPageThreads + threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i * kPageThreads + (int)threadIdx.x < n) dst[i * kPageThreads + threadIdx.x] = v[i];
+    return;
+  }
+  const u32x4 *scales = reinterpret_cast<const u32x4 *>(c.scales) + from * r.scales;
+  const u32x4 *zeros = reinterpret_cast<const u32x4 *>(c.zeros) + from * r.zeros;
+  u32x4 *scales_to = reinterpret_cast<u32x4 *>(c.scales) + to * r.scales;
+  u32x4 *zeros_to = reinterpret_cast<u32x4 *>(c.zeros) + to * r.zeros;
+  const int64_t first = (piece - code_pieces) * kPieceUnits + threadIdx.x;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int64_t u = piece * kPieceUnits + i * kPageThreads + threadIdx.x;
-    const bool in_codes = u < r.codes, in_scales = u < r.codes + r.scales;
-    const void *base = in_codes ? (const void *)c.codes : in_scales ? (const void *)c.scales : (const void *)c.zeros;
-    const int64_t run = in_codes ? r.codes : in_scales ? r.scales : r.zeros;
-    const int64_t at = in_codes ? u : in_scales ? u - r.codes : u - r.codes - r.scales;
-    const bool in = u < r.codes + r.scales + r.zeros;
-    src[i] = in ? reinterpret_cast<int64_t>(base) + (from * run + at) * 16 : 0;
-    dst[i] = reinterpret_cast<int64_t>(base) + (to * run + at) * 16;
+    const int64_t u = first + i * kPageThreads;
+    if (u < r.scales) v[i] = scales[u];
+    else if (u < r.scales + r.zeros) v[i] = zeros[u - r.scales];
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (src[i]) v[i] = *reinterpret_cast<const u32x4 *>(src[i]);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i)
-    if (src[i]) *reinterpret_cast<u32x4 *>(dst[i]) = v[i];
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t u = first + i * kPageThreads;
+    if (u < r.scales) scales_to[u] = v[i];
+    else if (u < r.scales + r.zeros) zeros_to[u - r.scales] = v[i];
+  }
 }
 
 __device__ __forceinline__ bool is_page(int64_t id, int64_t pages) { return id >= 0 && id < pages; }
@@ -100,9 +117,24 @@ __device__ __forceinline__ ForkPage fork_page(const ForkArgs &a, int i) {
 __global__ __launch_bounds__(kPageThreads) void kv_fork_kernel(ForkArgs a, KvCache c) {
   __shared__ int64_t s_count[kPageThreads / 64];
   const int i = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
-  const int64_t taken = a.taken && *a.taken > 0 ? *a.taken : 0;
-  // forks before i that take a page (the last workgroup: all of them, for pages_used)
+  const int parent = a.parents[i], child = a.children[i];
+  const bool valid = is_page(parent, a.num_seqs) && is_page(child, a.num_seqs) && parent != child;
+  const int64_t cap = (int64_t)a.max_blocks << a.pshift;
+  int64_t len = a.lens[i];
+  len = !valid || len < 0 ? 0 : len < cap ? len : cap;
+  const int64_t full = len >> a.pshift;
+  const bool partial = (len & (((int64_t)1 << a.pshift) - 1)) != 0;
+  const int32_t *from = a.table + (int64_t)parent * a.max_blocks;
+  int32_t *to = a.table + (int64_t)child * a.max_blocks;
+  for (int64_t j = (int64_t)part * kPageThreads + threadIdx.x; j < full; j += (int64_t)parts * kPageThreads) {
+    const int32_t id = from[j];
+    to[j] = id;
+    if (is_page(id, a.pages)) atomicAdd(a.shared + id, 1);
+  }
   const bool reports = i == a.n - 1 && part == 0;
+  if (!partial && !reports) return;
+  // forks before this one that take a page
+  const int64_t taken = a.taken && *a.taken > 0 ? *a.taken : 0;
   int64_t before = 0;
   for (int64_t j = threadIdx.x; j < i; j += kPageThreads) before += fork_page(a, (int)j).takes;
 #pragma unroll
@@ -117,20 +149,7 @@ __global__ __launch_bounds__(kPageThreads) void kv_fork_kernel(ForkArgs a, KvCac
     const int64_t all = taken + before + mine.takes;
     *a.pages_used = all > 0x7FFFFFFF ? 0x7FFFFFFF : (int32_t)all;
   }
-  const int parent = a.parents[i], child = a.children[i];
-  if (!is_page(parent, a.num_seqs) || !is_page(child, a.num_seqs) || parent == child) return;
-  const int64_t cap = (int64_t)a.max_blocks << a.pshift;
-  int64_t len = a.lens[i];
-  len = len < 0 ? 0 : len < cap ? len : cap;
-  const int64_t full = len >> a.pshift;
-  const int32_t *from = a.table + (int64_t)parent * a.max_blocks;
-  int32_t *to = a.table + (int64_t)child * a.max_blocks;
-  for (int64_t j = (int64_t)part * kPageThreads + threadIdx.x; j < full; j += (int64_t)parts * kPageThreads) {
-    const int32_t id = from[j];
-    to[j] = id;
-    if (is_page(id, a.pages)) atomicAdd(a.shared + id, 1);
-  }
-  if ((len & (((int64_t)1 << a.pshift) - 1)) == 0) return;
+  if (!partial) return;
   int64_t fresh = -1;
   if (mine.takes && taken + before < a.num_free) fresh = a.free_pages[taken + before];
   if (!is_page(fresh, a.pages)) fresh = -1;
@@ -146,43 +165,54 @@ __global__ void kv_fork_none_kernel(const int32_t *taken, int32_t *pages_used) {
 }
 
 // ---- ranks ---------------------------------------------------------------------------
-// A workgroup ranks the flagged ones of 32 items per thread, item r * THREADS + thread in
-// round r so that loads are coalesced: each wave's ballots are counted in LDS, and one
-// scan of the 32 * waves counts gives every ballot's first rank.
-constexpr int kRounds = 32;
-constexpr int kChunk = kRounds * kPageThreads;         // items of a workgroup of many
+// A workgroup ranks the flagged ones of its items, item r * THREADS + thread in round r so that
+// loads are coalesced: each wave's ballots are counted in LDS, and one scan of the counts
+// gives every ballot's first rank.
+constexpr int kChunkRounds = 4;
+constexpr int kChunk = kChunkRounds * kPageThreads;    // items of a workgroup of many
 constexpr int kAlone = 1024;                           // threads of a single workgroup
-constexpr int64_t kAloneItems = (int64_t)kRounds * kAlone;
+constexpr int kAloneRounds = 32;
+constexpr int64_t kAloneItems = (int64_t)kAloneRounds * kAlone;
+constexpr int64_t kAloneEntries = 65536;               // table entries that one workgroup looks through
 
 template <int THREADS>
 struct Ranks {
-  static constexpr int kWaves = THREADS / 64, kCounts = kRounds * kWaves;
+  static constexpr int kWaves = THREADS / 64, kRounds = THREADS == kAlone ? kAloneRounds : kChunkRounds;
+  static constexpr int kCounts = kRounds * kWaves;
   struct Shared {
     int32_t first[kCounts];
     int32_t total;
   };
   Shared &s;
+  int rounds;                                          // that hold items
   uint32_t mask = 0;                                   // bit r: the thread's item of round r
-  __device__ __forceinline__ explicit Ranks(Shared &sh) : s(sh) {}
+  __device__ __forceinline__ Ranks(Shared &sh, int64_t items)
+      : s(sh), rounds(items >= (int64_t)kRounds * THREADS ? kRounds : items > 0 ? (int)((items + THREADS - 1) / THREADS) : 0) {}
   // All threads call it; returns the number of flagged items.
   template <class F>
   __device__ __forceinline__ int32_t count(F flag) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll 8
-    for (int r = 0; r < kRounds; ++r) {
-      const bool f = flag(r * THREADS + (int)threadIdx.x);
-      mask |= (uint32_t)f << r;
-      const uint64_t b = __ballot(f);
-      if (lane == 0) s.first[r * kWaves + wave] = __popcll(b);
+    // (rolled up: code that one workgroup runs once costs its fetching)
+#pragma unroll 1
+    for (int r = 0; r < kRounds; r += 4) {
+      bool f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = r < rounds && flag((r + i) * THREADS + (int)threadIdx.x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mask |= (uint32_t)f[i] << (r + i);
+        const uint64_t b = __ballot(f[i]);
+        if (lane == 0) s.first[(r + i) * kWaves + wave] = __popcll(b);
+      }
     }
     __syncthreads();
-    if (wave == 0) {                                   // exclusive scan, kCounts / 64 per lane
-      constexpr int kPer = kCounts / 64;
+    if (wave == 0) {                                   // exclusive scan, kPer per lane
+      constexpr int kPer = kCounts < 64 ? 1 : kCounts / 64;
       int32_t v[kPer], sum = 0;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         v[i] = sum;
-        sum += s.first[lane * kPer + i];
+        if (lane * kPer + i < kCounts) sum += s.first[lane * kPer + i];
       }
       int32_t up = sum;
 #pragma unroll
@@ -191,7 +221,8 @@ struct Ranks {
         if (lane >= d) up += x;
       }
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) s.first[lane * kPer + i] = up - sum + v[i];
+      for (int i = 0; i < kPer; ++i)
+        if (lane * kPer + i < kCounts) s.first[lane * kPer + i] = up - sum + v[i];
       if (lane == 63) s.total = up;
     }
     __syncthreads();
@@ -243,7 +274,7 @@ __device__ __forceinline__ Sums sum_counts(const int32_t *counts, int64_t n, int
 // they are few (one launch), else in chunks (two: counts, then places).  Few: a pool of
 // 7000 pages took ... in one workgroup.
 __global__ __launch_bounds__(kPageThreads) void kv_release_rows_kernel(ReleaseArgs a) {
-  const int64_t b = blockIdx.x;
+  const int64_t b = blockIdx.x, part = blockIdx.y, parts = gridDim.y;
   const int64_t cap = (int64_t)a.max_blocks << a.pshift;
   int64_t len = a.seq_lens[b];
   len = len < 0 ? 0 : len < cap ? len : cap;
@@ -253,7 +284,7 @@ __global__ __launch_bounds__(kPageThreads) void kv_release_rows_kernel(ReleaseAr
   const int64_t first = (lo + ((int64_t)1 << a.pshift) - 1) >> a.pshift;
   const int64_t stop = hi >= len ? blocks_of(len, a.pshift, a.max_blocks) : hi > 0 ? hi >> a.pshift : 0;
   int32_t *row = a.table + b * a.max_blocks;
-  for (int64_t j = first + threadIdx.x; j < stop; j += kPageThreads) {
+  for (int64_t j = first + part * kPageThreads + threadIdx.x; j < stop; j += parts * kPageThreads) {
     const int32_t id = row[j];
     row[j] = -1;
     if (is_page(id, a.pages)) atomicSub(a.shared + id, 1);
@@ -278,9 +309,9 @@ __device__ __forceinline__ int64_t taken_of(const ReleaseArgs &a) { return a.tak
 
 __global__ __launch_bounds__(kPageThreads) void kv_release_count_kernel(ReleaseArgs a, int32_t *counts) {
   __shared__ Ranks<kPageThreads>::Shared s;
-  Ranks<kPageThreads> ranks(s);
   const ReleaseItems items{a, taken_of(a)};
   const int64_t base = (int64_t)blockIdx.x * kChunk;
+  Ranks<kPageThreads> ranks(s, a.num_free + a.pages - base);
   const int32_t n = ranks.count([&](int i) { return items.flag(base + i); });
   if (threadIdx.x == 0) counts[blockIdx.x] = n;
 }
@@ -289,13 +320,14 @@ __global__ __launch_bounds__(kPageThreads) void kv_release_count_kernel(ReleaseA
 template <int THREADS>
 __global__ __launch_bounds__(THREADS) void kv_release_list_kernel(ReleaseArgs a, const int32_t *counts) {
   __shared__ typename Ranks<THREADS>::Shared s;
-  Ranks<THREADS> ranks(s);
   const ReleaseItems items{a, taken_of(a)};
-  const int64_t base = (int64_t)blockIdx.x * (kRounds * THREADS);
+  const int64_t base = (int64_t)blockIdx.x * (Ranks<THREADS>::kRounds * THREADS);
+  Ranks<THREADS> ranks(s, a.num_free + a.pages - base);
   const int32_t n = ranks.count([&](int i) { return items.flag(base + i); });
   Sums sums = {0, n};
   if constexpr (THREADS != kAlone) sums = sum_counts(counts, gridDim.x, blockIdx.x);
-  for (int r = 0; r < kRounds; ++r) {
+#pragma unroll 1
+  for (int r = 0; r < ranks.rounds; ++r) {
     bool f;
     const int64_t at = sums.before + ranks.rank(r, f);
     if (f) items.place(base + r * THREADS + threadIdx.x, at);
@@ -310,7 +342,8 @@ __global__ __launch_bounds__(THREADS) void kv_release_list_kernel(ReleaseArgs a,
 // the first: the k-th hole from the front, number p, has p - (used ones before it) = k, and
 // the k-th page from the back has n - 1 - (used ones before it) = k, so both lists are
 // written from one ranking of the used pages.  One workgroup marks and ranks a pool of up
-// to 32768 pages in LDS (one launch); a larger one takes four: clear, mark, count, list.
+// to 32768 pages and a table of up to 65536 entries in LDS (one launch); larger ones take
+// four: clear, mark, count, list.
 // The last launch copies the pages, moves their counts and renumbers the tables.
 __global__ __launch_bounds__(kPageThreads) void kv_compact_clear_kernel(uint8_t *used, int64_t pages) {
   for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < pages; i += (int64_t)gridDim.x * kPageThreads)
@@ -328,8 +361,8 @@ __global__ __launch_bounds__(kPageThreads) void kv_compact_mark_kernel(CompactAr
 
 __global__ __launch_bounds__(kPageThreads) void kv_compact_count_kernel(const uint8_t *used, int64_t pages, int32_t *counts) {
   __shared__ Ranks<kPageThreads>::Shared s;
-  Ranks<kPageThreads> ranks(s);
   const int64_t base = (int64_t)blockIdx.x * kChunk;
+  Ranks<kPageThreads> ranks(s, pages - base);
   const int32_t n = ranks.count([&](int i) { return base + i < pages && used[base + i] != 0; });
   if (threadIdx.x == 0) counts[blockIdx.x] = n;
 }
@@ -339,44 +372,60 @@ __global__ __launch_bounds__(THREADS) void kv_compact_list_kernel(CompactArgs a,
                                                                   const int32_t *counts) {
   __shared__ typename Ranks<THREADS>::Shared s;
   __shared__ uint32_t marks[THREADS == kAlone ? kAloneItems / 32 : 1];
-  Ranks<THREADS> ranks(s);
-  const int64_t base = (int64_t)blockIdx.x * (kRounds * THREADS);
+  const int64_t base = (int64_t)blockIdx.x * (Ranks<THREADS>::kRounds * THREADS);
+  Ranks<THREADS> ranks(s, pages - base);
   int32_t in_chunk;
   if constexpr (THREADS == kAlone) {
     marks[threadIdx.x] = 0;
     __syncthreads();
-    // a wave per row at a time
-    for (int64_t b = threadIdx.x >> 6; b < a.num_seqs; b += kAlone / 64) {
-      const int64_t n = blocks_of(a.seq_lens[b], a.pshift, a.max_blocks);
-      for (int64_t j = threadIdx.x & 63; j < n; j += 64) {
-        const int32_t id = a.table[b * a.max_blocks + j];
-        if (is_page(id, pages)) atomicOr(&marks[id >> 5], 1u << (id & 31));
+    // all entries, four to a thread in flight, and the lengths beside them
+    constexpr int kPer = 4;
+    // (One workgroup's instructions count here: row numbers by one multiplication, exact
+    // because entries times the divisor's error stay below 2^32, and 32 bits throughout.)
+    const int entries = a.num_seqs * a.max_blocks;      // (at most kAloneEntries)
+    const uint32_t inverse = a.max_blocks > 1 ? 0xFFFFFFFFu / (uint32_t)a.max_blocks + 1 : 0;
+#pragma unroll 1
+    for (int e0 = threadIdx.x; e0 < entries; e0 += kPer * kAlone) {
+      int32_t id[kPer];
+      bool live[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = e0 + i * kAlone < entries ? e0 + i * kAlone : e0;
+        const int b = a.max_blocks > 1 ? (int)__umulhi((uint32_t)e, inverse) : e;
+        const int len = a.seq_lens[b];
+        id[i] = a.table[e];
+        live[i] = len > 0 && e - b * a.max_blocks <= (len - 1) >> a.pshift;
       }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (live[i] && (uint32_t)id[i] < (uint32_t)pages) atomicOr(&marks[id[i] >> 5], 1u << (id[i] & 31));
     }
     __syncthreads();
-    in_chunk = ranks.count([&](int i) { return i < pages && ((marks[i >> 5] >> (i & 31)) & 1u); });
+    in_chunk = ranks.count([&](int i) { return i < (int)pages && ((marks[i >> 5] >> (i & 31)) & 1u); });
   } else {
     in_chunk = ranks.count([&](int i) { return base + i < pages && used[base + i] != 0; });
   }
   Sums sums = {0, in_chunk};
   if constexpr (THREADS != kAlone) sums = sum_counts(counts, gridDim.x, blockIdx.x);
-  const int64_t n = sums.all;
-  for (int r = 0; r < kRounds; ++r) {
+  // (numbers of pages fit 31 bits)
+  const int32_t n = (int32_t)sums.all, total = (int32_t)pages;
+#pragma unroll 1
+  for (int r = 0; r < ranks.rounds; ++r) {
     bool f;
-    const int64_t p = base + r * THREADS + threadIdx.x, before = sums.before + ranks.rank(r, f);
-    if (p >= pages) continue;
-    if (p < n && !f) a.holes[p - before] = (int32_t)p;
+    const int32_t p = (int32_t)base + r * THREADS + threadIdx.x, before = (int32_t)sums.before + ranks.rank(r, f);
+    if (p >= total) continue;
+    if (p < n && !f) a.holes[p - before] = p;
     if (p >= n && f) {
-      a.movers[n - 1 - before] = (int32_t)p;
-      a.place[p] = (int32_t)(n - 1 - before);
+      a.movers[n - 1 - before] = p;
+      a.place[p] = n - 1 - before;
     }
     if (p >= n && !f) a.shared[p] = 0;
-    if (p == n) *a.moves = (int32_t)(n - before);
-    a.free_out[p] = p + n < pages ? (int32_t)(p + n) : -1;
+    if (p == n) *a.moves = n - before;
+    a.free_out[p] = p < total - n ? p + n : -1;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *a.num_used = (int32_t)n;
-    if (n == pages) *a.moves = 0;
+    *a.num_used = n;
+    if (n == total) *a.moves = 0;
   }
 }
 
@@ -407,8 +456,14 @@ __global__ __launch_bounds__(kPageThreads) void kv_compact_move_kernel(CompactAr
 
 // ---- launch -----------------------------------------------------------------------------
 namespace {
-constexpr int64_t kCopyWgs = 4096;         // 16 workgroups per CU
+constexpr int64_t kCopyWgs = 1 << 20;      // of a copy: a workgroup for each piece, but for the largest
+constexpr int64_t kFillWgs = 4096;         // 16 workgroups per CU
 int64_t chunks_of(int64_t items) { return (items + kChunk - 1) / kChunk; }
+// Workgroups along a row of the table: one for 256 entries, while that fills the card.
+unsigned row_parts(int64_t rows, int64_t blocks) {
+  const int64_t parts = (blocks + kPageThreads - 1) / kPageThreads, most = (kFillWgs + rows - 1) / rows;
+  return (unsigned)(parts < most ? parts : most);
+}
 size_t region(int64_t bytes) { return ((size_t)bytes + 255) & ~(size_t)255; }
 }  // namespace
 
@@ -423,9 +478,10 @@ hipError_t launch_kv_fork(const ForkArgs &a, const KvCache &c, hipStream_t st) {
     kv_fork_none_kernel<<<1, 1, 0, st>>>(a.taken, a.pages_used);
     return hipGetLastError();
   }
-  // a part for each piece of the page, while that fills the card
-  int64_t parts = pieces_of(page_runs(c));
-  const int64_t most = (kCopyWgs + a.n - 1) / a.n;
+  // a part for each piece of the page and 256 entries of the row, while that fills the card
+  int64_t parts = pieces_of(page_runs(c)), rows = row_parts(a.n, a.max_blocks);
+  parts = parts > rows ? parts : rows;
+  const int64_t most = (kFillWgs + a.n - 1) / a.n;
   parts = parts < most ? parts : most;
   kv_fork_kernel<<<dim3((unsigned)a.n, (unsigned)parts), kPageThreads, 0, st>>>(a, c);
   return hipGetLastError();
@@ -438,7 +494,7 @@ size_t kv_release_workspace(int64_t pages, int64_t num_free) {
 
 hipError_t launch_kv_release(const ReleaseArgs &a, void *workspace, hipStream_t st) {
   if (a.num_seqs > 0 && a.max_blocks > 0) {
-    kv_release_rows_kernel<<<(unsigned)a.num_seqs, kPageThreads, 0, st>>>(a);
+    kv_release_rows_kernel<<<dim3((unsigned)a.num_seqs, row_parts(a.num_seqs, a.max_blocks)), kPageThreads, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -455,10 +511,9 @@ hipError_t launch_kv_release(const ReleaseArgs &a, void *workspace, hipStream_t 
   return hipGetLastError();
 }
 
-// Workspace: moves, holes, movers, places, and for a large pool the marks and the chunks' counts.
+// Workspace: moves, holes, movers, places, marks, the chunks' counts.
 size_t kv_compact_workspace(int64_t pages) {
-  const size_t lists = 256 + 3 * region(pages * 4);
-  return pages <= kAloneItems ? lists : lists + region(pages) + region(chunks_of(pages) * 4);
+  return 256 + 3 * region(pages * 4) + region(pages) + region(chunks_of(pages) * 4);
 }
 
 hipError_t launch_kv_compact(CompactArgs a, const KvCache &c, void *workspace, hipStream_t st) {
@@ -469,7 +524,7 @@ hipError_t launch_kv_compact(CompactArgs a, const KvCache &c, void *workspace, h
   a.movers = reinterpret_cast<int32_t *>(w + 256 + list);
   a.place = reinterpret_cast<int32_t *>(w + 256 + 2 * list);
   hipError_t e;
-  if (c.pages <= kAloneItems) {
+  if (c.pages <= kAloneItems && (int64_t)a.num_seqs * a.max_blocks <= kAloneEntries) {
     kv_compact_list_kernel<kAlone><<<1, kAlone, 0, st>>>(a, c.pages, nullptr, nullptr);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {

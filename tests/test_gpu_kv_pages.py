@@ -183,6 +183,20 @@ def test_compact(name, rows, most, page, spare, share, heads, D, zp):
     assert before[0].shape == cache[0].shape
 
 
+def test_compact_with_a_wide_table():
+    """A small pool, and more table entries than one workgroup looks through."""
+    import bit_weight_only_quantize_amd as awq
+    rng = np.random.default_rng(5)
+    lens = rng.integers(0, 200, 90)
+    table, shared, _ = _pool(rng, lens, 16, 300, 800, 0.2)
+    cache = kv.new_cache(len(shared), 1, 64, 16, True, rng)
+    got, tab, sh = _to_cache(cache), _i32(table), _i32(shared)
+    free, used = awq.awq_kv_compact(got, tab, _i32(lens), sh)
+    want, n = pg.compact(cache, table, lens, shared, 16)
+    _eq(tab, table), _eq(sh, shared), _eq(used, [n]), _eq(free, pg.padded(want, len(shared)))
+    _same_cache(got, cache)
+
+
 def test_compact_of_nothing():
     import bit_weight_only_quantize_amd as awq
     torch = torch_mod()
