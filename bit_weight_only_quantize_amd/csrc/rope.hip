@@ -10,10 +10,13 @@
 // products and the sum are fp32, each rounded once and not fused, so what they give
 // does not depend on the kernel, and the codes that a cache gets neither.
 //
-// A workgroup takes a run of tokens, computes their cosines and sines once, a
-// thread for each (LDS, 8 KiB at most), and keeps a lane's in registers while it
-// walks heads: a lane holds eight channels of a token.  Paired halves are R/16 lanes
-// apart and exchanged between lanes, so every channel is read once.
+// A workgroup takes four tokens, computes their cosines and sines, one or two to a thread
+// (LDS, 8 KiB at most), and walks heads.  A lane holds eight channels; paired halves are
+// R/16 lanes apart and exchanged between lanes, so every channel is read once.  Queries: a wave
+// per token, neighbouring heads side by side in its lanes, which is one run of memory.  Keys and
+// values on their way into the cache: the four tokens of a head side by side, because their
+// value words interleave.  Loads of the next heads are under way while some are turned,
+// and the first before the angles are.
 //
 // Bound by memory; few tokens by a launch's latency and the chain of fp64 operations
 // (about 30 per angle).
@@ -25,8 +28,9 @@
 
 namespace awq {
 
-constexpr int kRopeThreads = 256, kRopePairs = 1024;   // pairs of a workgroup's tokens, at most
-constexpr int kRopeAhead = 4;                          // heads whose loads are in flight together
+constexpr int kRopeThreads = 256, kRopeTokens = 4;
+constexpr int kRopePairs = kRopeTokens * kRopeMaxDim / 2;
+constexpr int kRopeAhead = 4;                          // loads of a lane that are in flight together
 
 // cos and sin of x, each times factor, rounded to fp32.  x = n pi/2 + r, |r| <= pi/4
 // (a little more for |x| past 2^31), then the Taylor series of r: the first terms left out
@@ -61,10 +65,10 @@ struct Turn {
   bool on;               // the channels are among the first R
 };
 
-// Cosines and sines of `tokens` tokens from t0 on into `table` [token][R/2].
-__device__ __forceinline__ void fill_turns(const RopeArgs &p, int64_t t0, int tokens, int64_t T, float2 *table) {
+// Cosines and sines of the workgroup's tokens, from t0 on, into `table` [token][R/2].
+__device__ __forceinline__ void fill_turns(const RopeArgs &p, int64_t t0, int64_t T, float2 *table) {
   const int half = p.rotary_dim / 2;
-  for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads) {
+  for (int i = threadIdx.x; i < kRopeTokens * half; i += kRopeThreads) {
     const int t = i / half, j = i - t * half;
     const int64_t at = t0 + t < T ? t0 + t : T - 1;
     float2 cs = cos_sin((double)p.positions[at] * p.inv_freq[j], p.factor);
@@ -116,61 +120,94 @@ __device__ __forceinline__ void turn8(const Turn &t, u32x4 raw, float (&v)[8]) {
   }
 }
 
+// Rounded to nearest even; bfloat16 pairs by one instruction.
 template <bool BF16>
 __device__ __forceinline__ u32x4 narrow8(const float (&v)[8]) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   u32x4 r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = BF16 ? float_to_bf16_bits(v[2 * i]) : float_to_half_bits(v[2 * i]);
-    const uint32_t hi = BF16 ? float_to_bf16_bits(v[2 * i + 1]) : float_to_half_bits(v[2 * i + 1]);
-    r[i] = lo | (hi << 16);
+    if constexpr (BF16) r[i] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * i], (__bf16)v[2 * i + 1]});
+    else r[i] = __builtin_bit_cast(uint32_t, f16x2{(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
   }
   return r;
 }
 
-// Heads begin .. end of the lane's token: from x (its channels of head 0) to y, D
-// channels a head.  x and y may be the same place: a wave has read a head's
-// channels before any of its lanes writes one.
-template <bool BF16, bool PAIRS>
-__device__ __forceinline__ void turn_heads(const Turn &t, const uint16_t *x, uint16_t *y, int D, int begin, int end,
-                                           bool active) {
-  for (int h = begin; h < end; h += kRopeAhead) {
-    u32x4 raw[kRopeAhead];
+// Which heads a lane turns of a token: first, first + step, ... before `end`.
+struct Heads {
+  int first, step, end;
+};
+// Heads of part blockIdx.y of gridDim.y, `side` of them side by side, the lane's the `mine`-th.
+__device__ __forceinline__ Heads heads_of(int heads, int side, int mine) {
+  const int part = blockIdx.y, parts = gridDim.y;
+  return Heads{(int)((int64_t)heads * part / parts) + mine, side, (int)((int64_t)heads * (part + 1) / parts)};
+}
+
+// A lane's channels of kRopeAhead of its heads, from x (its channels of head 0), D to a head.
+struct Loaded {
+  u32x4 raw[kRopeAhead];
+  __device__ __forceinline__ void load(const uint16_t *x, int D, const Heads &hs, int h, bool active) {
 #pragma unroll
     for (int i = 0; i < kRopeAhead; ++i) {
       raw[i] = u32x4{0u, 0u, 0u, 0u};
-      if (active && h + i < end) raw[i] = *reinterpret_cast<const u32x4 *>(x + (int64_t)(h + i) * D);
+      const int at = h + i * hs.step;
+      if (active && at < hs.end) raw[i] = *reinterpret_cast<const u32x4 *>(x + (int64_t)at * D);
     }
+  }
+};
+// Heads from x to y; `l` holds the first ones.  x and y may be the same place: a lane reads a
+// head's channels, its own and by exchange its partner's, before it writes them.
+// The wave's lanes run as many steps as any of them needs (hs.first - mine is the same in all).
+template <bool BF16, bool PAIRS>
+__device__ __forceinline__ void turn_heads(const Turn &t, const uint16_t *x, uint16_t *y, int D, const Heads &hs, int mine,
+                                           bool active, Loaded &l) {
+  for (int h = hs.first; h - mine < hs.end;) {
+    const int next = h + kRopeAhead * hs.step;
+    Loaded more;
+    more.load(x, D, hs, next, active);
 #pragma unroll
     for (int i = 0; i < kRopeAhead; ++i) {
       float v[8];
-      turn8<BF16, PAIRS>(t, raw[i], v);
-      if (active && h + i < end) *reinterpret_cast<u32x4 *>(y + (int64_t)(h + i) * D) = narrow8<BF16>(v);
+      turn8<BF16, PAIRS>(t, l.raw[i], v);
+      const int at = h + i * hs.step;
+      if (active && at < hs.end) *reinterpret_cast<u32x4 *>(y + (int64_t)at * D) = narrow8<BF16>(v);
     }
+    l = more;
+    h = next;
   }
 }
 
-// Heads of part `part` of `parts`.
-__device__ __forceinline__ int part_begin(int heads, int part, int parts) { return (int)((int64_t)heads * part / parts); }
+// How a wave's lanes lie over the heads of a token, D / 8 lanes each (D need not divide 512).
+struct HeadLanes {
+  int side, mine, w;     // heads side by side; the lane's; its channels are 8w on
+  bool used;
+  __device__ __forceinline__ HeadLanes(int D, int lane) {
+    const int lanes = D / 8;
+    side = 64 / lanes;
+    used = lane < side * lanes;
+    mine = used ? lane / lanes : 0;
+    w = used ? lane - mine * lanes : 0;
+  }
+};
 
 template <bool BF16, bool PAIRS>
 __global__ __launch_bounds__(kRopeThreads) void rope_kernel(RopeArgs p, RopeArray q, RopeArray k, int64_t T, int D) {
   __shared__ float2 table[kRopePairs];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  // a wave takes as many whole tokens as fit its lanes (D need not divide 512)
-  const int lanes = D / 8, per_wave = 64 / lanes;
-  const int mine = lane / lanes < per_wave ? lane / lanes : per_wave - 1;
-  const int token = wave * per_wave + mine, w = lane < per_wave * lanes ? lane - mine * lanes : 0;
-  const int64_t t0 = (int64_t)blockIdx.x * (4 * per_wave), t = t0 + token;
-  fill_turns(p, t0, 4 * per_wave, T, table);
+  const HeadLanes at(D, lane);
+  const int64_t t0 = (int64_t)blockIdx.x * kRopeTokens, t = t0 + wave;
+  const bool active = at.used && t < T;
+  const Heads qh = heads_of(q.heads, at.side, at.mine), kh = heads_of(k.heads, at.side, at.mine);
+  const uint16_t *qx = q.x + t * q.x_stride + at.w * 8, *kx = k.x + t * k.x_stride + at.w * 8;
+  Loaded lq, lk;
+  lq.load(qx, D, qh, qh.first, active);
+  fill_turns(p, t0, T, table);
   __syncthreads();
-  const Turn turn = turn_of<PAIRS>(p, table, token, w, lane);
-  const bool active = t < T && lane < per_wave * lanes;
-  const int part = blockIdx.y, parts = gridDim.y;
-  turn_heads<BF16, PAIRS>(turn, q.x + t * q.x_stride + w * 8, q.y + t * q.y_stride + w * 8, D,
-                          part_begin(q.heads, part, parts), part_begin(q.heads, part + 1, parts), active);
-  turn_heads<BF16, PAIRS>(turn, k.x + t * k.x_stride + w * 8, k.y + t * k.y_stride + w * 8, D,
-                          part_begin(k.heads, part, parts), part_begin(k.heads, part + 1, parts), active);
+  const Turn turn = turn_of<PAIRS>(p, table, wave, at.w, lane);
+  turn_heads<BF16, PAIRS>(turn, qx, q.y + t * q.y_stride + at.w * 8, D, qh, at.mine, active, lq);
+  if (k.heads == 0) return;
+  lk.load(kx, D, kh, kh.first, active);
+  turn_heads<BF16, PAIRS>(turn, kx, k.y + t * k.y_stride + at.w * 8, D, kh, at.mine, active, lk);
 }
 
 template <int D, bool SYM, bool BF16, bool PAIRS>
@@ -179,34 +216,50 @@ __global__ __launch_bounds__(kRopeThreads) void kv_append_rope_kernel(
     int64_t k_stride, int64_t v_stride, const int32_t *__restrict__ slots, int64_t num_slots, int pshift,
     uint32_t *__restrict__ codes, uint16_t *__restrict__ scales, uint8_t *__restrict__ zeros,
     int32_t *__restrict__ nonfinite) {
-  constexpr int kLanes = D / 8, kTokens = kRopeThreads / kLanes;
-  __shared__ float2 table[kRopePairs];
-  const int lane = threadIdx.x & 63;
-  const int token = threadIdx.x / kLanes, w = threadIdx.x % kLanes;
-  const int64_t t0 = (int64_t)blockIdx.x * kTokens, t = t0 + token;
+  constexpr int kLanes = D / 8, kSide = 64 / kLanes;
+  __shared__ float2 table[kRopeTokens * D / 2];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = lane % kLanes;
+  const int64_t t0 = (int64_t)blockIdx.x * kRopeTokens;
+  // queries: wave's token, kSide heads; keys and values: four tokens of 256 / (4 kLanes) heads
+  constexpr int kKvSide = kRopeThreads / (kRopeTokens * kLanes);
+  const int64_t tq = t0 + wave;
+  const int kv_token = (threadIdx.x / kLanes) % kRopeTokens, kv_mine = threadIdx.x / (kLanes * kRopeTokens);
+  const int64_t t = t0 + kv_token;
   const int32_t slot = t < T ? slots[t] : -1;
-  fill_turns(p, t0, kTokens, T, table);
-  __syncthreads();
-  const Turn turn = turn_of<PAIRS>(p, table, token, w, lane);
-  const int part = blockIdx.y, parts = gridDim.y;
-  if (q.heads > 0)
-    turn_heads<BF16, PAIRS>(turn, q.x + t * q.x_stride + w * 8, q.y + t * q.y_stride + w * 8, D,
-                            part_begin(q.heads, part, parts), part_begin(q.heads, part + 1, parts), t < T);
+  const Heads qh = heads_of(q.heads, kSide, lane / kLanes), kh = heads_of(heads, kKvSide, kv_mine);
+  const uint16_t *qx = q.x + tq * q.x_stride + w * 8;
+  Loaded l;
+  l.load(qx, D, qh, qh.first, tq < T);
   // lanes of a group share their token, so a group is active as a whole
   const bool active = slot >= 0 && slot < num_slots;
-  int bad = 0;
-  const int end = part_begin(heads, part + 1, parts);
-  for (int h = part_begin(heads, part, parts); h < end; ++h) {
-    u32x4 kr = {0u, 0u, 0u, 0u}, vr = kr;
-    if (active) {
-      kr = *reinterpret_cast<const u32x4 *>(K + t * k_stride + (int64_t)h * D + w * 8);
-      vr = *reinterpret_cast<const u32x4 *>(V + t * v_stride + (int64_t)h * D + w * 8);
+  const uint16_t *kx = K + t * k_stride + w * 8, *vx = V + t * v_stride + w * 8;
+  auto load_pair = [&](u32x4 &k, u32x4 &v, int h) {
+    k = v = u32x4{0u, 0u, 0u, 0u};
+    if (active && h < kh.end) {
+      k = *reinterpret_cast<const u32x4 *>(kx + (int64_t)h * D);
+      v = *reinterpret_cast<const u32x4 *>(vx + (int64_t)h * D);
     }
+  };
+  u32x4 kr, vr;
+  load_pair(kr, vr, kh.first);
+  fill_turns(p, t0, T, table);
+  __syncthreads();
+  if (q.heads > 0) {
+    const Turn turn = turn_of<PAIRS>(p, table, wave, w, lane);
+    turn_heads<BF16, PAIRS>(turn, qx, q.y + tq * q.y_stride + w * 8, D, qh, lane / kLanes, tq < T, l);
+  }
+  const Turn turn = turn_of<PAIRS>(p, table, kv_token, w, lane);
+  int bad = 0;
+  for (int h = kh.first; h - kv_mine < kh.end; h += kKvSide) {
+    u32x4 kn, vn;
+    load_pair(kn, vn, h + kKvSide);
     float k[8], v[8];
     turn8<BF16, PAIRS>(turn, kr, k);
     widen8<BF16>(vr, v);
+    kr = kn;
+    vr = vn;
     const QuantWord qk = quantize_word<kLanes, SYM>(k, bad), qv = quantize_word<kLanes, SYM>(v, bad);
-    if (!active) continue;
+    if (!active || h >= kh.end) continue;
     if (nonfinite != nullptr && w == 0) bad += (int)qk.overflow + (int)qv.overflow;
     const KvPlace at = kv_place<D>(slot, pshift, h, heads, w);
     codes[at.k_word] = qk.word;
@@ -227,11 +280,11 @@ __global__ __launch_bounds__(kRopeThreads) void kv_append_rope_kernel(
 
 namespace {
 // Workgroups along the tokens and along the heads: parts of the heads while there are
-// fewer than eight workgroups per CU, a head each at least.
-dim3 rope_grid(int64_t T, int tokens, int heads) {
-  const int64_t along = (T + tokens - 1) / tokens;
+// fewer than eight workgroups per CU, `side` heads each at least.
+dim3 rope_grid(int64_t T, int heads, int side) {
+  const int64_t along = (T + kRopeTokens - 1) / kRopeTokens, most = (heads + side - 1) / side;
   int64_t parts = (2048 + along - 1) / along;
-  parts = parts < heads ? parts : heads;
+  parts = parts < most ? parts : most;
   return dim3((unsigned)along, (unsigned)(parts < 1 ? 1 : parts));
 }
 
@@ -239,7 +292,7 @@ template <int D, bool SYM, bool BF16>
 hipError_t append_rope_go(const RopeArgs &p, const RopeArray &q, const uint16_t *K, const uint16_t *V, int64_t T,
                           int64_t ks, int64_t vs, const int32_t *slots, const KvCache &c, int32_t *nonfinite,
                           hipStream_t st) {
-  const dim3 grid = rope_grid(T, kRopeThreads / (D / 8), q.heads > c.heads ? q.heads : c.heads);
+  const dim3 grid = rope_grid(T, q.heads > c.heads ? q.heads : c.heads, 64 / (D / 8));
   const int sh = __builtin_ctz((unsigned)c.page_size);
   const int64_t ns = c.pages * c.page_size;
   if (p.pairs) kv_append_rope_kernel<D, SYM, BF16, true><<<grid, kRopeThreads, 0, st>>>(p, q, K, V, T, c.heads, ks, vs, slots, ns, sh, c.codes, c.scales, c.zeros, nonfinite);
@@ -250,7 +303,7 @@ hipError_t append_rope_go(const RopeArgs &p, const RopeArray &q, const uint16_t 
 
 hipError_t launch_rope(const RopeArgs &p, const RopeArray &q, const RopeArray &k, XType xt, int64_t T, int D,
                        hipStream_t st) {
-  const dim3 grid = rope_grid(T, 4 * (64 / (D / 8)), q.heads > k.heads ? q.heads : k.heads);
+  const dim3 grid = rope_grid(T, q.heads > k.heads ? q.heads : k.heads, 64 / (D / 8));
   const bool bf16 = xt == XType::BF16;
   if (bf16 && p.pairs) rope_kernel<true, true><<<grid, kRopeThreads, 0, st>>>(p, q, k, T, D);
   else if (bf16) rope_kernel<true, false><<<grid, kRopeThreads, 0, st>>>(p, q, k, T, D);
