@@ -1021,14 +1021,13 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     stride = _token_rows(Q, "Q", heads, D)
     more = sinks != 0 or prefix_len != 0
     if more:
+        at, entries = block_table, blocks            # (its first row)
         if prefix_table is not None:
             _tensor(prefix_table, "prefix_table", torch.int32)
             if prefix_table.dim() != 1:
                 raise ValueError("prefix_table must be 1-D")
-        elif prefix_len > 0 and B > 0:
-            prefix_table = block_table[0]
-        opts = awq_kv_attention_options(int(causal), window, sinks, prefix_len, _address(prefix_table),
-                                        blocks if prefix_table is None else prefix_table.shape[0])
+            at, entries = prefix_table, prefix_table.shape[0]
+        opts = awq_kv_attention_options(int(causal), window, sinks, prefix_len, _address(at), entries)
         need = 0 if workspace is None else lib.awq_kv_attention_ex_workspace_size(
             T, B, heads, c, cfg, max_query_len, max_seq_len, opts)
     else:
