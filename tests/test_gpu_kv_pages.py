@@ -273,3 +273,29 @@ def test_a_step_captured():
         k, _ = awq.awq_kv_gather(tuple(fresh[8:]), fresh[0][3, 0] * page + torch.arange(5, device=dev(), dtype=torch.int32))
         was, _ = awq.awq_kv_gather(cache0, _i32(table0[1, 0] * page + np.arange(5)))
         assert torch.equal(bits(k), bits(was))
+
+
+def test_pages_past_32_bit_byte_offsets():
+    """A cache of more than 4 GiB of codes: pages at its end are copied, forked from and drawn to the front."""
+    import bit_weight_only_quantize_amd as awq
+    torch = torch_mod()
+    H, D, page = 8, 128, 64
+    pages = 72 * 1024                                       # 4.5 GiB of codes
+    cache = awq.empty_kv_cache(pages, H, D, page, dev())
+    g = torch.Generator(device=dev()).manual_seed(3)
+    last = [pages - 1, pages - 2]
+    for c in cache:
+        c[:4].zero_()
+        for p in last:
+            c[p] = torch.randint(0, 100, c[p].shape, generator=g, device=dev()).to(c.dtype)
+    kept = [[c[p].clone() for c in cache] for p in last]
+    same = lambda p, want: all(torch.equal(c[p], w) for c, w in zip(cache, want))     # noqa: E731
+    awq.awq_kv_copy_pages(cache, _i32(last), _i32([1, pages - 3]))
+    assert same(1, kept[0]) and same(pages - 3, kept[1]) and same(pages - 1, kept[0])
+    table, shared = _i32([[pages - 1, pages - 2], [-1, -1]]), torch.zeros(pages, dtype=torch.int32, device=dev())
+    used = awq.awq_kv_fork(cache, table, _i32([0]), _i32([1]), _i32([page + 5]), shared, _i32([pages - 4]))
+    assert used.item() == 1 and table.tolist()[1] == [pages - 1, pages - 4] and same(pages - 4, kept[1])
+    free, n = awq.awq_kv_compact(cache, table, _i32([2 * page, page + 5]), shared)
+    assert n.item() == 3 and table.tolist() == [[0, 1], [0, 2]] and free[0].item() == 3
+    assert same(0, kept[0]) and same(1, kept[1]) and same(2, kept[1])
+    assert shared[0].item() == 1 and shared.sum().item() == 1

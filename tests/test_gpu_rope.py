@@ -235,3 +235,25 @@ def test_captured_and_on_another_stream():
         want = awq.awq_kv_append_rope(K, V, cache, slots, pos, inv, Q=Q)
         for a, b in zip(got, (want, *cache)):
             assert torch.equal(a, b)
+
+
+def test_strides_past_32_bits():
+    """Tokens 2^27 elements apart: the last ones lie beyond 4 GiB."""
+    import bit_weight_only_quantize_amd as awq
+    torch = torch_mod()
+    T, H, D, stride = 20, 2, 64, 1 << 27
+    big = torch.empty((T - 1) * stride + H * D, dtype=torch.float16, device=dev())
+    q = torch.as_strided(big, (T, H, D), (stride, D, 1))
+    rng = np.random.default_rng(4)
+    x, x32 = _input(rng, (T, H, D), "float16")
+    q.copy_(x)
+    pos, inv = rng.integers(0, 5000, T), frequencies(64)[0]
+    got = awq.awq_rope(q, _i32(pos), _freq(inv), out=q)
+    assert got.data_ptr() == big.data_ptr()
+    _close(q, x32, pos, inv, "float16")
+    q.copy_(x)
+    cache = kv.new_cache(2, H, D, 16, True, rng)
+    dc = _to_cache(cache)
+    awq.awq_kv_append_rope(q, q, dc, _i32(range(T)), _i32(pos), _freq(inv))
+    kv.append(cache, rotate32(x32, pos, inv), x32, np.arange(T))
+    _same_cache(dc, cache)
