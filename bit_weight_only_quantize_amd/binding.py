@@ -963,9 +963,10 @@ def awq_kv_attention_workspace_size(num_tokens: int, num_seqs: int, num_heads: i
     """Workspace bytes of awq_kv_attention for these sizes; cache as passed to it."""
     c, cfg = _cache_arg(cache)
     if sinks != 0 or prefix_len != 0:
-        return int(lib.awq_kv_attention_ex_workspace_size(
+        need = lambda table: int(lib.awq_kv_attention_ex_workspace_size(      # noqa: E731
             num_tokens, num_seqs, num_heads, c, cfg, max_query_len, max_seq_len,
-            awq_kv_attention_options(1, window, sinks, prefix_len, None, -(-prefix_len // c.page_size))))
+            awq_kv_attention_options(1, window, sinks, prefix_len, table, -(-prefix_len // c.page_size))))
+        return max(need(None), need(256) if prefix_len > 0 else 0)    # (with a prefix_table or without)
     return int(lib.awq_kv_attention_workspace_size(num_tokens, num_seqs, num_heads, c, cfg,
                                                    max_query_len, max_seq_len, window))
 
@@ -989,9 +990,10 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     ``workspace``: as in awq_linear_ex.
 
     ``sinks``: beside a window's keys the first `sinks` stay visible.  ``prefix_len``:
-    the first prefix_len tokens of every request are the same, and are read once for all
-    of them, from prefix_table's pages (int32, at least ceil(prefix_len / page_size); the
-    first request's row, if not given)."""
+    the first prefix_len tokens of every request are the same.  They are read once for all
+    of them from prefix_table's pages (int32, at least ceil(prefix_len / page_size)), or
+    without one from the first request's where that saves time; every row then holds
+    them, as awq_kv_fork makes it."""
     torch = _torch()
     c, cfg = _cache_arg(cache)
     D = c.head_dim
@@ -1021,13 +1023,12 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     stride = _token_rows(Q, "Q", heads, D)
     more = sinks != 0 or prefix_len != 0
     if more:
-        at, entries = block_table, blocks            # (its first row)
         if prefix_table is not None:
             _tensor(prefix_table, "prefix_table", torch.int32)
             if prefix_table.dim() != 1:
                 raise ValueError("prefix_table must be 1-D")
-            at, entries = prefix_table, prefix_table.shape[0]
-        opts = awq_kv_attention_options(int(causal), window, sinks, prefix_len, _address(at), entries)
+        opts = awq_kv_attention_options(int(causal), window, sinks, prefix_len, _address(prefix_table),
+                                        0 if prefix_table is None else prefix_table.shape[0])
         need = 0 if workspace is None else lib.awq_kv_attention_ex_workspace_size(
             T, B, heads, c, cfg, max_query_len, max_seq_len, opts)
     else:

@@ -42,7 +42,7 @@ awq_status check_attention_sizes(const char *who, int64_t num_tokens, int32_t nu
     return fail(AWQ_ERR_INVALID_ARG, "%s: negative prefix_len or prefix_blocks", who);
   if (opts->prefix_len > 0) {
     if (opts->window > 0) return fail(AWQ_ERR_UNSUPPORTED, "%s: a shared prefix takes no window", who);
-    if (opts->prefix_len > (int64_t)opts->prefix_blocks * cache->page_size)
+    if (opts->prefix_table && opts->prefix_len > (int64_t)opts->prefix_blocks * cache->page_size)
       return fail(AWQ_ERR_INVALID_ARG, "%s: prefix_len=%d is beyond the prefix_blocks=%d pages of %d tokens", who,
                   opts->prefix_len, opts->prefix_blocks, cache->page_size);
     if (opts->prefix_len > kMaxContext) return fail(AWQ_ERR_UNSUPPORTED, "%s: prefix_len=%d exceeds 2^30", who, opts->prefix_len);
@@ -63,9 +63,11 @@ struct AttentionPlan {
 AttentionPlan plan_of(int64_t num_tokens, int32_t num_seqs, int heads, int group, int D, int32_t max_query_len,
                       int64_t max_seq_len, const awq_kv_attention_options &o) {
   AttentionPlan p{};
-  p.prefix = o.prefix_len > 0;
-  if (p.prefix) p.split = kv_prefix_plan(num_tokens, num_seqs, heads, group, D, max_query_len, max_seq_len, o.prefix_len);
-  else p.whole = kv_attention_plan(num_tokens, num_seqs, heads, group, D, max_query_len, max_seq_len, o.window, o.sinks);
+  if (o.prefix_len > 0) {
+    p.split = kv_prefix_plan(num_tokens, num_seqs, heads, group, D, max_query_len, max_seq_len, o.prefix_len);
+    p.prefix = o.prefix_table || kv_prefix_pays(p.split, num_tokens, num_seqs, heads, group, D, max_query_len, o.prefix_len);
+  }
+  if (!p.prefix) p.whole = kv_attention_plan(num_tokens, num_seqs, heads, group, D, max_query_len, max_seq_len, o.window, o.sinks);
   return p;
 }
 
@@ -110,8 +112,9 @@ awq_status attend(const char *who, const void *Q, int32_t q_dtype, int64_t num_t
   if (!work) return ok();
   if (!Q || !O || !seq_lens || (max_blocks > 0 && !block_table))
     return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
-  if (o.prefix_len > 0 && !o.prefix_table)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: a required pointer is NULL", who);
+  if (o.prefix_len > 0 && !o.prefix_table && o.prefix_len > (int64_t)max_blocks * cache->page_size)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: prefix_len=%d is beyond the max_blocks=%d pages of %d tokens", who,
+                o.prefix_len, max_blocks, cache->page_size);
   if (!aligned(Q, 16) || !aligned(O, 16)) return fail(AWQ_ERR_INVALID_ARG, "%s: Q and O must be 16-byte aligned", who);
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(query_start, 4) || !aligned(lse, 4) ||
       !aligned(o.prefix_table, 4))
@@ -132,7 +135,7 @@ awq_status attend(const char *who, const void *Q, int32_t q_dtype, int64_t num_t
              in[] = {{Q, strided_bytes(num_tokens, q_stride, (int64_t)num_heads * cache->head_dim, 2)},
                      cs.codes, cs.scales, cs.zeros, {block_table, (size_t)num_seqs * max_blocks * 4},
                      {seq_lens, (size_t)num_seqs * 4}, {query_start, query_start ? ((size_t)num_seqs + 1) * 4 : 0},
-                     {o.prefix_table, o.prefix_len > 0 ? (size_t)o.prefix_blocks * 4 : 0}};
+                     {o.prefix_table, o.prefix_table && o.prefix_len > 0 ? (size_t)o.prefix_blocks * 4 : 0}};
   if (!all_apart(out, in))
     return fail(AWQ_ERR_INVALID_ARG, "%s: O, lse or the workspace overlaps Q, the cache or the request arrays", who);
   if (!apart(lse, lse_bytes, O, o_bytes) || !apart(workspace, need, O, o_bytes) ||
@@ -162,12 +165,12 @@ awq_status attend(const char *who, const void *Q, int32_t q_dtype, int64_t num_t
   p.window = o.window;
   p.num_seqs = num_seqs;
   p.sinks = o.window > 0 ? o.sinks : 0;
-  p.after = o.prefix_len;
-  p.prefix_table = o.prefix_table;
-  p.prefix_blocks = o.prefix_blocks;
+  p.after = plan.prefix ? o.prefix_len : 0;
+  p.prefix_table = o.prefix_table ? o.prefix_table : block_table;
+  p.prefix_blocks = o.prefix_table ? o.prefix_blocks : max_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
   const XType xt = q_dtype == AWQ_BF16 ? XType::BF16 : XType::F16;
-  return hip_status(o.prefix_len > 0
+  return hip_status(plan.prefix
                         ? launch_kv_attention_prefix(p, num_seqs, cache->head_dim, xt, plan.split, workspace, as_stream(stream))
                         : launch_kv_attention(p, num_seqs, cache->head_dim, xt, plan.whole, workspace, as_stream(stream)),
                     who);

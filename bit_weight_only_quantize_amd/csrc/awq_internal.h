@@ -318,6 +318,8 @@ struct KvPrefixPlan {
   size_t sum_offset, lo_offset, workspace_bytes;
 };
 KvPrefixPlan kv_prefix_plan(int64_t T, int B, int heads, int group, int D, int max_q, int64_t max_kv, int prefix_len);
+// Whether reading the prefix once, by that plan, is faster than by every request.
+bool kv_prefix_pays(const KvPrefixPlan &plan, int64_t T, int B, int heads, int group, int D, int max_q, int prefix_len);
 hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPlan &plan,
                                void *workspace, hipStream_t st);
 hipError_t launch_kv_attention_prefix(KvAttn p, int B, int D, XType xt, const KvPrefixPlan &plan, void *workspace,

@@ -98,6 +98,21 @@ KvPrefixPlan kv_prefix_plan(int64_t T, int B, int heads, int group, int D, int m
   return pl;
 }
 
+// Reading a prefix once saves passes over its keys, in which the kernels' tiles of rows differ: of 16
+// (decode) cost 1 a key and head, of a prompt's 64 rows 2, of its 128 rows 3, about 1/35000 us each where the
+// card is full (48 requests of up to 4096 tokens, 32 heads of 128: 90 us; half for heads of 64).  It costs two
+// launches, 6 us, and that the parts' results are written and read, 4 TB/s.  Calls of 8 requests of 4 tokens
+// behind 2000 (32 heads over 8) take 15 us in one pass and 25 in two; 32 single tokens behind 200: 9.5 and 21; 64
+// behind 8192 of 32 heads: 275 and 68.  Of 46 calls of all sizes two took the way that was slower by more than 15% (15 requests of 4 tokens behind
+// 3630, 64 heads over 8: 42 us for 33).
+bool kv_prefix_pays(const KvPrefixPlan &pl, int64_t T, int B, int heads, int group, int D, int max_q, int prefix_len) {
+  const int64_t each = (int64_t)max_q * group, all = T * group;
+  const int64_t apart = B * (each <= 32 ? (each + 15) / 16 : 3 * ((each + kPtRows - 1) / kPtRows));
+  const int64_t once = all <= 32 ? (all + 15) / 16 : all <= kPtRows / 2 ? 2 : 3 * ((all + kPtRows - 1) / kPtRows);
+  const double saved = (double)(apart - once) * heads * prefix_len * D / 128 / 35e3;
+  return saved > 6.0 + 2.0 * (double)pl.workspace_bytes / 4e6;
+}
+
 hipError_t launch_kv_attention(KvAttn p, int B, int D, XType xt, const KvAttnPlan &pl,
                                void *workspace, hipStream_t st) {
   if (pl.splits > 1) {

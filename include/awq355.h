@@ -593,22 +593,25 @@ typedef struct awq_kv_attention_options {
     int32_t sinks;               /* with a window: a row sees the first `sinks` keys too, up to
                                   * its last one; without a window it sees them anyway */
     int32_t prefix_len;          /* > 0: the first prefix_len tokens are the same in every
-                                  * request, and lie in prefix_table's pages; window 0 only */
-    const int32_t *prefix_table; /* device, int32 [prefix_blocks]; prefix_blocks * P at
-                                  * least prefix_len */
+                                  * request; window 0 only */
+    const int32_t *prefix_table; /* device, int32 [prefix_blocks]: the pages that hold them,
+                                  * prefix_blocks * P at least prefix_len; or NULL: every
+                                  * row's own entries do, as awq_kv_fork makes them, the first
+                                  * row's among them (max_blocks * P at least prefix_len) */
     int32_t prefix_blocks;
 } awq_kv_attention_options;
 
 /*
  * awq_kv_attention_ex - awq_kv_attention with a window that keeps the first tokens
- * visible, or over a prefix that all requests share (a row of a table that awq_kv_fork
- * made serves as prefix_table).
+ * visible, or over a prefix that all requests share.
  *   opts      host.  With sinks the keys between them and a row's window are not read,
- *             so their pages may have been released.  With a prefix its keys are read once for
- *             the query rows of all requests; seq_lens and max_seq_len count it, what the
- *             block table says of its full pages does not matter, and a row sees of it what it
- *             sees by its own length: a request of seq_lens 0, as a padded batch has, gets
- *             O = 0.  prefix_len is the host's: a captured graph keeps it.  (Logits above 2^21
+ *             so their pages may have been released.  With a prefix in prefix_table its keys are
+ *             read once for the query rows of all requests, and what the block table says of
+ *             its full pages does not matter; without that table they are, from the first row's
+ *             pages, where it saves time, else by each request as awq_kv_attention does (few
+ *             requests, or a short prefix).  seq_lens and max_seq_len count the prefix, and a row
+ *             sees of it what it sees by its own length: a request of seq_lens 0, as a
+ *             padded batch has, gets O = 0.  prefix_len is the host's: a captured graph keeps it.  (Logits above 2^21
  *             or so that tie between the prefix and the rest are decided by their roundings.)
  *   workspace  awq_kv_attention_ex_workspace_size() bytes for the same opts.
  * Everything else as awq_kv_attention, which is this with no sinks and no prefix.
@@ -622,7 +625,8 @@ awq_status awq_kv_attention_ex(const void *Q, int32_t q_dtype, int64_t num_token
                                float *lse, void *workspace, size_t workspace_bytes,
                                awq_stream_t stream);
 
-/* awq_kv_attention_workspace_size for awq_kv_attention_ex (prefix_table may be NULL here). */
+/* awq_kv_attention_workspace_size for awq_kv_attention_ex (of prefix_table only whether it is
+ * NULL matters here). */
 size_t awq_kv_attention_ex_workspace_size(int64_t num_tokens, int32_t num_seqs, int32_t num_heads,
                                           const awq_kv_cache *cache, awq_config cfg,
                                           int32_t max_query_len, int64_t max_seq_len,

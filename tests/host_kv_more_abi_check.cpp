@@ -130,7 +130,7 @@ int main() {
         for (int64_t mk : {(int64_t)0, (int64_t)1, (int64_t)5000, (int64_t)1 << 31, top64})
           for (int32_t prefix : {0, 1, 16, 17, 5000, (int32_t)1 << 30})
             for (int32_t window : {0, 1, 1000, top}) {
-              const size_t n = size(T, seqs, 4, mq, mk, {1, window, prefix ? 0 : 1 << 30, prefix, nullptr, (int32_t)1 << 26});
+              const size_t n = size(T, seqs, 4, mq, mk, {1, window, prefix ? 0 : 1 << 30, prefix, i[3], (int32_t)1 << 26});
               EXPECT(n % 4 == 0);
               if (prefix && !window && T <= 70000 && seqs <= 65535 && mq == 1 && mq * 2 <= 1 << 30) EXPECT(n > 0);
               if (prefix && window) EXPECT(n == 0);

@@ -128,12 +128,15 @@ class Behind(Attend):
                 if zeros is not None:
                     zeros[self.table[b, same]][:, pos] = zeros[src[same]][:, pos]
 
-    def check(self, causal=True, scale=None, table=None, **kw):
-        O, lse = self.run(causal=causal, scale=scale, prefix_len=self.prefix, **kw)
-        _within(O, lse, *kv.attention64(self.q64, self.cache, self.table if table is None else table, self.kv_lens,
-                                        self.start, self.D ** -0.5 if scale is None else scale, causal, 0,
-                                        EPS[self.dtype]))
-        return O, lse
+    def check(self, causal=True, scale=None, table=None, prefix_table=None, whole=True):
+        """Read once, from a table of its own, and (`whole`) as the rows' own entries have it."""
+        want = kv.attention64(self.q64, self.cache, self.table if table is None else table, self.kv_lens, self.start,
+                              self.D ** -0.5 if scale is None else scale, causal, 0, EPS[self.dtype])
+        kw = dict(causal=causal, scale=scale, prefix_len=self.prefix)
+        ids = self.table[0] if prefix_table is None else prefix_table
+        _within(*self.run(prefix_table=_i32(ids), **kw), *want)
+        if whole:
+            _within(*self.run(**kw), *want)
 
 
 @pytest.mark.parametrize("prefix,kv_lens,Hq,Hkv,D,page,zp,dtype", [
@@ -182,7 +185,7 @@ def test_own_prefix_table(n):
     full = a.table.copy()
     a.table[:, :80 // 16] = [[-1], [2 ** 31 - 1]]
     ids = np.concatenate([full[0, :5], [-1, 7]])
-    a.check(table=full, prefix_table=_i32(ids))
+    a.check(table=full, prefix_table=ids, whole=False)
 
 
 @pytest.mark.parametrize("n", [1, 40])
@@ -190,6 +193,15 @@ def test_a_missing_page_of_the_prefix(n):
     a = Behind(96, [n, n], [150, 99 + n], 4, 2, 64, 16, True, "float16", seed=9)
     a.table[:, 2], a.table[0, 4], a.table[1, 4] = -1, -7, -7
     a.check()
+
+
+def test_where_it_pays_the_first_row_is_read():
+    """Enough requests behind a prefix long enough: the other rows' entries do not matter then."""
+    a = Behind(3000, [1] * 40, [3001 + 3 * i for i in range(40)], 8, 8, 128, 64, True, "float16", seed=6)
+    full = a.table.copy()
+    a.check()
+    a.table[1:, :3000 // 64] = -1
+    a.check(table=full)
 
 
 @pytest.mark.parametrize("n", [1, 40])
@@ -208,9 +220,10 @@ def test_rows_of_no_request_are_left_alone():
     Q[3:10] = a.Q
     out = torch.full_like(Q, 7.0)
     cache = _to_cache(a.cache)
+    row = _i32(a.table[0])
     awq.awq_kv_attention(Q, cache, _i32(a.table), _i32(a.kv_lens), query_start=_i32([3, 5, 10]), max_query_len=3,
-                         out=out, prefix_len=40)
-    full, _ = a.run(prefix_len=40)
+                         out=out, prefix_len=40, prefix_table=row)
+    full, _ = a.run(prefix_len=40, prefix_table=row)
     assert (out[:3] == 7).all() and (out[8:] == 7).all()
     # (split otherwise: equal up to rounding)
     assert (out[3:8].float() - full[:5].float()).abs().max().item() <= 2.0 ** -9 * float(full.abs().max())
@@ -232,9 +245,10 @@ def test_calls_repeat_and_do_not_depend_on_the_workspace(n, kind):
     torch = torch_mod()
     a = Behind(700, [n, n], [2400, 2300], 8, 1, 64, 16, True, "float16", seed=13)
     kw = dict(window=1900, sinks=70) if kind == "sinks" else dict(prefix_len=700)
+    table = {} if kind == "sinks" else dict(prefix_table=_i32(a.table[0]))
     cache = _to_cache(a.cache)
     args = (a.Q, cache, _i32(a.table), _i32(a.kv_lens))
-    more = dict(query_start=_i32(a.start), max_query_len=n, max_seq_len=2400, return_lse=True, **kw)
+    more = dict(query_start=_i32(a.start), max_query_len=n, max_seq_len=2400, return_lse=True, **kw, **table)
     want = awq.awq_kv_attention(*args, **more)
     need = awq.awq_kv_attention_workspace_size(2 * n, 2, 8, cache, n, 2400, **kw)
     assert need > 0
@@ -317,6 +331,7 @@ def test_two_calls_at_once_on_two_streams(n):
     import bit_weight_only_quantize_amd as awq
     cases = [(Behind(300, [n] * 3, [900, 700, 0], 8, 2, 64, 16, True, "float16", seed=s),
               dict(prefix_len=300) if s else dict(window=200, sinks=40)) for s in (0, 1)]
+    cases[1][1]["prefix_table"] = _i32(cases[1][0].table[0])
     calls, wants = [], []
     for a, kw in cases:
         args = (a.Q, _to_cache(a.cache), _i32(a.table), _i32(a.kv_lens))

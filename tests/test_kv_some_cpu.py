@@ -33,7 +33,7 @@ def test_cache_refusals(kw, status):
     (dict(o=opts(causal=2)), INVALID), (dict(o=opts(causal=0, window=4, sinks=1)), INVALID),
     (dict(o=opts(prefix=-1)), INVALID), (dict(o=opts(prefix=20, blocks=-1)), INVALID), (dict(o=opts(prefix=20, blocks=1)), INVALID),
     (dict(o=opts(prefix=20, window=5)), UNSUPPORTED), (dict(o=opts(prefix=2 ** 30 + 1, blocks=2 ** 27)), UNSUPPORTED),
-    (dict(o=opts(prefix=20, table=None)), INVALID), (dict(o=opts(prefix=20, table=P(0x10002))), INVALID),
+    (dict(o=opts(prefix=20, table=None), blocks=1), INVALID), (dict(o=opts(prefix=20, table=P(0x10002))), INVALID),
     (dict(T=2 ** 30, B=3, start=addr(11), mq=1, o=opts(prefix=20)), UNSUPPORTED),
     (dict(qt=2), INVALID), (dict(T=-1), INVALID), (dict(heads=3), INVALID), (dict(qs=250), INVALID), (dict(mq=2), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(blocks=2 ** 28), INVALID), (dict(Q=None), INVALID), (dict(O=None), INVALID),
@@ -54,6 +54,8 @@ def test_workspaces():
     assert size(mk=60000, o=opts(window=100, sinks=4)) == 0 < size(mk=60000, o=opts(window=100, sinks=50000))
     rows = 3 * 4 * (64 * 4 + 12)                            # a part's results: values, two floats, one
     assert size(o=opts(prefix=20)) == 2 * rows and size(T=0, B=0, o=opts(prefix=20)) == 0
+    assert size(o=opts(prefix=20, table=None)) == 0         # (in one pass: too little to save)
+    assert size(T=64, B=64, mk=9000, o=opts(prefix=8000, table=None)) == size(T=64, B=64, mk=9000, o=opts(prefix=8000, blocks=500)) > 0
     assert size(o=opts(prefix=200, blocks=8)) == 0 and size(o=opts(prefix=20, window=3)) == 0
     assert attend(T=0, B=0, Q=None, O=None, lens=None, table=None, ws=None) == OK
     assert attend(T=0, B=0, Q=None, O=None, lens=None, table=None, ws=None, o=opts(prefix=20, table=None)) == OK
