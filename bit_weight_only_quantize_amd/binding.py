@@ -1081,8 +1081,8 @@ def _free_arg(free_pages, taken, name="taken"):
         _check(taken, name, i32, (1,))
 
 
-def _named(**tensors):
-    return ((t, name) for name, t in tensors.items() if t is not None)
+def _maybe(t, name):
+    return None if t is None else (t, name)
 
 
 def awq_kv_copy_pages(cache, src, dst):
@@ -1117,9 +1117,9 @@ def awq_kv_fork(cache, block_table, parents, children, lens, shared, free_pages,
     _free_arg(free_pages, taken)
     if out is not None:
         _check(out, "out", i32, (1,))
-    dev = _one_gpu(*_cache_tensors(cache), *_named(block_table=block_table, parents=parents, children=children,
-                                                   lens=lens, shared=shared, free_pages=free_pages, taken=taken,
-                                                   out=out))
+    dev = _one_gpu(*_cache_tensors(cache), (block_table, "block_table"), (parents, "parents"), (children, "children"),
+                   (lens, "lens"), (shared, "shared"), (free_pages, "free_pages"), _maybe(taken, "taken"),
+                   _maybe(out, "out"))
     if out is None:
         out = parents.new_empty(1)
     st = _launch(lib.awq_kv_fork, dev, c, cfg, _address(parents), _address(children), _address(lens),
@@ -1160,10 +1160,10 @@ def awq_kv_release(block_table, seq_lens, shared, free_pages, page_size: int, st
         _check(out[1], "count", i32, (1,))
     need = 0 if workspace is None else lib.awq_kv_release_workspace_size(pages, free_pages.shape[0])
     ws, ws_bytes = _scratch(workspace, need, shared)
-    dev = _one_gpu((block_table, "block_table"), *_named(
-        seq_lens=seq_lens, start=start, end=end, shared=shared, free_pages=free_pages, pages_used=pages_used,
-        out=None if out is None else out[0], count=None if out is None else out[1], workspace=ws))
-    if out is None:
+    dev = _one_gpu((block_table, "block_table"), (seq_lens, "seq_lens"), _maybe(start, "start"), _maybe(end, "end"),
+                   (shared, "shared"), (free_pages, "free_pages"), _maybe(pages_used, "pages_used"),
+                   *(() if out is None else ((out[0], "out"), (out[1], "count"))), _maybe(ws, "workspace"))
+    if out is None:                                 # one allocation, in two parts
         out = shared.new_empty(pages + 1).split_with_sizes((pages, 1))
     st = _launch(lib.awq_kv_release, dev, _address(block_table), B, blocks, page_size, _address(seq_lens),
                  _address(start), _address(end), _address(shared), pages, _address(free_pages), free_pages.shape[0],
@@ -1192,9 +1192,8 @@ def awq_kv_compact(cache, block_table, seq_lens, shared, out=None, workspace="au
         _check(out[1], "num_used", i32, (1,))
     need = 0 if workspace is None else lib.awq_kv_compact_workspace_size(c.num_pages, c.page_size)
     ws, ws_bytes = _scratch(workspace, need, shared)
-    dev = _one_gpu(*_cache_tensors(cache), *_named(
-        block_table=block_table, seq_lens=seq_lens, shared=shared, out=None if out is None else out[0],
-        num_used=None if out is None else out[1], workspace=ws))
+    dev = _one_gpu(*_cache_tensors(cache), (block_table, "block_table"), (seq_lens, "seq_lens"), (shared, "shared"),
+                   *(() if out is None else ((out[0], "free_pages"), (out[1], "num_used"))), _maybe(ws, "workspace"))
     if out is None:
         out = shared.new_empty(c.num_pages + 1).split_with_sizes((c.num_pages, 1))
     st = _launch(lib.awq_kv_compact, dev, c, cfg, _address(block_table), B, blocks, _address(seq_lens),
