@@ -46,9 +46,9 @@ awq_status check_attention_sizes(const char *who, int64_t num_tokens, int32_t nu
       return fail(AWQ_ERR_INVALID_ARG, "%s: prefix_len=%d is beyond the prefix_blocks=%d pages of %d tokens", who,
                   opts->prefix_len, opts->prefix_blocks, cache->page_size);
     if (opts->prefix_len > kMaxContext) return fail(AWQ_ERR_UNSUPPORTED, "%s: prefix_len=%d exceeds 2^30", who, opts->prefix_len);
-    // (the rows of all requests are counted as one's)
-    if (num_tokens * (num_heads / cache->num_kv_heads) > ((int64_t)1 << 30))
-      return fail(AWQ_ERR_UNSUPPORTED, "%s: a shared prefix takes at most 2^30 query tokens times the query heads per key/value head", who);
+    // (the rows of all requests are counted as one's, and a grid of waves joins a row each)
+    if (num_tokens * (num_heads / cache->num_kv_heads) > ((int64_t)1 << 25))
+      return fail(AWQ_ERR_UNSUPPORTED, "%s: a shared prefix takes at most 2^25 query tokens times the query heads per key/value head", who);
   }
   return AWQ_OK;
 }

@@ -12,6 +12,8 @@ using namespace awq;
 namespace {
 
 constexpr double kTwoPi = 6.283185307179586;
+// Four tokens to a workgroup of 256, and a grid holds less than 2^32 threads.
+constexpr int64_t kMaxRopeTokens = (int64_t)1 << 25;
 
 awq_status check_rope(const char *who, const awq_rope_args *r, int32_t head_dim) {
   if (!r) return fail(AWQ_ERR_INVALID_ARG, "%s: rope is NULL", who);
@@ -135,8 +137,8 @@ awq_status awq_rope(const void *Q, void *Q_out, int32_t num_heads, int64_t q_str
   if (head_dim < 16 || head_dim % 16 != 0 || head_dim > AWQ_ROPE_MAX_DIM)
     return fail(AWQ_ERR_UNSUPPORTED, "%s: head_dim=%d: must be a multiple of 16 in [16, %d]", who, head_dim,
                 AWQ_ROPE_MAX_DIM);
-  if (num_tokens < 0 || num_tokens > kMaxTokens)
-    return fail(AWQ_ERR_INVALID_ARG, "%s: num_tokens=%lld: must be in [0, 2^27]", who, (long long)num_tokens);
+  if (num_tokens < 0 || num_tokens > kMaxRopeTokens)
+    return fail(AWQ_ERR_INVALID_ARG, "%s: num_tokens=%lld: must be in [0, 2^25]", who, (long long)num_tokens);
   awq_status st = check_rope(who, rope, head_dim);
   if (st == AWQ_OK) st = check_heads(who, "Q", num_heads, (int64_t)num_heads * head_dim, num_tokens, q_stride, qo_stride);
   if (st == AWQ_OK) st = check_heads(who, "K", num_kv_heads, (int64_t)num_kv_heads * head_dim, num_tokens, k_stride, ko_stride);
@@ -169,6 +171,7 @@ awq_status awq_kv_append_rope(const void *Q, void *Q_out, int32_t num_heads, int
   const char *who = "awq_kv_append_rope";
   awq_status st = check_append(who, K, V, x_dtype, num_tokens, k_stride, v_stride, cache, cfg, slots, nonfinite_count);
   if (st != AWQ_OK) return st;
+  if (num_tokens > kMaxRopeTokens) return fail(AWQ_ERR_INVALID_ARG, "%s: more than 2^25 tokens", who);
   const int32_t D = cache->head_dim;
   st = check_rope(who, rope, D);
   if (st == AWQ_OK) st = check_heads(who, "Q", num_heads, (int64_t)num_heads * D, num_tokens, q_stride, qo_stride);

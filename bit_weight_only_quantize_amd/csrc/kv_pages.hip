@@ -79,7 +79,8 @@ __device__ __forceinline__ int64_t blocks_of(int64_t len, int pshift, int max_bl
 }
 
 // ---- copy ---------------------------------------------------------------------------
-// Bound by memory: a read and a write of every byte.
+// Bound by memory: a read and a write of every byte.  2000 pages of 69 KB: 57 us, 4.8 TB/s (4096
+// workgroups in a loop: 65).
 __global__ __launch_bounds__(kPageThreads) void kv_copy_pages_kernel(KvCache c, const int32_t *__restrict__ src,
                                                                      const int32_t *__restrict__ dst, int64_t units,
                                                                      int64_t pieces) {
@@ -96,7 +97,8 @@ __global__ __launch_bounds__(kPageThreads) void kv_copy_pages_kernel(KvCache c, 
 // The free page that it takes is numbered by the forks before it that take one, which every
 // workgroup counts itself: a few hundred pairs of loads, where an exchange between
 // workgroups would cost another launch.  Bound by latency: lists, lengths, the parent's
-// entries, the page.
+// entries, the page (8 forks of up to 1500 tokens 5.4 us; 200 of up to 20000 in small pages, 120000
+// counts, 9.8).
 struct ForkPage {
   int64_t last;            // the parent's page that is copied, or -1
   bool takes;
@@ -375,7 +377,8 @@ __global__ __launch_bounds__(THREADS) void kv_release_list_kernel(ReleaseArgs a,
 // written from one ranking of the used pages.  One workgroup marks and ranks a pool of up
 // to 32768 pages and a table of up to 65536 entries in LDS (one launch); larger ones take
 // four: clear, mark, count, list.
-// The last launch copies the pages, moves their counts and renumbers the tables.
+// The last launch copies the pages, moves their counts and renumbers the tables.  (7300 pages of 68
+// KB, 96 rows, 1700 pages moved: 11 us for the lists and 53, 4.4 TB/s, for the pages.)
 __global__ __launch_bounds__(kPageThreads) void kv_compact_clear_kernel(uint8_t *used, int64_t pages) {
   for (int64_t i = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; i < pages; i += (int64_t)gridDim.x * kPageThreads)
     used[i] = 0;

@@ -611,7 +611,7 @@ typedef struct awq_kv_attention_options {
  *             pages, where it saves time, else by each request as awq_kv_attention does (few
  *             requests, or a short prefix).  seq_lens and max_seq_len count the prefix, and a row
  *             sees of it what it sees by its own length: a request of seq_lens 0, as a
- *             padded batch has, gets O = 0.  prefix_len is the host's: a captured graph keeps it.  (Logits above 2^21
+ *             padded batch has, gets O = 0.  num_tokens * num_heads / H at most 2^25 then.  prefix_len is the host's: a captured graph keeps it.  (Logits above 2^21
  *             or so that tie between the prefix and the rest are decided by their roundings.)
  *   workspace  awq_kv_attention_ex_workspace_size() bytes for the same opts.
  * Everything else as awq_kv_attention, which is this with no sinks and no prefix.
@@ -638,8 +638,10 @@ size_t awq_kv_attention_ex_workspace_size(int64_t num_tokens, int32_t num_seqs, 
  * counts for each page the table entries that hold it beyond the first.  All zeros
  * at the start; awq_kv_fork adds, awq_kv_release subtracts, awq_kv_compact moves the
  * counts along, and a page that awq_kv_assign hands out has none.  Nothing may be
- * appended to a page that is shared (awq_kv_fork shares full pages only, so a
- * request that appends behind its own last token never does).
+ * appended to a page that is shared.  awq_kv_fork shares full pages only, so a
+ * request that appends behind its own last token never does; one that has given
+ * tokens back, so that it would go on inside a shared page, goes on as a branch of
+ * itself in another row.
  *
  * A free list is device int32 [num_free], ids to take from the front and entries
  * outside [0, num_pages) for none.  `taken`, device int32 [1] or NULL, says how many of
@@ -725,7 +727,8 @@ size_t awq_kv_release_workspace_size(int64_t num_pages, int32_t num_free);
  *   num_used  device, int32 [1], written: n.
  *   workspace  device, 256-byte aligned, awq_kv_compact_workspace_size() bytes; scratch,
  *             not to be shared by calls that overlap in time.
- * Free lists from before the call are void.  max_blocks * P < 2^31, num_seqs at most 2^20.
+ * Free lists from before the call are void, and pages that only other tables hold are
+ * lost.  max_blocks * P < 2^31, num_seqs at most 2^20.
  */
 awq_status awq_kv_compact(const awq_kv_cache *cache, awq_config cfg, int32_t *block_table,
                           int32_t num_seqs, int32_t max_blocks, const int32_t *seq_lens,
@@ -800,7 +803,7 @@ awq_status awq_rope_frequencies(int32_t rotary_dim, double base, const awq_rope_
  *   Q_out, K_out  likewise, qo_stride / ko_stride apart, rounded once to x_dtype.
  *            Q_out may be Q with the same stride, and K_out K (in place); otherwise
  *            what is written overlaps neither what is read nor itself.
- * head_dim a multiple of 16, at most AWQ_ROPE_MAX_DIM; num_tokens at most 2^27; at
+ * head_dim a multiple of 16, at most AWQ_ROPE_MAX_DIM; num_tokens at most 2^25; at
  * most AWQ_KV_MAX_HEADS heads each.
  */
 awq_status awq_rope(const void *Q, void *Q_out, int32_t num_heads, int64_t q_stride,
@@ -816,6 +819,7 @@ awq_status awq_rope(const void *Q, void *Q_out, int32_t num_heads, int64_t q_str
  *            with num_heads = 0.  Q_out may be Q with the same stride, and may
  *            overlap nothing else that the call reads or writes.  Queries of tokens
  *            without a slot are rotated too.
+ * num_tokens at most 2^25.
  */
 awq_status awq_kv_append_rope(const void *Q, void *Q_out, int32_t num_heads, int64_t q_stride,
                               int64_t qo_stride, const void *K, const void *V, int32_t x_dtype,

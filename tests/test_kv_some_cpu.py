@@ -35,6 +35,7 @@ def test_cache_refusals(kw, status):
     (dict(o=opts(prefix=20, window=5)), UNSUPPORTED), (dict(o=opts(prefix=2 ** 30 + 1, blocks=2 ** 27)), UNSUPPORTED),
     (dict(o=opts(prefix=20, table=None), blocks=1), INVALID), (dict(o=opts(prefix=20, table=P(0x10002))), INVALID),
     (dict(T=2 ** 30, B=3, start=addr(11), mq=1, o=opts(prefix=20)), UNSUPPORTED),
+    (dict(T=2 ** 24 + 1, B=3, start=addr(11), mq=1, o=opts(prefix=20)), UNSUPPORTED),
     (dict(qt=2), INVALID), (dict(T=-1), INVALID), (dict(heads=3), INVALID), (dict(qs=250), INVALID), (dict(mq=2), INVALID),
     (dict(scale=float("nan")), INVALID), (dict(blocks=2 ** 28), INVALID), (dict(Q=None), INVALID), (dict(O=None), INVALID),
     (dict(lens=None), INVALID), (dict(table=None), INVALID), (dict(ws=None), WORKSPACE), (dict(wsb=64), WORKSPACE),

@@ -84,7 +84,7 @@ def append(Q=addr(2), Qo=addr(3), heads=4, qs=256, qos=256, K=addr(4), V=addr(5)
 
 
 ROPE_REFUSALS = [
-    (dict(xt=2), INVALID), (dict(T=-1), INVALID), (dict(T=2 ** 27 + 1), INVALID), (dict(heads=-1), INVALID),
+    (dict(xt=2), INVALID), (dict(T=-1), INVALID), (dict(T=2 ** 25 + 1), INVALID), (dict(T=2 ** 27 + 1), INVALID), (dict(heads=-1), INVALID),
     (dict(heads=1025, qs=1 << 20, qos=1 << 20), INVALID), (dict(qs=248), INVALID), (dict(qos=260), INVALID),
     (dict(qs=1 << 58), INVALID), (dict(r=args(R=0)), UNSUPPORTED), (dict(r=args(R=24)), UNSUPPORTED),
     (dict(r=args(R=80)), UNSUPPORTED), (dict(r=args(pairs=2)), INVALID), (dict(r=args(inverse=-1)), INVALID),
