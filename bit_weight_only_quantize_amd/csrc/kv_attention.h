@@ -1318,6 +1318,50 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
 
   // ---- store: lane (q, hh) holds LDS rows 32n + 8g + 4hh + e of row q, all
   // eight channels of D/16 of its words
+  // (a shared prefix' parts: every workgroup has one, and they end together, so rows go through LDS to
+  // whole lines: 33 MB of 504 workgroups cost ... us so, 8 in pieces of 32 bytes)
+  if constexpr (KEYS == kShared) {
+    if (!wave_live) return;
+    l += __shfl_xor(l, 32, 64);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // (a row that sees no key: zeros, and its sum says so)
+    constexpr int kStoreRow = D + 4, kPerStep = 256 / D;     // floats of a row in LDS; rows that a wave stores at a time
+    static_assert(4 * 32 * kStoreRow * 4 <= (int)sizeof(sms));
+    float *st = reinterpret_cast<float *>(sms) + rw * (32 * kStoreRow);
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      const int word = D == 128 ? 8 * (x >> 2) + 4 * hh + (x & 3) : 4 * hh + x;
+      float v[8];
+#pragma unroll
+      for (int ch = 0; ch < 8; ++ch) {
+        const int n = D == 128 ? ch >> 1 : ch >> 2;
+        const int g = D == 128 ? 2 * (ch & 1) + (x >> 2) : ch & 3;
+        v[ch] = o[n][4 * g + (x & 3)] * inv;
+      }
+      float4 *q4 = reinterpret_cast<float4 *>(st + qc * kStoreRow + 8 * word);
+      q4[0] = float4{v[0], v[1], v[2], v[3]};
+      q4[1] = float4{v[4], v[5], v[6], v[7]};
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // (the wave's own rows: its lanes' stores come first)
+    __builtin_amdgcn_wave_barrier();
+    const int64_t all = (int64_t)p.heads * p.group, base = split * p.T * all + h * p.group;
+    auto place = [&](int r) {                                // of row r among the part's
+      const int token = token_of(p, r);
+      return base + token * all + (r - token * p.group);
+    };
+    const int first = row0 + rw * 32;
+    if (hh == 0 && first + qc < rows) {
+      const int64_t at = place(first + qc);
+      p.part_sum[at] = float2{M, l};
+      if (__builtin_expect(may_have_low_part(M), 0)) p.part_lo[at] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += kPerStep) {
+      const int rr = i + lane / (D / 4), c = (lane % (D / 4)) * 4;
+      const float4 v = *reinterpret_cast<const float4 *>(st + rr * kStoreRow + c);
+      if (first + rr < rows) *reinterpret_cast<float4 *>(p.part_o + place(first + rr) * D + c) = v;
+    }
+    return;
+  }
   l += __shfl_xor(l, 32, 64);
   if (row0 + rw * 32 + qc >= rows) return;
   const bool none = l == 0.0f;
