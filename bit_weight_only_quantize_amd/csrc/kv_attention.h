@@ -1319,7 +1319,8 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   // ---- store: lane (q, hh) holds LDS rows 32n + 8g + 4hh + e of row q, all
   // eight channels of D/16 of its words
   // (a shared prefix' parts: every workgroup has one, and they end together, so rows go through LDS to
-  // whole lines: 33 MB of 504 workgroups cost ... us so, 8 in pieces of 32 bytes)
+  // whole lines: with 33 MB of parts of 504 workgroups the kernel takes 78.7 us for 32768 keys and 33.4 for
+  // 10752 so, 83.6 and 38.8 in pieces of 32 bytes)
   if constexpr (KEYS == kShared) {
     if (!wave_live) return;
     l += __shfl_xor(l, 32, 64);
