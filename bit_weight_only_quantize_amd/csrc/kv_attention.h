@@ -1327,6 +1327,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;           // (a row that sees no key: zeros, and its sum says so)
     constexpr int kStoreRow = D + 4, kPerStep = 256 / D;     // floats of a row in LDS; rows that a wave stores at a time
     static_assert(4 * 32 * kStoreRow * 4 <= (int)sizeof(sms));
+    static_assert(32 * kStoreRow == (16 * kTiles + 2) * 64);   // (a wave's rows lie over its own sums alone, which it has read)
     float *st = reinterpret_cast<float *>(sms) + rw * (32 * kStoreRow);
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
