@@ -64,7 +64,7 @@ __device__ __forceinline__ float2 cos_sin(double x, double factor) {
 struct Turn {
   float c[8], s[8];
   int from;              // the partner's lane (paired halves)
-  bool on;               // the channels are among the first R
+  uint32_t on;           // all bits where the channels are among the first R, else none
 };
 
 // Cosines and sines of the workgroup's tokens, from t0 on, into `table` [token][R/2].
@@ -84,13 +84,13 @@ template <bool PAIRS>
 __device__ __forceinline__ Turn turn_of(const RopeArgs &p, const float2 *table, int token, int w, int lane) {
   Turn t;
   const int half = p.rotary_dim / 2, apart = half / 8;
-  t.on = w < 2 * apart;
-  const bool low = w < apart;
-  t.from = lane + (t.on ? (low ? apart : -apart) : 0);
+  const bool on = w < 2 * apart, low = w < apart;
+  t.on = on ? ~0u : 0u;
+  t.from = lane + (on ? (low ? apart : -apart) : 0);
   const float2 *row = table + token * half;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int j = !t.on ? 0 : PAIRS ? 4 * w + i / 2 : 8 * (low ? w : w - apart) + i;
+    const int j = !on ? 0 : PAIRS ? 4 * w + i / 2 : 8 * (low ? w : w - apart) + i;
     const float2 cs = row[j];
     t.c[i] = cs.x;
     t.s[i] = (PAIRS ? (i & 1) == 0 : low) ? -cs.y : cs.y;
@@ -115,10 +115,11 @@ __device__ __forceinline__ void turn8(const Turn &t, u32x4 raw, float (&v)[8]) {
     }
     widen8<BF16>(theirs, other);
   }
+  // (chosen by bits: the compiler makes branches of a choice between a product and a value)
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = v[i] * t.c[i] + other[i] * t.s[i];
-    v[i] = t.on ? y : v[i];
+    const uint32_t y = __builtin_bit_cast(uint32_t, v[i] * t.c[i] + other[i] * t.s[i]);
+    v[i] = __builtin_bit_cast(float, (y & t.on) | (__builtin_bit_cast(uint32_t, v[i]) & ~t.on));
   }
 }
 
@@ -252,6 +253,9 @@ __global__ __launch_bounds__(kRopeThreads) void kv_append_rope_kernel(
   }
   const Turn turn = turn_of<PAIRS>(p, table, kv_token, w, lane);
   int bad = 0;
+  // (places of the lane's first head; the next ones' lie as far apart)
+  KvPlace at = kv_place<D>(active ? slot : 0, pshift, kh.first, heads, w);
+  const int64_t apart = (int64_t)kKvSide << pshift;
   for (int h = kh.first; h - kv_mine < kh.end; h += kKvSide) {
     u32x4 kn, vn;
     load_pair(kn, vn, h + kKvSide);
@@ -261,16 +265,19 @@ __global__ __launch_bounds__(kRopeThreads) void kv_append_rope_kernel(
     kr = kn;
     vr = vn;
     const QuantWord qk = quantize_word<kLanes, SYM>(k, bad), qv = quantize_word<kLanes, SYM>(v, bad);
+    const KvPlace here = at;
+    at.k_word += apart * kLanes;
+    at.v_word += apart * kLanes;
+    at.meta += apart * 2;
     if (!active || h >= kh.end) continue;
     if (nonfinite != nullptr && w == 0) bad += (int)qk.overflow + (int)qv.overflow;
-    const KvPlace at = kv_place<D>(slot, pshift, h, heads, w);
-    codes[at.k_word] = qk.word;
-    codes[at.v_word] = qv.word;
+    codes[here.k_word] = qk.word;
+    codes[here.v_word] = qv.word;
     if (w == 0) {
-      *reinterpret_cast<uint32_t *>(scales + at.meta) =
+      *reinterpret_cast<uint32_t *>(scales + here.meta) =
           (uint32_t)__builtin_bit_cast(uint16_t, qk.step) | ((uint32_t)__builtin_bit_cast(uint16_t, qv.step) << 16);
       if constexpr (!SYM)
-        *reinterpret_cast<uint16_t *>(zeros + at.meta) = (uint16_t)((uint32_t)qk.zero | ((uint32_t)qv.zero << 8));
+        *reinterpret_cast<uint16_t *>(zeros + here.meta) = (uint16_t)((uint32_t)qk.zero | ((uint32_t)qv.zero << 8));
     }
   }
   if (nonfinite != nullptr) {
