@@ -1516,7 +1516,7 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   if constexpr (KEYS != kShared) {
     const int parts = p.splits + (KEYS == kSome ? p.prefix_parts : 0);
     if (e != hipSuccess || parts == 1) return e;
-    // (enough rows fill the card with a wave each: 3072 rows of 23 parts take 8.4 us so, 12.4 with four)
+    // (enough rows fill the card with a wave each: 48 tokens of 64 heads, 23 parts, take 8.4 us so, 12.4 with four)
     const bool many = KEYS == kSome && rows * p.heads * B >= kJoinRows;
     if (parts > kJoinWide && !many)
       kv_join_kernel<D, BF16, 4, KEYS><<<dim3((unsigned)rows, (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);

@@ -18,10 +18,12 @@
 // value words interleave.  Loads of the next heads are under way while some are turned,
 // and the first before the angles are.
 //
-// Bound by memory: 4097 tokens, 32 and 8 heads of 128 of which 64 channels turn, 84 MB: 16.4 us, 5.1
-// TB/s, a copy's rate (16 tokens to a workgroup, a wave on four tokens of one head: 20.0).  Into the cache
-// by the quantizer's VALU as well (71% busy): 8192 tokens, 32 heads of 128 each, 304 MB: 80 us.  Few tokens by
-// a launch's latency and the chain of fp64 operations, about 30 per angle (32 tokens: 6.3 us).
+// Bound by memory: 4097 tokens, 32 and 8 heads of 128 of which 64 channels turn, 84 MB: 15.6 us, 5.4
+// TB/s, a copy's rate (16 tokens to a workgroup, a wave on four tokens of one head: 20.0).  Into the
+// cache 8192 tokens, 32 heads of 128 each, 304 MB: 78 us, 3.9 TB/s, its VALU 72% busy; 32 of 430
+// VALU instructions per step fewer in the quantizer gave 1%, and neither twice the workgroups nor
+// loads two heads ahead gave any.  Few tokens by a launch's latency and the chain of fp64 operations, about 30 per angle (32
+// tokens: 5.8 us).
 
 #include "awq_internal.h"
 #include "device_common.h"
