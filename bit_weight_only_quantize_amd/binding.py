@@ -992,8 +992,9 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     ``sinks``: beside a window's keys the first `sinks` stay visible.  ``prefix_len``:
     the first prefix_len tokens of every request are the same.  They are read once for all
     of them from prefix_table's pages (int32, at least ceil(prefix_len / page_size)), or
-    without one from the first request's where that saves time; every row then holds
-    them, as awq_kv_fork makes it."""
+    without one, where that saves time, from those of the first request with query tokens
+    that reaches prefix_len (of the longest, if none does); each request then holds them, as
+    awq_kv_fork makes it, as far as its length goes, and idle or padded rows need not."""
     torch = _torch()
     c, cfg = _cache_arg(cache)
     D = c.head_dim

@@ -166,7 +166,7 @@ awq_status attend(const char *who, const void *Q, int32_t q_dtype, int64_t num_t
   p.num_seqs = num_seqs;
   p.sinks = o.window > 0 ? o.sinks : 0;
   p.after = plan.prefix ? o.prefix_len : 0;
-  p.prefix_table = o.prefix_table ? o.prefix_table : block_table;
+  p.prefix_table = o.prefix_table;                   // (null: the kernel finds a row that holds it)
   p.prefix_blocks = o.prefix_table ? o.prefix_blocks : max_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
   const XType xt = q_dtype == AWQ_BF16 ? XType::BF16 : XType::F16;

@@ -298,8 +298,8 @@ struct KvAttn {
   // calls with sinks, or a shared prefix
   int num_seqs, sinks;        // the first `sinks` keys are seen beside the window's
   int after;                  // tokens of the prefix, or 0
-  const int32_t *prefix_table;
-  int prefix_blocks;
+  const int32_t *prefix_table;// its pages, or null: those of a row that holds it
+  int prefix_blocks;          // entries of the table, or of a row
   int prefix_parts;           // parts that the prefix takes, before the others
 };
 // Kernel, its tile of rows, waves per workgroup and parts of the keys, and the

@@ -220,6 +220,29 @@ __device__ __forceinline__ Request all_requests(const KvAttn &p) {
   const int64_t cap = (int64_t)p.prefix_blocks << p.pshift;
   return Request{0, (int)p.T, (int)p.T, (int)(p.after < cap ? p.after : cap)};
 }
+// The row whose pages hold the prefix of a call without a table of its own: of the requests
+// with query tokens the first that reaches the prefix' end or, where none does, the longest,
+// since nobody sees further.  (An idle row's entries may be gone and its length stale.)
+__device__ __forceinline__ int prefix_row(const KvAttn &p, int lane) {
+  int longest = -1, row = 0;                         // of the lane's rows
+  for (int b0 = 0; b0 < p.num_seqs; b0 += 64) {
+    const int b = b0 + lane;
+    int kv = -1;
+    if (b < p.num_seqs) {
+      const Request r = request_of(p, b);
+      if (r.ql > 0) kv = r.kv;
+    }
+    const uint64_t reach = __ballot(kv >= p.after);
+    if (reach) return b0 + __builtin_ctzll(reach);
+    if (kv > longest) longest = kv, row = b;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int kv = __shfl_xor(longest, d, 64), b = __shfl_xor(row, d, 64);
+    if (kv > longest || (kv == longest && b < row)) longest = kv, row = b;
+  }
+  return __builtin_amdgcn_readfirstlane(row);
+}
 template <int KEYS>
 __device__ __forceinline__ Request rows_of(const KvAttn &p, int b) {
   if constexpr (KEYS == kShared) return all_requests(p);
@@ -389,7 +412,7 @@ void kv_decode_kernel(KvAttn p) {
   const int row_end = row0 + 15 < rows ? row0 + 15 : rows - 1;
   const int row = row0 + c < rows ? row0 + c : rows - 1;
   const int qi = token_of(p, row);
-  const int32_t *table = KEYS == kShared ? p.prefix_table : p.table + (int64_t)b * p.max_blocks;
+  const int32_t *table = KEYS == kShared && p.prefix_table ? p.prefix_table : p.table + (int64_t)b * p.max_blocks;
   const int table_blocks = KEYS == kShared ? p.prefix_blocks : p.max_blocks;
   int page_base = 0;
   int32_t page_ids = -1;                             // lane i: page page_base + i of the request
@@ -408,6 +431,13 @@ void kv_decode_kernel(KvAttn p) {
   u32x4 q[kWords];
 #pragma unroll
   for (int j = 0; j < kWords; ++j) q[j] = *reinterpret_cast<const u32x4 *>(qp + 8 * j);
+  if (KEYS == kShared && !p.prefix_table) {          // (the first row's pages are under way: it is nearly always the one)
+    const int from = prefix_row(p, lane);
+    if (from > 0) {
+      table += (int64_t)from * p.max_blocks;
+      load_pages(0);
+    }
+  }
   const int my_last = row_last<KEYS>(p, rq, qi), my_first = row_first<KEYS>(p, my_last);
   // keys that all rows see
   int all_last, all_first;
@@ -928,7 +958,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   const char *scales = reinterpret_cast<const char *>(p.scales) + h * P * 4;
   const char *zeros = reinterpret_cast<const char *>(p.zeros) + h * P * 2;
   const int pages = p.pages < 0x7FFFFFFF ? (int)p.pages : 0x7FFFFFFF;
-  const int32_t *table = KEYS == kShared ? p.prefix_table : p.table + (int64_t)b * p.max_blocks;
+  const int32_t *table = KEYS == kShared && p.prefix_table ? p.prefix_table : p.table + (int64_t)b * p.max_blocks;
   int page_id = -1;                                          // of the tile to load next (uniform)
   int page_left = 0;                                         // its tokens of this wave's group
   uint32_t kc[kKw], vc[kVt];
@@ -1037,6 +1067,7 @@ __global__ __launch_bounds__(kPtThreads *NG, D == 64 && NG == 1 ? 3 : 2) void kv
   u32x4 q[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const u32x4 *>(qp + 16 * s);
+  if (KEYS == kShared && !p.prefix_table) table += (int64_t)prefix_row(p, lane) * p.max_blocks;
   if constexpr (BF16) {
     uint32_t m = 0;                                          // the row's largest
 #pragma unroll

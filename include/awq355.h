@@ -595,9 +595,10 @@ typedef struct awq_kv_attention_options {
     int32_t prefix_len;          /* > 0: the first prefix_len tokens are the same in every
                                   * request; window 0 only */
     const int32_t *prefix_table; /* device, int32 [prefix_blocks]: the pages that hold them,
-                                  * prefix_blocks * P at least prefix_len; or NULL: every
-                                  * row's own entries do, as awq_kv_fork makes them, the first
-                                  * row's among them (max_blocks * P at least prefix_len) */
+                                  * prefix_blocks * P at least prefix_len; or NULL: the
+                                  * requests' own entries do, as awq_kv_fork makes them, as far
+                                  * as each one's length goes (max_blocks * P at least
+                                  * prefix_len).  Rows of no query token or seq_lens 0 need none */
     int32_t prefix_blocks;
 } awq_kv_attention_options;
 
@@ -607,9 +608,10 @@ typedef struct awq_kv_attention_options {
  *   opts      host.  With sinks the keys between them and a row's window are not read,
  *             so their pages may have been released.  With a prefix in prefix_table its keys are
  *             read once for the query rows of all requests, and what the block table says of
- *             its full pages does not matter; without that table they are, from the first row's
- *             pages, where it saves time, else by each request as awq_kv_attention does (few
- *             requests, or a short prefix).  seq_lens and max_seq_len count the prefix, and a row
+ *             its full pages does not matter; without that table they are where it saves time, from
+ *             the pages of the first request with query tokens that reaches prefix_len (if none does,
+ *             of the longest), else by each request as awq_kv_attention does (few requests, or a
+ *             short prefix).  seq_lens and max_seq_len count the prefix, and a row
  *             sees of it what it sees by its own length: a request of seq_lens 0, as a
  *             padded batch has, gets O = 0.  num_tokens * num_heads / H at most 2^25 then.  prefix_len is the host's: a captured graph keeps it.  (Logits above 2^21
  *             or so that tie between the prefix and the rest are decided by their roundings.)
