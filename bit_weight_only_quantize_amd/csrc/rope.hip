@@ -5,7 +5,7 @@
 // Of each head's first R channels, pair j < R/2 is (a, b) = channels (j, j + R/2),
 // or (2j, 2j + 1) where neighbours are paired:
 //   a' = a c - b s,   b' = b c + a s,   c, s = factor * cos, sin(position * inv_freq_j).
-// The angle is an fp64 product and so are its cosine and sine, to about 2^-50,
+// The angle is an fp64 product and so are its cosine and sine, to 2^-51 (cos_sin.h),
 // rounded once to fp32: at position 2^20 an fp32 angle would be off by 2^-4.  The
 // products and the sum are fp32, each rounded once and not fused, so what they give
 // does not depend on the kernel, and the codes that a cache gets neither.
@@ -22,10 +22,11 @@
 // TB/s, a copy's rate (16 tokens to a workgroup, a wave on four tokens of one head: 20.0).  Into the
 // cache 8192 tokens, 32 heads of 128 each, 304 MB: 78 us, 3.9 TB/s, its VALU 72% busy; 32 of 430
 // VALU instructions per step fewer in the quantizer gave 1%, and neither twice the workgroups nor
-// loads two heads ahead gave any.  Few tokens by a launch's latency and the chain of fp64 operations, about 30 per angle (32
+// loads two heads ahead gave any.  Few tokens by a launch's latency and the chain of fp64 operations, about 32 per angle (32
 // tokens: 5.8 us).
 
 #include "awq_internal.h"
+#include "cos_sin.h"
 #include "device_common.h"
 #include "kv_place.h"
 #include "quant_group.h"
@@ -36,30 +37,11 @@ constexpr int kRopeThreads = 256, kRopeTokens = 4;
 constexpr int kRopePairs = kRopeTokens * kRopeMaxDim / 2;
 constexpr int kRopeAhead = 4;                          // loads of a lane that are in flight together
 
-// cos and sin of x, each times factor, rounded to fp32.  x = n pi/2 + r, |r| <= pi/4
-// (a little more for |x| past 2^31), then the Taylor series of r: the first terms left out
-// are r^15/15! and r^16/16!, below 2^-45 of the results.
-__device__ __forceinline__ float2 cos_sin(double x, double factor) {
-  const double n = __builtin_rint(x * 0x1.45f306dc9c883p-1);          // 2/pi
-  double r = __builtin_fma(-n, 0x1.921fb54442d18p0, x);                // pi/2 in two parts
-  r = __builtin_fma(-n, 0x1.1a62633145c07p-54, r);
-  const double r2 = r * r;
-  double s = __builtin_fma(r2, 1.0 / 6227020800.0, -1.0 / 39916800.0);
-  s = __builtin_fma(r2, s, 1.0 / 362880.0);
-  s = __builtin_fma(r2, s, -1.0 / 5040.0);
-  s = __builtin_fma(r2, s, 1.0 / 120.0);
-  s = __builtin_fma(r2, s, -1.0 / 6.0);
-  s = __builtin_fma(r * r2, s, r);
-  double c = __builtin_fma(r2, -1.0 / 87178291200.0, 1.0 / 479001600.0);
-  c = __builtin_fma(r2, c, -1.0 / 3628800.0);
-  c = __builtin_fma(r2, c, 1.0 / 40320.0);
-  c = __builtin_fma(r2, c, -1.0 / 720.0);
-  c = __builtin_fma(r2, c, 1.0 / 24.0);
-  c = __builtin_fma(r2, c, -0.5);
-  c = __builtin_fma(r2, c, 1.0);
-  const int quarter = (int)(int64_t)n & 3;
-  const double a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
-  return float2{(float)((quarter == 1 || quarter == 2 ? -a : a) * factor), (float)((quarter & 2 ? -b : b) * factor)};
+// cos and sin of x, each times factor, rounded to fp32.
+__device__ __forceinline__ float2 turn_by(double x, double factor) {
+  double c, s;
+  cos_sin(x, c, s);
+  return float2{(float)(c * factor), (float)(s * factor)};
 }
 
 // What a lane does with its eight channels: out = own * c + partner * s.
@@ -75,7 +57,7 @@ __device__ __forceinline__ void fill_turns(const RopeArgs &p, int64_t t0, int64_
   for (int i = threadIdx.x; i < kRopeTokens * half; i += kRopeThreads) {
     const int t = i / half, j = i - t * half;
     const int64_t at = t0 + t < T ? t0 + t : T - 1;
-    float2 cs = cos_sin((double)p.positions[at] * p.inv_freq[j], p.factor);
+    float2 cs = turn_by((double)p.positions[at] * p.inv_freq[j], p.factor);
     if (p.inverse) cs.y = -cs.y;
     table[i] = cs;
   }

@@ -748,8 +748,8 @@ size_t awq_kv_compact_workspace_size(int64_t num_pages, int32_t page_size);
  * interleaved = 1 (2j, 2j + 1):
  *   a' = a c - b s,  b' = b c + a s,
  *   c, s = attention_factor * cos, sin(position * inv_freq[j]),
- * the angle, its cosine and sine in 64 bits and then rounded to fp32; products and
- * sums are fp32, each rounded once (no fused multiply-add), so results do not
+ * the angle in 64 bits, its cosine and sine to 2^-51 of themselves and then rounded to
+ * fp32; products and sums are fp32, each rounded once (no fused multiply-add), so results do not
  * depend on sizes.  The channels behind the first rotary_dim are kept as they are.
  *
  *   positions  device, int32 [num_tokens], of either sign (distances between
