@@ -1022,19 +1022,19 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     if out is not None:
         _check(out, "out", Q.dtype, (T, heads, D))
     stride = _token_rows(Q, "Q", heads, D)
+    if prefix_table is not None:
+        if prefix_len == 0:
+            raise ValueError("prefix_table needs prefix_len")
+        _tensor(prefix_table, "prefix_table", torch.int32)
+        if prefix_table.dim() != 1 or prefix_table.shape[0] < 1:     # (an empty tensor's address is NULL: no table)
+            raise ValueError("prefix_table must be 1-D and hold a page")
     more = sinks != 0 or prefix_len != 0
     if more:
-        if prefix_table is not None:
-            _tensor(prefix_table, "prefix_table", torch.int32)
-            if prefix_table.dim() != 1:
-                raise ValueError("prefix_table must be 1-D")
         opts = awq_kv_attention_options(int(causal), window, sinks, prefix_len, _address(prefix_table),
                                         0 if prefix_table is None else prefix_table.shape[0])
         need = 0 if workspace is None else lib.awq_kv_attention_ex_workspace_size(
             T, B, heads, c, cfg, max_query_len, max_seq_len, opts)
     else:
-        if prefix_table is not None:
-            raise ValueError("prefix_table needs prefix_len")
         need = 0 if workspace is None else lib.awq_kv_attention_workspace_size(
             T, B, heads, c, cfg, max_query_len, max_seq_len, window)
     ws, ws_bytes = _scratch(workspace, need, seq_lens)

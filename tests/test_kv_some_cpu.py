@@ -86,3 +86,11 @@ def test_binding_refuses_wrong_prefixes():
         binding.awq_kv_attention(**ok)
     with pytest.raises(ValueError, match="GPU"):
         binding.awq_kv_attention(**{**ok, "prefix_len": 0, "window": 3, "sinks": 2})
+
+
+@pytest.mark.parametrize("kw", [dict(prefix_table=i32(0)), dict(prefix_len=0, window=3, sinks=2, prefix_table=i32(4))])
+def test_binding_refuses_tables_that_would_go_unread(kw):
+    """An empty one (its address is NULL, which means none), and one beside sinks alone."""
+    ok = dict(Q=torch.zeros((3, 4, 64), dtype=torch.float16), cache=tensors(), block_table=i32(3, 4), seq_lens=i32(3), prefix_len=20)
+    with pytest.raises(ValueError, match="prefix_table"):
+        binding.awq_kv_attention(**{**ok, **kw})
