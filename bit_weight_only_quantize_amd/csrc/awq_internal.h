@@ -294,7 +294,8 @@ struct KvAttn {
   float *part_o;              // [splits][T * heads * group][D], normalized
   float2 *part_sum;           // [splits][T * heads * group]: weights are relative to 2^x; y, their
                               // sum, is 0 where a part holds no key of the row
-  float *part_lo;             // likewise, where |x| >= 2^24 only: a part of the reference below x
+  float *part_lo;             // likewise, where |x| >= 2^22 only (may_have_low_part): a part of the
+                              // reference below x
   // calls with sinks, or a shared prefix
   int num_seqs, sinks;        // the first `sinks` keys are seen beside the window's
   int after;                  // tokens of the prefix, or 0
