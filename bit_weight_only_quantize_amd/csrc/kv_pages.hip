@@ -176,7 +176,7 @@ constexpr int kAlone = 1024;                           // threads of a single wo
 constexpr int kAloneRounds = 32;
 constexpr int64_t kAloneItems = (int64_t)kAloneRounds * kAlone;
 constexpr int64_t kAloneEntries = 65536;               // table entries that one workgroup looks through,
-constexpr int64_t kAloneReleases = 4096;               // ... and releases
+constexpr int64_t kAloneReleases = 2048;               // ... and releases
 
 template <int THREADS>
 struct Ranks {
@@ -276,7 +276,9 @@ __device__ __forceinline__ Sums sum_counts(const int32_t *counts, int64_t n, int
 // number.  A workgroup per 256 entries of a row, and a second launch whose one workgroup
 // ranks the list, or for long ones two, in chunks: counts, then places.  A small table and a short
 // list take one launch of one workgroup: whoever brings a count below zero marks the page in
-// LDS, so counts are not read again (24 rows of 26 entries, 600 pages: 6.4 us, 7.4 in two).
+// LDS, so counts are not read again.  One launch against two, in a graph: 256 entries of 1024 pages, all
+// released, 5.9 us and 6.9; 1024 entries 6.5 and 6.8; 1536 entries 7.8 and 7.4; 4096 entries 13.8 and 9.2.  With
+// two rows of many released, as a step has it: 2048 entries 6.9 and 7.4, 4096 entries 9.3 and 9.1.  So up to 2048.
 // Blocks of row b that are released: those whose tokens below its length all lie in [lo, hi).
 struct Blocks {
   int64_t first, stop;

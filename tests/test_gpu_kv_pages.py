@@ -299,3 +299,20 @@ def test_pages_past_32_bit_byte_offsets():
     assert n.item() == 3 and table.tolist() == [[0, 1], [0, 2]] and free[0].item() == 3
     assert same(0, kept[0]) and same(1, kept[1]) and same(2, kept[1])
     assert shared[0].item() == 1 and shared.sum().item() == 1
+
+
+@pytest.mark.parametrize("blocks", [32, 33, 64, 65])
+def test_release_of_small_and_large_tables(blocks):
+    """64 rows of so many entries: up to 2048 one launch serves, beyond that two."""
+    import bit_weight_only_quantize_amd as awq
+    rng = np.random.default_rng(blocks)
+    lens = rng.integers(1, blocks * 16 + 1, 64)
+    lens[0] = blocks * 16
+    table, shared, free = _pool(rng, lens, 16, 50, None, 0.3)
+    assert table.shape[1] >= blocks
+    table = np.ascontiguousarray(table[:, :blocks])
+    start = np.where(rng.random(64) < 0.5, 0, rng.integers(0, blocks * 16, 64))
+    tab, sh = _i32(table), _i32(shared)
+    got, count = awq.awq_kv_release(tab, _i32(lens), sh, _i32(free), 16, start=_i32(start), pages_used=_i32([3]))
+    want = pg.release(table, lens, shared, free, 16, start, None, 3)
+    _eq(tab, table), _eq(sh, shared), _eq(count, [len(want)]), _eq(got, pg.padded(want, len(shared)))
