@@ -1547,7 +1547,9 @@ hipError_t attn_go(const KvAttn &p, int B, const KvAttnPlan &pl, hipStream_t st)
   if constexpr (KEYS != kShared) {
     const int parts = p.splits + (KEYS == kSome ? p.prefix_parts : 0);
     if (e != hipSuccess || parts == 1) return e;
-    // (enough rows fill the card with a wave each: 48 tokens of 64 heads, 23 parts, take 8.4 us so, 12.4 with four)
+    // (enough rows fill the card with a wave each: 48 tokens of 64 heads, 23 parts, take 8.4 us so, 12.4 with four.
+    // A whole call behind 16000 keys, 64 heads over 8, in a graph: 1024 rows 41.0 us so and 39.5 with four, 1536 rows
+    // 42.3 and 42.5, 2048 rows 44.9 and 46.5, 4096 rows 64.5 and 67.0)
     const bool many = KEYS == kSome && rows * p.heads * B >= kJoinRows;
     if (parts > kJoinWide && !many)
       kv_join_kernel<D, BF16, 4, KEYS><<<dim3((unsigned)rows, (unsigned)p.heads, (unsigned)B), 256, 0, st>>>(p);
