@@ -993,8 +993,9 @@ def awq_kv_attention(Q, cache, block_table, seq_lens, query_start=None, max_quer
     the first prefix_len tokens of every request are the same.  They are read once for all
     of them from prefix_table's pages (int32, at least ceil(prefix_len / page_size)), or
     without one, where that saves time, from those of the first request with query tokens
-    that reaches prefix_len (of the longest, if none does); each request then holds them, as
-    awq_kv_fork makes it, as far as its length goes, and idle or padded rows need not."""
+    that has the prefix up to its last page (or most of it, if none does); each request then
+    holds them, as awq_kv_fork makes it, as far as its length goes, and idle or padded rows
+    need not."""
     torch = _torch()
     c, cfg = _cache_arg(cache)
     D = c.head_dim

@@ -221,25 +221,30 @@ __device__ __forceinline__ Request all_requests(const KvAttn &p) {
   return Request{0, (int)p.T, (int)p.T, (int)(p.after < cap ? p.after : cap)};
 }
 // The row whose pages hold the prefix of a call without a table of its own: of the requests
-// with query tokens the first that reaches the prefix' end or, where none does, the longest,
-// since nobody sees further.  (An idle row's entries may be gone and its length stale.)
+// with query tokens the first that has it to its end or, where none does, the one that has
+// most of it.  (An idle row's entries may be gone and its length stale; a branch that found no
+// free page lacks the one that it ends in.)
 __device__ __forceinline__ int prefix_row(const KvAttn &p, int lane) {
-  int longest = -1, row = 0;                         // of the lane's rows
+  int most = -1, row = 0;                            // of the lane's rows
   for (int b0 = 0; b0 < p.num_seqs; b0 += 64) {
     const int b = b0 + lane;
-    int kv = -1;
+    int has = -1;
     if (b < p.num_seqs) {
       const Request r = request_of(p, b);
-      if (r.ql > 0) kv = r.kv;
+      const int n = r.kv < p.after ? r.kv : p.after;
+      if (r.ql > 0 && n > 0) {
+        const int32_t id = p.table[(int64_t)b * p.max_blocks + ((n - 1) >> p.pshift)];
+        has = id >= 0 && id < p.pages ? n : (n - 1) & -(1 << p.pshift);
+      }
     }
-    const uint64_t reach = __ballot(kv >= p.after);
-    if (reach) return b0 + __builtin_ctzll(reach);
-    if (kv > longest) longest = kv, row = b;
+    const uint64_t whole = __ballot(has == p.after);
+    if (whole) return b0 + __builtin_ctzll(whole);
+    if (has > most) most = has, row = b;
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int kv = __shfl_xor(longest, d, 64), b = __shfl_xor(row, d, 64);
-    if (kv > longest || (kv == longest && b < row)) longest = kv, row = b;
+    const int has = __shfl_xor(most, d, 64), b = __shfl_xor(row, d, 64);
+    if (has > most || (has == most && b < row)) most = has, row = b;
   }
   return __builtin_amdgcn_readfirstlane(row);
 }

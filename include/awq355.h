@@ -609,9 +609,9 @@ typedef struct awq_kv_attention_options {
  *             so their pages may have been released.  With a prefix in prefix_table its keys are
  *             read once for the query rows of all requests, and what the block table says of
  *             its full pages does not matter; without that table they are where it saves time, from
- *             the pages of the first request with query tokens that reaches prefix_len (if none does,
- *             of the longest), else by each request as awq_kv_attention does (few requests, or a
- *             short prefix).  seq_lens and max_seq_len count the prefix, and a row
+ *             the pages of the first request with query tokens that has the prefix up to its last
+ *             page (if none does, of the one that has most of it), else by each request as
+ *             awq_kv_attention does (few requests, or a short prefix).  seq_lens and max_seq_len count the prefix, and a row
  *             sees of it what it sees by its own length: a request of seq_lens 0, as a
  *             padded batch has, gets O = 0.  num_tokens * num_heads / H at most 2^25 then.  prefix_len is the host's: a captured graph keeps it.  (Logits above 2^21
  *             or so that tie between the prefix and the rest are decided by their roundings.)

@@ -159,3 +159,27 @@ def test_requests_that_end_between_replays():
         want = call(prefix_table=_i32(a.whole[0]))
         assert all(torch.equal(x, y) for x, y in zip(out, want))
         assert all(torch.equal(x, y) for x, y in zip(call(), want))
+
+
+@pytest.mark.parametrize("n,q,once", BATCHES)
+def test_a_first_branch_that_found_no_page(n, q, once):
+    """The page that the prefix ends in is -1 in its row, as awq_kv_fork leaves it when none is free: it
+    misses those keys, and nobody else does."""
+    torch = torch_mod()
+    a = Batch(n, q)
+    a.table[0, a.prefix // a.page] = -1
+    assert a.reads_once() == once
+    want = a.call(a.whole, prefix_table=_i32(a.whole[0]), prefix_len=a.prefix) if once else a.call(a.whole)
+    got = a.call(a.table, prefix_len=a.prefix)
+    assert all(torch.equal(w[q:], g[q:]) for w, g in zip(want, got))
+
+
+def test_no_branch_found_a_page():
+    """The longest that anybody sees is then what comes before it."""
+    a = Batch(40, 1)
+    a.lens[:] = a.prefix - np.arange(40)
+    a.table[:, a.prefix // a.page] = -1
+    torch = torch_mod()
+    want = a.call(a.table, prefix_table=_i32(a.table[7]), prefix_len=a.prefix)
+    assert a.reads_once()
+    assert all(torch.equal(w, g) for w, g in zip(want, a.call(a.table, prefix_len=a.prefix)))
